@@ -79,7 +79,8 @@ typedef enum specv_status {
 
 typedef enum specv_dtype {
   SPECV_F32 = 0,   /* IEEE float32 logits                          */
-  SPECV_BF16 = 1   /* bfloat16 logits (raw 16-bit storage)          */
+  SPECV_BF16 = 1,  /* bfloat16 logits (raw 16-bit storage)          */
+  SPECV_F16 = 2    /* IEEE half: the cache operators only           */
 } specv_dtype;
 
 /* Bits of the device status word. */
@@ -94,10 +95,16 @@ typedef enum specv_dtype {
 #define SPECV_DEV_TIMEOUT         0x40  /* a bounded wait on a copy gave up        */
 #define SPECV_DEV_BAD_TREE        0x80  /* a token tree whose parent of node i is not
                                            below i, or a node token outside [0,V) */
+#define SPECV_DEV_BAD_CACHE       0x100 /* a cache length or page number out of range */
+#define SPECV_DEV_BAD_PENALTY     0x200 /* a penalty that is not finite, or a
+                                           repetition penalty not above 0         */
 
 /* Limits. */
 #define SPECV_MAX_DRAFT 16      /* K <= 16                               */
 #define SPECV_MAX_BATCH 65535   /* B <= 65535                            */
+#define SPECV_MAX_NODES 64      /* nodes of a tree, rows of a request     */
+#define SPECV_MAX_HEAD_DIM 128  /* cache operators: a multiple of 8 in 8..128 */
+#define SPECV_MAX_BIAS 1024     /* biased tokens of a request             */
 
 /* Library version (major*10000 + minor*100 + patch). */
 int specv_version(void);
@@ -340,6 +347,160 @@ specv_status spec_insert_accepted(const int32_t* accepted_len, const int32_t* ou
                                   int K, int32_t* seq_lens, int32_t* history, int L,
                                   int32_t* next_tokens, int32_t* cu_emitted, int32_t* packed,
                                   int32_t* status, specv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The target's pass over a drafted tree ("Decodificación Especulativa y
+ * EAGLE", section "Verificación de Atención en Árvore": each token attends
+ * to its ancestors; "Accelerating Sonar through speculation", section
+ * "EAGLE"), around a paged key/value cache:
+ *
+ *   spec_append_nodes    norms, rotates and writes the nodes' keys and values
+ *   spec_tree_attention  attends from the nodes to the cache and their paths
+ *   spec_process_logits  penalties, biases and grammar masks for every node
+ *   (the verification)   spec_verify_tree_greedy, spec_verify_sample, ...
+ *   spec_keep_path       keeps the accepted path's cache rows
+ *
+ * Nodes.  A request has n_nodes[b] of N nodes; node 0 is the root (the last
+ * verified token), parents[b,0] = -1 and 0 <= parents[b,i] < i.  parents =
+ * NULL is a chain (node i's parent is node i-1): the K+1 positions of
+ * spec_verify_sample, or with N = 1 plain decoding.  n_nodes = NULL: all N.
+ * Node i lives in cache slot lens[b] + i and has position lens[b] + depth(i).
+ *
+ * Errors in the data.  These calls write status[b] (int32, device): 0, or
+ * SPECV_DEV_* bits.  A flagged request's cache rows stay as they were, its
+ * output rows (the n_nodes[b] of them, all N where n_nodes[b] itself is bad)
+ * become 0 (spec_process_logits: -inf).  Rows at and behind n_nodes[b] are
+ * left as they were.
+ * ---------------------------------------------------------------------- */
+
+/* A paged key/value cache.  Request b's slot s is row s % page_size of page
+ * page_table[b, s / page_size].  Element (layer, page, row, head, d) of k is
+ * at k + layer*layer_stride + page*page_stride + row*row_stride +
+ * head*head_stride + d; v has the same strides.  Strides count elements, are
+ * multiples of 8 and may pass 32 bits; k and v are 16-byte aligned. */
+typedef struct specv_cache {
+  void* k;
+  void* v;
+  const int32_t* page_table; /* [B, max_pages], rows table_stride apart */
+  const int32_t* lens;       /* [B]: verified tokens, 0 <= lens[b], and
+                                lens[b] + n_nodes[b] <= max_pages*page_size */
+  int64_t layer_stride, page_stride, row_stride, head_stride;
+  int32_t layers; /* 1 but for spec_keep_path */
+  int32_t pages;  /* pages in k and v: 0 <= page_table[b, .] < pages where used */
+  int32_t page_size, max_pages, table_stride;
+  int32_t heads;    /* key heads */
+  int32_t head_dim; /* a multiple of 8, at most SPECV_MAX_HEAD_DIM */
+  specv_dtype dtype; /* SPECV_BF16 or SPECV_F16 */
+} specv_cache;
+
+/* Rows [B, N, heads, head_dim] of the cache's dtype: element (b, i, h, d) is
+ * at data + b*batch_stride + i*node_stride + h*head_stride + d.  data is
+ * 16-byte aligned, strides are multiples of 8 elements. */
+typedef struct specv_rows {
+  void* data;
+  int64_t batch_stride, node_stride, head_stride;
+} specv_rows;
+
+/*
+ * Norms, rotation and append of the nodes' projections, one kernel:
+ *   x <- x / sqrt(mean(x^2) + eps) * weight      (queries and keys, per head;
+ *                                                 a NULL weight: no norm)
+ *   (x_a, x_c) <- (x_a cos t - x_c sin t, x_c cos t + x_a sin t) * rope_scale,
+ *       t = (lens[b] + depth(i)) * inv_freq[j], for j < rot_dim / 2 and
+ *       (a, c) = (2j, 2j + 1) if interleaved, else (j, j + rot_dim / 2);
+ *       elements d >= rot_dim keep their value.
+ * Queries go to q_out, keys and values (these as they are) to the cache's
+ * slots lens[b] + i.  In 32 bits, the angles in 64; rounded once, to nearest.
+ *   q, k, v   [B, N, q_heads | heads | heads, head_dim] (specv_rows, of one
+ *             projection or of three); q_out may be q itself, but no two of
+ *             the buffers may overlap otherwise.
+ *   q_weight, k_weight  [head_dim] of the cache's dtype, or NULL.
+ *   inv_freq  [rot_dim / 2] float32 (a long-context scaling is in it), or
+ *             NULL with rot_dim = 0: no rotation.  rot_dim even, <= head_dim.
+ * Two requests that share a page must not both write the same slot.
+ */
+specv_status spec_append_nodes(const specv_cache* cache, const specv_rows* q, const specv_rows* k,
+                               const specv_rows* v, const int32_t* parents,
+                               const int32_t* n_nodes, int B, int N, int q_heads,
+                               const void* q_weight, const void* k_weight, float eps,
+                               const float* inv_freq, int rot_dim, int interleaved,
+                               float rope_scale, const specv_rows* q_out, int32_t* status,
+                               specv_stream_t stream);
+
+/* Bytes of workspace spec_tree_attention needs (0 for sizes out of range). */
+size_t specv_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * Attention of the nodes over the cache:
+ *   out[b,i,h] = sum_s softmax_s(scale q[b,i,h] . k[s, h / (q_heads/heads)]) v[s, ...]
+ * over the slots s < lens[b] and s = lens[b] + a for a = i and its ancestors
+ * (their rows in the cache already: spec_append_nodes).  No other slot counts,
+ * whatever it holds.  Scores, maxima and sums in 32 bits; the weights are
+ * rounded to the cache's dtype before the product with the values.
+ *   q, out    [B, N, q_heads, head_dim]; q_heads a multiple of cache->heads.
+ *   scale     > 0 and finite (1/sqrt(head_dim) as a rule).
+ *   workspace specv_attention_workspace_bytes bytes, 256-byte aligned.  It
+ *             needs no initialisation and keeps nothing between calls; calls
+ *             that may run at the same time need one each.
+ */
+specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
+                                 const int32_t* parents, const int32_t* n_nodes, int B, int N,
+                                 int q_heads, float scale, const specv_rows* out, int32_t* status,
+                                 void* workspace, size_t workspace_bytes, specv_stream_t stream);
+
+/*
+ * Keeps the accepted path (spec_verify_tree_greedy's outputs) in the cache:
+ * for j = 1 .. accepted_len[b], in every layer, keys and values,
+ *   slot lens[b] + j <- slot lens[b] + path_nodes[b, j];
+ *   new_lens[b] = lens[b] + accepted_len[b] + 1  (lens[b] for a flagged request).
+ *   path_nodes   [B, N] int32: 0, then strictly increasing node numbers < N
+ *                (else SPECV_DEV_BAD_TREE); entries behind accepted_len[b]
+ *                are not read.
+ *   accepted_len [B] int32 in 0..N-1 (else SPECV_DEV_BAD_DRAFT_LEN).
+ *   new_lens     [B] int32 output, not cache->lens itself.
+ * One kernel; no workspace.
+ */
+specv_status spec_keep_path(const specv_cache* cache, const int32_t* path_nodes,
+                            const int32_t* accepted_len, int B, int N, int32_t* new_lens,
+                            int32_t* status, specv_stream_t stream);
+
+/*
+ * Penalties, biases and grammar masks, before the verification or a sampler.
+ * Row (b, i) of the logits is what the target says after node i; its text is
+ * history[b, 0 .. seq_lens[b]) (as spec_insert_accepted keeps it; the root is
+ * its last token) and then the tokens on the path from the root to node i.
+ * With c = how often a token occurs in the text at or behind prompt_lens[b]:
+ *   z <- z > 0 ? z / repetition[b] : z * repetition[b]  if the text has the token;
+ *   z <- z - frequency[b] * c - presence[b] * (c > 0);
+ *   z <- z + the token's bias (a token listed more than once: their sum, in
+ *        the listed order);
+ *   z <- -inf  if the token's bit of the mask is 0
+ * in 32 bits, rounded once.  A row whose mask allows nothing becomes -inf.
+ *   logits, out [B, R, V] of `dtype` (SPECV_F32 or SPECV_BF16), element (b, i, t)
+ *             at b*batch_stride + i*row_stride + t; out may be logits itself
+ *             (with its strides), else they do not overlap.
+ *   tokens    parents != NULL: [B, R], node i's token (tokens[b,0] unused);
+ *             parents == NULL (a chain): [B, R-1], the drafted tokens of
+ *             spec_verify_sample.  NULL only where R = 1.
+ *   n_rows    [B] in 1..R (a chain: draft_len + 1; a tree: n_nodes), or NULL.
+ *   history   [B, L], rows history_stride apart; 0 <= prompt_lens[b] <=
+ *             seq_lens[b] <= L (else SPECV_DEV_BAD_CACHE); prompt_lens NULL: 0.
+ *   repetition, frequency, presence  [B] float32, or NULL: 1, 0, 0.
+ *   bias_tokens, bias_values [B, num_bias] int32, float32, or NULL; a token
+ *             below 0 is an empty place, one at or above V is flagged.
+ *   allowed   [B, R, ceil(V/32)] int32, bit t % 32 of word t / 32, or NULL.
+ * One kernel; no workspace.
+ */
+specv_status spec_process_logits(const void* logits, int64_t batch_stride, int64_t row_stride,
+                                 specv_dtype dtype, int B, int R, int V, const int32_t* tokens,
+                                 const int32_t* parents, const int32_t* n_rows,
+                                 const int32_t* history, int64_t history_stride, int L,
+                                 const int32_t* seq_lens, const int32_t* prompt_lens,
+                                 const float* repetition, const float* frequency,
+                                 const float* presence, const int32_t* bias_tokens,
+                                 const float* bias_values, int num_bias, const int32_t* allowed,
+                                 void* out, int64_t out_batch_stride, int64_t out_row_stride,
+                                 int32_t* status, specv_stream_t stream);
 
 /*
  * The sampler without any allocation, for callers that cannot allocate

@@ -10,9 +10,9 @@ status codes into exceptions.  Nothing here computes any step of the rule.
 
 from __future__ import annotations
 
-from ._native import (DEV_BAD_DRAFT_LEN, DEV_BAD_ROW, DEV_BAD_TEMPERATURE, DEV_BAD_TOKEN,
-                      DEV_BAD_TREE, DEV_BAD_UNIFORM, DEV_NO_DRAFT, DEV_TIMEOUT, SPECV_BF16,
-                      SPECV_F32, SpecVerifyError, check, lib)
+from ._native import (DEV_BAD_CACHE, DEV_BAD_DRAFT_LEN, DEV_BAD_PENALTY, DEV_BAD_ROW,
+                      DEV_BAD_TEMPERATURE, DEV_BAD_TOKEN, DEV_BAD_TREE, DEV_BAD_UNIFORM,
+                      DEV_NO_DRAFT, DEV_TIMEOUT, SPECV_BF16, SPECV_F32, SpecVerifyError, check, lib)
 from .build import build
 
 __all__ = [
@@ -21,8 +21,21 @@ __all__ = [
     "spec_verify_sample_onehot", "verify_tree_greedy", "insert_accepted", "launch_plan",
     "workspace_bytes", "max_vocab", "SpecVerifyError", "DEV_BAD_TREE",
     "DEV_BAD_DRAFT_LEN", "DEV_BAD_TOKEN", "DEV_BAD_TEMPERATURE", "DEV_BAD_UNIFORM",
-    "DEV_BAD_ROW", "DEV_NO_DRAFT", "DEV_TIMEOUT",
+    "DEV_BAD_ROW", "DEV_NO_DRAFT", "DEV_TIMEOUT", "DEV_BAD_CACHE", "DEV_BAD_PENALTY",
+    "AttentionWorkspace", "append_nodes", "tree_attention", "process_logits", "keep_path",
 ]
+
+
+_TREE = ("AttentionWorkspace", "append_nodes", "tree_attention", "process_logits", "keep_path")
+
+
+def __getattr__(name):
+    # the binding of a drafted tree's operators needs torch, this module does not
+    if name in _TREE:
+        from . import tree
+        globals().update({n: getattr(tree, n) for n in _TREE})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _torch():

@@ -9,8 +9,9 @@ import subprocess
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 INCLUDE = os.path.join(ROOT, "include")
-SOURCES = [os.path.join(PKG_DIR, "csrc", "specverify.cu")]
-HEADERS = [os.path.join(INCLUDE, "specverify.h")]
+SOURCES = [os.path.join(PKG_DIR, "csrc", name)
+           for name in ("specverify.cu", "cache.cu", "attention.cu", "logits.cu")]
+HEADERS = [os.path.join(INCLUDE, "specverify.h"), os.path.join(PKG_DIR, "csrc", "cache.cuh")]
 LIB_PATH = os.path.join(PKG_DIR, "libspecverify.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,7 +39,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     cuda_lib = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "lib64")
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-I", INCLUDE,
-           "-shared", "-Xcompiler", "-fPIC", "-cudart", "shared",
+           "-shared", "-Xcompiler", "-fPIC", "-cudart", "shared", "--threads", str(len(SOURCES)),
            "-Xlinker", f"-rpath,{cuda_lib}", *extra_flags, "-o", tmp, *SOURCES]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
