@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const Cache C, const
     }
     last = __reduce_max_sync(kFullMask, last);
     if (__any_sync(kFullMask, bad_path)) bad |= SPECV_DEV_BAD_TREE;
-    if (len < 0 || len > INT_MAX - 2 * kMaxNodes ||
+    if (len < 0 || len > INT_MAX - 4 * kMaxNodes ||
         (!bad && static_cast<int64_t>(len) + last >= static_cast<int64_t>(C.max_pages) * C.page_size))
       bad |= SPECV_DEV_BAD_CACHE;
     bool bad_page = false;

@@ -93,7 +93,7 @@ __device__ __forceinline__ Tree read_tree(const int32_t* parents, const int32_t*
     t.bad |= SPECV_DEV_BAD_DRAFT_LEN;
     t.n = 0;
   }
-  if (t.len < 0 || t.len > INT_MAX - 2 * kMaxNodes ||
+  if (t.len < 0 || t.len > INT_MAX - 4 * kMaxNodes ||
       static_cast<int64_t>(t.len) + t.n > slots)
     t.bad |= SPECV_DEV_BAD_CACHE;
   bool bad_tree = false;
