@@ -32,8 +32,7 @@ struct Params {
   const int32_t* allowed;
   int32_t* status;
   int R, V, L, num_bias;
-  int rows;     // of a block
-  int shifted;  // rows do not all begin at a 16-byte boundary
+  int rows;  // of a block
 };
 
 template <int DT> struct Elt;
@@ -50,157 +49,239 @@ template <> struct Elt<SPECV_BF16> {
   static __device__ uint16_t store(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 };
 
+constexpr int kThreads = 256;
+constexpr int kTextThreads = 128;  // of them, the ones that count the text first
+constexpr int kSegment = 1024;     // entries of a row that a warp takes at a time
+
 // What a block needs of one request's text, for its chunk of the vocabulary.
 template <int kChunk> struct Text {
   uint32_t count[kChunk];
-  uint32_t touched[kChunk / 32];
-  uint16_t list[kChunk];  // touched entries, each warp's from its first element on
   uint64_t path[kMaxNodes];
-  float bias[SPECV_MAX_BIAS];      // sums of the biases in this chunk ...
-  uint16_t biased[SPECV_MAX_BIAS]; // ... and their entries
+  float bias[SPECV_MAX_BIAS];       // sums of the biases in this chunk ...
+  uint16_t biased[SPECV_MAX_BIAS];  // ... and their entries
+  uint16_t list[kChunk];            // touched entries
   int drafted[kMaxNodes];  // entry of node i's token, -1 where it is another chunk's
-  int num_biased, n, bad;
+  int num_biased, touched, ticket, bad;
 };
 
+// How a row's elements lie against 16 bytes: every row begins there, rows
+// begin anywhere but input and output alike, or not alike.
+enum Layout { kAligned, kShifted, kSingle };
+
+// -inf where keep's bit is 0.
+template <int DT> __device__ __forceinline__ void mask_vec(uint4& v, uint32_t keep) {
+  uint32_t* w = &v.x;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if (DT == SPECV_F32) {
+      if (!(keep >> i & 1)) w[i] = 0xff800000u;
+    } else {
+      const uint32_t m = (keep >> 2 * i & 1) * 0xffffu | (keep >> (2 * i + 1) & 1) * 0xffff0000u;
+      w[i] = (w[i] & m) | (0xff80ff80u & ~m);
+    }
+  }
+}
+
 // A block takes kChunk vocabulary entries of one request, for P.rows of its
-// rows.  It counts the text's tokens among them once, in shared memory, then
-// streams the rows through: nearly every element is only masked and copied, 16
-// bytes at a time (kVec elements; 1 where input and output are not aligned
-// alike), and the few that the text, a draft or a bias touches are computed
-// one to a lane and stored over the copy.  A warp owns the same columns in
-// every row, so it alone orders the two stores; only where the rows' vectors
-// are shifted against the chunk the block has to.
-template <int DT, int kChunk, int kThreads, int kVec>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const Params P) {
+// rows.  Nearly every element is only masked and copied, whatever the text
+// says: the warps take segments of rows off a counter and stream them, while
+// the first four count the text's tokens in this chunk in shared memory and
+// list the entries they touch; those join the streaming when they are done.
+// Then the listed entries are computed from the input, one to a thread, and
+// stored over the copies.
+template <int DT, int kChunk, Layout kLayout>
+__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
   using E = Elt<DT>;
   using T = typename E::T;
-  constexpr int kMine = kChunk / kVec / kThreads;         // vectors of a row a thread has
-  constexpr int kBlock = kMine < 8 ? kMine : 8;           // ... in flight
-  constexpr int kWords = kChunk / 32 / (kThreads / 32);   // bitmap words of a warp
-  static_assert(kChunk % (kVec * kThreads) == 0 && kWords <= 32 && kWords % kMine == 0 || kVec == 1, "");
-  struct __align__(kVec * sizeof(T)) Vec {
-    T x[kVec];
-  };
+  constexpr int kVec = kLayout == kSingle ? 1 : 16 / sizeof(T);
+  constexpr int kMine = kSegment / 32 / kVec;        // vectors of a segment a lane has
+  constexpr int kFlight = kMine < 4 ? kMine : 4;     // ... in flight
   extern __shared__ __align__(16) char smem[];
   Text<kChunk>& s = *reinterpret_cast<Text<kChunk>*>(smem);
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, b = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
   const int c0 = blockIdx.x * kChunk, c1 = min(P.V, c0 + kChunk);
-  for (int e = tid; e < kChunk; e += kThreads) s.count[e] = 0;
-  for (int e = tid; e < kChunk / 32; e += kThreads) s.touched[e] = 0;
-
-  const int total = P.seq_lens[b], prompt = P.prompt_lens ? P.prompt_lens[b] : 0;
+  const int given = P.n_rows ? P.n_rows[b] : P.R;
+  const int n = given < 1 || given > P.R ? P.R : given;
+  const int first_row = blockIdx.z * P.rows, last_row = min(n, first_row + P.rows);
+  if (first_row >= last_row) return;
   const float rho = P.repetition ? P.repetition[b] : 1.0f;
   const float freq = P.frequency ? P.frequency[b] : 0.0f;
   const float pres = P.presence ? P.presence[b] : 0.0f;
-  if (tid < 32) {
-    Tree t = read_tree(P.parents, P.n_rows, P.seq_lens, b, P.R, INT64_MAX, lane);
-    bool bad_token = false;
-    if (!(t.bad & SPECV_DEV_BAD_TREE)) {
-#pragma unroll
-      for (int k = 0; k < 2; k++) {
-        const int i = lane + 32 * k;
-        int at = -1;
-        if (i >= 1 && i < t.n) {
-          const int token = P.parents ? P.tokens[static_cast<int64_t>(b) * P.R + i]
-                                      : P.tokens[static_cast<int64_t>(b) * (P.R - 1) + i - 1];
-          bad_token |= token < 0 || token >= P.V;
-          if (token >= c0 && token < c1) at = token - c0;
-        }
-        s.drafted[i] = at;
-      }
-      uint64_t bits[2];
-      ancestors(t, lane, bits);
-      s.path[lane] = bits[0];
-      s.path[lane + 32] = bits[1];
-    }
-    if (__any_sync(kFullMask, bad_token)) t.bad |= SPECV_DEV_BAD_TOKEN;
-    if (total > P.L || prompt < 0 || prompt > total) t.bad |= SPECV_DEV_BAD_CACHE;
-    if (!(rho > 0.0f) || !isfinite(rho) || !isfinite(freq) || !isfinite(pres))
-      t.bad |= SPECV_DEV_BAD_PENALTY;
-    if (lane == 0) {
-      s.n = t.n;
-      s.bad = static_cast<int>(t.bad);
-      s.num_biased = 0;
-    }
+  if (tid == 0) {
+    s.num_biased = 0;
+    s.touched = 0;
+    s.ticket = 0;
+    s.bad = 0;
   }
   __syncthreads();
 
-  // The text's tokens in this chunk.  Counts are whole numbers: the order in
-  // which the threads add does not show.
-  bool bad_token = false;
-  auto touch = [&](int e) { atomicOr(&s.touched[e / 32], 1u << (e & 31)); };
-  if (!s.bad) {
-    auto count = [&](int i, int token) {
-      bad_token |= static_cast<unsigned>(token) >= static_cast<unsigned>(P.V);
-      const int e = token - c0;
-      if (e < 0 || token >= c1) return;
-      if (i < prompt) atomicOr(&s.count[e], kInPrompt);
-      else atomicAdd(&s.count[e], 1u);
-      touch(e);
-    };
-    const int32_t* hist = P.history + b * P.history_stride;
-    const int vectors = reinterpret_cast<uintptr_t>(hist) % 16 == 0 ? total / 4 : 0;
-    for (int i = tid; i < vectors; i += kThreads) {
-      const int4 t = reinterpret_cast<const int4*>(hist)[i];
-      count(4 * i, t.x);
-      count(4 * i + 1, t.y);
-      count(4 * i + 2, t.z);
-      count(4 * i + 3, t.w);
-    }
-    for (int i = 4 * vectors + tid; i < total; i += kThreads) count(i, hist[i]);
-    if (tid < s.n && s.drafted[tid] >= 0) {
-      atomicOr(&s.count[s.drafted[tid]], kDrafted);
-      touch(s.drafted[tid]);
-    }
-    const int32_t* names = P.bias_tokens + static_cast<int64_t>(b) * P.num_bias;
-    const float* values = P.bias_values + static_cast<int64_t>(b) * P.num_bias;
-    for (int i = tid; i < P.num_bias; i += kThreads) {
-      const int token = names[i];
-      bad_token |= token >= P.V;
-      if (token < c0 || token >= c1) continue;
-      // the first place that names a token adds up all of them, in their order
-      float sum = 0.0f;
-      bool first = true;
-      for (int j = 0; j < P.num_bias; j++)
-        if (names[j] == token) {
-          if (j < i) first = false;
-          sum = sum + values[j];
+  if (tid < kTextThreads) {
+    const int total = P.seq_lens[b], prompt = P.prompt_lens ? P.prompt_lens[b] : 0;
+    for (int e = tid; e < kChunk / 4; e += kTextThreads)
+      reinterpret_cast<uint4*>(s.count)[e] = make_uint4(0, 0, 0, 0);
+    bool bad_token = false;
+    if (tid < 32) {
+      Tree t = read_tree(P.parents, P.n_rows, P.seq_lens, b, P.R, INT64_MAX, lane);
+      if (!(t.bad & SPECV_DEV_BAD_TREE)) {
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+          const int i = lane + 32 * k;
+          int at = -1;
+          if (i >= 1 && i < t.n) {
+            const int token = P.parents ? P.tokens[static_cast<int64_t>(b) * P.R + i]
+                                        : P.tokens[static_cast<int64_t>(b) * (P.R - 1) + i - 1];
+            bad_token |= token < 0 || token >= P.V;
+            if (token >= c0 && token < c1) at = token - c0;
+          }
+          s.drafted[i] = at;
         }
-      if (first) {
-        const int at = atomicAdd(&s.num_biased, 1);
-        s.biased[at] = static_cast<uint16_t>(token - c0);
-        s.bias[at] = sum;
-        atomicOr(&s.count[token - c0], kBiased);
-        touch(token - c0);
+        uint64_t bits[2];
+        ancestors(t, lane, bits);
+        s.path[lane] = bits[0];
+        s.path[lane + 32] = bits[1];
+      }
+      if (total > P.L || prompt < 0 || prompt > total) t.bad |= SPECV_DEV_BAD_CACHE;
+      if (!(rho > 0.0f) || !isfinite(rho) || !isfinite(freq) || !isfinite(pres))
+        t.bad |= SPECV_DEV_BAD_PENALTY;
+      if (lane == 0) s.bad = static_cast<int>(t.bad);
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kTextThreads) : "memory");
+    if (!s.bad) {
+      // Counts are whole numbers: the order in which the threads add does not
+      // show.  Whoever finds an untouched word lists its entry.
+      auto touch = [&](int e, uint32_t old) {
+        if (old == 0) s.list[atomicAdd(&s.touched, 1)] = static_cast<uint16_t>(e);
+      };
+      auto count = [&](int i, int token) {
+        bad_token |= static_cast<unsigned>(token) >= static_cast<unsigned>(P.V);
+        const int e = token - c0;
+        if (e < 0 || token >= c1) return;
+        touch(e, i < prompt ? atomicOr(&s.count[e], kInPrompt) : atomicAdd(&s.count[e], 1u));
+      };
+      const int32_t* hist = P.history + b * P.history_stride;
+      const int vectors = reinterpret_cast<uintptr_t>(hist) % 16 == 0 ? total / 4 : 0;
+#pragma unroll 4
+      for (int i = tid; i < vectors; i += kTextThreads) {
+        const int4 t = reinterpret_cast<const int4*>(hist)[i];
+        count(4 * i, t.x);
+        count(4 * i + 1, t.y);
+        count(4 * i + 2, t.z);
+        count(4 * i + 3, t.w);
+      }
+      for (int i = 4 * vectors + tid; i < total; i += kTextThreads) count(i, hist[i]);
+      if (tid < n && s.drafted[tid] >= 0)
+        touch(s.drafted[tid], atomicOr(&s.count[s.drafted[tid]], kDrafted));
+      const int32_t* names = P.bias_tokens + static_cast<int64_t>(b) * P.num_bias;
+      const float* values = P.bias_values + static_cast<int64_t>(b) * P.num_bias;
+      for (int i = tid; i < P.num_bias; i += kTextThreads) {
+        const int token = names[i];
+        bad_token |= token >= P.V;
+        if (token < c0 || token >= c1) continue;
+        // the first place that names a token adds up all of them, in their order
+        float sum = 0.0f;
+        bool first = true;
+        for (int j = 0; j < P.num_bias; j++)
+          if (names[j] == token) {
+            if (j < i) first = false;
+            sum = sum + values[j];
+          }
+        if (first) {
+          const int at = atomicAdd(&s.num_biased, 1);
+          s.biased[at] = static_cast<uint16_t>(token - c0);
+          s.bias[at] = sum;
+          touch(token - c0, atomicOr(&s.count[token - c0], kBiased));
+        }
+      }
+    }
+    if (bad_token) atomicOr(&s.bad, SPECV_DEV_BAD_TOKEN);
+  }
+
+  const T* in0 = reinterpret_cast<const T*>(P.in) + b * P.batch_stride;
+  T* out0 = reinterpret_cast<T*>(P.out) + b * P.out_batch_stride;
+  const int64_t words = (P.V + 31) / 32;
+  auto mask_of = [&](int row) { return P.allowed + (static_cast<int64_t>(b) * P.R + row) * words; };
+
+  // Copies and masks.
+  const int segments = (c1 - c0 + kSegment - 1) / kSegment;
+  const int tickets = (last_row - first_row) * segments;
+  while (true) {
+    int ticket = lane == 0 ? atomicAdd(&s.ticket, 1) : 0;
+    ticket = __shfl_sync(kFullMask, ticket, 0);
+    if (ticket >= tickets) break;
+    const int row = first_row + ticket / segments, segment = ticket % segments;
+    const T* in = in0 + row * P.row_stride;
+    T* out = out0 + row * P.out_row_stride;
+    const int32_t* mask = P.allowed ? mask_of(row) : nullptr;
+    const int s0 = c0 + segment * kSegment, s1 = min(c1, s0 + kSegment);
+    if (kLayout == kAligned && s1 - s0 == kSegment) {
+      uint32_t keep[kMine];
+#pragma unroll
+      for (int u = 0; u < kMine; u++) {
+        const int at = s0 + (u * 32 + lane) * kVec;
+        keep[u] = mask ? static_cast<uint32_t>(mask[at >> 5]) >> (at & 31) : ~0u;
+        keep[u] &= (1u << kVec) - 1;
+      }
+#pragma unroll
+      for (int u0 = 0; u0 < kMine; u0 += kFlight) {
+        uint4 data[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; u++)
+          if (keep[u0 + u])  // where nothing is allowed there is nothing to read
+            data[u] = *reinterpret_cast<const uint4*>(in + s0 + ((u0 + u) * 32 + lane) * kVec);
+#pragma unroll
+        for (int u = 0; u < kFlight; u++) {
+          if (keep[u0 + u] != (1u << kVec) - 1) mask_vec<DT>(data[u], keep[u0 + u]);
+          *reinterpret_cast<uint4*>(out + s0 + ((u0 + u) * 32 + lane) * kVec) = data[u];
+        }
+      }
+    } else {
+      // vectors that begin before the segment and end behind it go by elements
+      const int lead = kLayout == kSingle ? 0
+                                          : static_cast<int>(reinterpret_cast<uintptr_t>(in + s0) /
+                                                             sizeof(T) % kVec);
+#pragma unroll 4
+      for (int u = 0; u < kMine + (kVec > 1); u++) {
+        const int at = s0 - lead + (u * 32 + lane) * kVec;
+        const int from = max(at, s0), to = min(at + kVec, s1);
+        if (from >= to) continue;
+        uint32_t keep = (1u << kVec) - 1;
+        if (mask) {
+          uint64_t both = static_cast<uint32_t>(mask[from >> 5]);
+          if ((to - 1) >> 5 != from >> 5) both |= static_cast<uint64_t>(mask[(to - 1) >> 5]) << 32;
+          keep &= static_cast<uint32_t>(both >> (from & 31)) << (from - at);
+        }
+        if (kVec > 1 && to - from == kVec) {
+          uint4 data;
+          if (keep) data = *reinterpret_cast<const uint4*>(in + at);
+          mask_vec<DT>(data, keep);
+          *reinterpret_cast<uint4*>(out + at) = data;
+        } else {
+#pragma unroll
+          for (int e = 0; e < kVec; e++)
+            if (at + e >= from && at + e < to)
+              out[at + e] = keep >> e & 1 ? in[at + e] : static_cast<T>(E::kNegInf);
+        }
       }
     }
   }
-  const bool any_bad = __syncthreads_or(bad_token);
-  const int bad = s.bad | (any_bad ? SPECV_DEV_BAD_TOKEN : 0);
+  __syncthreads();
+  const int bad = s.bad;
   if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) P.status[b] = bad;
-
-  // This warp's touched entries: a bitmap word to a lane.  Its elements are
-  // 32 kVec in a row, once in every kThreads kVec (kVec = 1: any share will do,
-  // the block orders the stores).
-  const int word = lane >= kWords ? 0
-                   : kVec == 1    ? warp * kWords + lane
-                                  : (lane / kVec * (kThreads / 32) + warp) * kVec + lane % kVec;
-  uint32_t bits = lane < kWords && !bad ? s.touched[word] : 0;
-  int upto = __popc(bits);
-  const int own = upto;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int x = __shfl_up_sync(kFullMask, upto, o);
-    if (lane >= o) upto += x;
+  if (bad) {
+    for (int row = first_row; row < last_row; row++)
+      for (int t = c0 + tid; t < c1; t += kThreads)
+        out0[row * P.out_row_stride + t] = static_cast<T>(E::kNegInf);
+    return;
   }
-  const int fixes = __shfl_sync(kFullMask, upto, 31);
-  uint16_t* list = s.list + warp * kWords * 32;
-  for (int at = upto - own; bits; bits &= bits - 1)
-    list[at++] = static_cast<uint16_t>(word * 32 + __ffs(bits) - 1);
-  __syncwarp();
 
-  auto changed = [&](float z, int e, int row) {
+  // The entries that the text, a draft or a bias touches.  (In place, the copy
+  // left them as they were, or masked.)
+  const int touched = s.touched;
+  for (int i = tid; i < touched * (last_row - first_row); i += kThreads) {
+    const int k = i / touched, row = first_row + k, e = s.list[i - k * touched], t = c0 + e;
+    if (P.allowed && !(mask_of(row)[t >> 5] >> (t & 31) & 1)) continue;
+    float z = E::load(in0[row * P.row_stride + t]);
     const uint32_t w = s.count[e];
     uint32_t count = w & kCount;
     if (w & kDrafted) {
@@ -213,111 +294,39 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const Params P) {
     if (w & kBiased)
       for (int j = 0; j < s.num_biased; j++)
         if (s.biased[j] == e) z += s.bias[j];
-    return z;
-  };
-
-  const int n = s.n ? s.n : P.R;
-  const int first_row = blockIdx.z * P.rows, last_row = min(n, first_row + P.rows);
-  const int64_t words = (P.V + 31) / 32;
-  for (int row = first_row; row < last_row; row++) {
-    const T* in = reinterpret_cast<const T*>(P.in) + b * P.batch_stride + row * P.row_stride;
-    T* out = reinterpret_cast<T*>(P.out) + b * P.out_batch_stride + row * P.out_row_stride;
-    const int32_t* mask =
-        P.allowed ? P.allowed + (static_cast<int64_t>(b) * P.R + row) * words : nullptr;
-    const int lead =
-        kVec == 1 || !P.shifted
-            ? 0
-            : static_cast<int>(reinterpret_cast<uintptr_t>(in + c0) / sizeof(T) % kVec);
-    auto allowed = [&](int t) { return !mask || (mask[t >> 5] >> (t & 31) & 1); };
-    // the first of the touched elements, in flight with the copies
-    T fix = 0;
-    int fix_at = lane < fixes ? list[lane] : -1;
-    if (fix_at >= 0 && !allowed(c0 + fix_at)) fix_at = -1;
-    if (fix_at >= 0) fix = in[c0 + fix_at];
-#pragma unroll 1
-    for (int u0 = 0; u0 < kMine; u0 += kBlock) {
-      Vec data[kBlock];
-      uint32_t keep[kBlock];
-#pragma unroll
-      for (int u = 0; u < kBlock; u++) {
-        const int at = c0 - lead + ((u0 + u) * kThreads + tid) * kVec;
-        const int from = max(at, c0), to = min(at + kVec, c1);
-        keep[u] = 0;
-        if (from < to && !bad) {
-          keep[u] = (1u << kVec) - 1;
-          if (mask) {
-            uint64_t both = static_cast<uint32_t>(mask[from >> 5]);
-            if ((to - 1) >> 5 != from >> 5) both |= static_cast<uint64_t>(mask[(to - 1) >> 5]) << 32;
-            keep[u] &= static_cast<uint32_t>(both >> (from & 31)) << (from - at);
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kBlock; u++) {
-        const int at = c0 - lead + ((u0 + u) * kThreads + tid) * kVec;
-        if (keep[u] == 0) continue;  // nothing to read
-        if (at >= c0 && at + kVec <= c1) {
-          data[u] = *reinterpret_cast<const Vec*>(in + at);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kVec; e++)
-            if (at + e >= c0 && at + e < c1) data[u].x[e] = in[at + e];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kBlock; u++) {
-        const int at = c0 - lead + ((u0 + u) * kThreads + tid) * kVec;
-#pragma unroll
-        for (int e = 0; e < kVec; e++)
-          if (!(keep[u] >> e & 1)) data[u].x[e] = E::kNegInf;
-        if (at >= c0 && at + kVec <= c1) {
-          *reinterpret_cast<Vec*>(out + at) = data[u];
-        } else {
-#pragma unroll
-          for (int e = 0; e < kVec; e++)
-            if (at + e >= c0 && at + e < c1) out[at + e] = data[u].x[e];
-        }
-      }
-    }
-    if (lead && tid < lead) {  // what the shifted vectors leave at the chunk's end
-      const int t = c0 + kChunk - lead + tid;
-      if (t < c1) out[t] = bad || !allowed(t) ? static_cast<T>(E::kNegInf) : in[t];
-    }
-    if (kVec == 1 || P.shifted) __syncthreads();
-    else __syncwarp();
-    if (fix_at >= 0) out[c0 + fix_at] = E::store(changed(E::load(fix), fix_at, row));
-    for (int i = lane + 32; i < fixes; i += 32) {
-      const int e = list[i];
-      if (allowed(c0 + e)) out[c0 + e] = E::store(changed(E::load(in[c0 + e]), e, row));
-    }
+    out0[row * P.out_row_stride + t] = E::store(z);
   }
 }
 
-template <int DT, int kChunk, int kThreads, int kVec>
+template <int DT, int kChunk, Layout kLayout>
 cudaError_t run(const Params& P, int B, cudaStream_t stream) {
   constexpr int kSmem = sizeof(Text<kChunk>);
   if (kSmem > 48 * 1024) {
     const cudaError_t e =
-        cudaFuncSetAttribute(logits_kernel<DT, kChunk, kThreads, kVec>,
+        cudaFuncSetAttribute(logits_kernel<DT, kChunk, kLayout>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
   }
   const dim3 grid((P.V + kChunk - 1) / kChunk, B, (P.R + P.rows - 1) / P.rows);
-  logits_kernel<DT, kChunk, kThreads, kVec><<<grid, kThreads, kSmem, stream>>>(P);
+  logits_kernel<DT, kChunk, kLayout><<<grid, kThreads, kSmem, stream>>>(P);
   return cudaSuccess;
 }
 
-// Large chunks read the text less often; small ones fill the machine where
-// requests are few.
-template <int DT>
-cudaError_t launch(Params& P, int B, bool vectors, cudaStream_t stream) {
-  constexpr int kVec = DT == SPECV_F32 ? 4 : 8;
-  if (static_cast<int64_t>(B) * ((P.V + 8191) / 8192) >= 304) {
-    P.rows = P.R;
-    return vectors ? run<DT, 8192, 256, kVec>(P, B, stream) : run<DT, 8192, 256, 1>(P, B, stream);
-  }
+template <int DT, Layout kLayout>
+cudaError_t launch(Params& P, int B, cudaStream_t stream) {
+  // Large chunks read the text less often; small ones fill the machine where
+  // requests are few.
   P.rows = P.R < 8 ? P.R : 8;
-  return vectors ? run<DT, 1024, 128, kVec>(P, B, stream) : run<DT, 1024, 128, 1>(P, B, stream);
+  return static_cast<int64_t>(B) * ((P.V + 8191) / 8192) >= 304 ? run<DT, 8192, kLayout>(P, B, stream)
+                                                                : run<DT, 1024, kLayout>(P, B, stream);
+}
+
+template <int DT> cudaError_t launch(Params& P, int B, Layout layout, cudaStream_t stream) {
+  switch (layout) {
+    case kAligned: return launch<DT, kAligned>(P, B, stream);
+    case kShifted: return launch<DT, kShifted>(P, B, stream);
+    default: return launch<DT, kSingle>(P, B, stream);
+  }
 }
 
 }  // namespace
@@ -373,18 +382,16 @@ specv_status spec_process_logits(const void* logits, int64_t batch_stride, int64
                  V,
                  L,
                  num_bias,
-                 R,
-                 0};
-  // A row's place against 16 bytes: the same in the output, or single elements go.
+                 R};
   const int64_t n = static_cast<int64_t>(size);
-  const bool vectors = (reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(out)) % 16 == 0 &&
-                       (batch_stride - out_batch_stride) * n % 16 == 0 &&
-                       (row_stride - out_row_stride) * n % 16 == 0;
-  P.shifted = reinterpret_cast<uintptr_t>(logits) % 16 != 0 || batch_stride * n % 16 != 0 ||
-              row_stride * n % 16 != 0;
+  const bool alike = (reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(out)) % 16 == 0 &&
+                     (batch_stride - out_batch_stride) * n % 16 == 0 &&
+                     (row_stride - out_row_stride) * n % 16 == 0;
+  const bool aligned = aligned_to(logits, 16) && batch_stride * n % 16 == 0 && row_stride * n % 16 == 0;
+  const Layout layout = !alike ? kSingle : aligned ? kAligned : kShifted;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == SPECV_F32 ? launch<SPECV_F32>(P, B, vectors, st)
-                                           : launch<SPECV_BF16>(P, B, vectors, st);
+  const cudaError_t e = dtype == SPECV_F32 ? launch<SPECV_F32>(P, B, layout, st)
+                                           : launch<SPECV_BF16>(P, B, layout, st);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return SPECV_ERR_CUDA;
