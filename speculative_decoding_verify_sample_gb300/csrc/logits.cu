@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
   const float rho = P.repetition ? P.repetition[b] : 1.0f;
   const float freq = P.frequency ? P.frequency[b] : 0.0f;
   const float pres = P.presence ? P.presence[b] : 0.0f;
+  const int total = P.seq_lens[b], prompt = P.prompt_lens ? P.prompt_lens[b] : 0;
   if (tid == 0) {
     s.num_biased = 0;
     s.touched = 0;
@@ -117,7 +118,16 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
   __syncthreads();
 
   if (tid < kTextThreads) {
-    const int total = P.seq_lens[b], prompt = P.prompt_lens ? P.prompt_lens[b] : 0;
+    // the text's first tokens are on their way while the counts are cleared
+    constexpr int kAhead = 4;
+    const int32_t* hist = P.history + b * P.history_stride;
+    const bool fits = total >= 0 && total <= P.L;
+    const int vectors = fits && reinterpret_cast<uintptr_t>(hist) % 16 == 0 ? total / 4 : 0;
+    int4 ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; k++)
+      if (tid + k * kTextThreads < vectors)
+        ahead[k] = reinterpret_cast<const int4*>(hist)[tid + k * kTextThreads];
     for (int e = tid; e < kChunk / 4; e += kTextThreads)
       reinterpret_cast<uint4*>(s.count)[e] = make_uint4(0, 0, 0, 0);
     bool bad_token = false;
@@ -159,16 +169,18 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
         if (e < 0 || token >= c1) return;
         touch(e, i < prompt ? atomicOr(&s.count[e], kInPrompt) : atomicAdd(&s.count[e], 1u));
       };
-      const int32_t* hist = P.history + b * P.history_stride;
-      const int vectors = reinterpret_cast<uintptr_t>(hist) % 16 == 0 ? total / 4 : 0;
-#pragma unroll 4
-      for (int i = tid; i < vectors; i += kTextThreads) {
-        const int4 t = reinterpret_cast<const int4*>(hist)[i];
+      auto count4 = [&](int i, const int4& t) {
         count(4 * i, t.x);
         count(4 * i + 1, t.y);
         count(4 * i + 2, t.z);
         count(4 * i + 3, t.w);
-      }
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; k++)
+        if (tid + k * kTextThreads < vectors) count4(tid + k * kTextThreads, ahead[k]);
+#pragma unroll 4
+      for (int i = tid + kAhead * kTextThreads; i < vectors; i += kTextThreads)
+        count4(i, reinterpret_cast<const int4*>(hist)[i]);
       for (int i = 4 * vectors + tid; i < total; i += kTextThreads) count(i, hist[i]);
       if (tid < n && s.drafted[tid] >= 0)
         touch(s.drafted[tid], atomicOr(&s.count[s.drafted[tid]], kDrafted));
@@ -202,26 +214,40 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
   const int64_t words = (P.V + 31) / 32;
   auto mask_of = [&](int row) { return P.allowed + (static_cast<int64_t>(b) * P.R + row) * words; };
 
-  // Copies and masks.
+  // Copies and masks.  A segment's mask is read while the one before is copied.
   const int segments = (c1 - c0 + kSegment - 1) / kSegment;
   const int tickets = (last_row - first_row) * segments;
-  while (true) {
+  struct Segment {
+    int row, s0, s1;
+  };
+  auto take = [&](uint32_t (&keep)[kMine]) {
     int ticket = lane == 0 ? atomicAdd(&s.ticket, 1) : 0;
     ticket = __shfl_sync(kFullMask, ticket, 0);
-    if (ticket >= tickets) break;
-    const int row = first_row + ticket / segments, segment = ticket % segments;
-    const T* in = in0 + row * P.row_stride;
-    T* out = out0 + row * P.out_row_stride;
-    const int32_t* mask = P.allowed ? mask_of(row) : nullptr;
-    const int s0 = c0 + segment * kSegment, s1 = min(c1, s0 + kSegment);
-    if (kLayout == kAligned && s1 - s0 == kSegment) {
-      uint32_t keep[kMine];
+    Segment g{-1, 0, 0};
+    if (ticket >= tickets) return g;
+    g.row = first_row + ticket / segments;
+    g.s0 = c0 + ticket % segments * kSegment;
+    g.s1 = min(c1, g.s0 + kSegment);
+    if (kLayout == kAligned && g.s1 - g.s0 == kSegment) {
 #pragma unroll
       for (int u = 0; u < kMine; u++) {
-        const int at = s0 + (u * 32 + lane) * kVec;
-        keep[u] = mask ? static_cast<uint32_t>(mask[at >> 5]) >> (at & 31) : ~0u;
-        keep[u] &= (1u << kVec) - 1;
+        const int at = g.s0 + (u * 32 + lane) * kVec;
+        keep[u] = P.allowed ? static_cast<uint32_t>(mask_of(g.row)[at >> 5]) >> (at & 31) : ~0u;
       }
+    }
+    return g;
+  };
+  uint32_t keep_next[kMine];
+  Segment next = take(keep_next);
+  while (next.row >= 0) {
+    const int row = next.row, s0 = next.s0, s1 = next.s1;
+    uint32_t keep[kMine];
+#pragma unroll
+    for (int u = 0; u < kMine; u++) keep[u] = keep_next[u] & ((1u << kVec) - 1);
+    const T* in = in0 + row * P.row_stride;
+    T* out = out0 + row * P.out_row_stride;
+    if (kLayout == kAligned && s1 - s0 == kSegment) {
+      bool asked = false;
 #pragma unroll
       for (int u0 = 0; u0 < kMine; u0 += kFlight) {
         uint4 data[kFlight];
@@ -229,6 +255,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
         for (int u = 0; u < kFlight; u++)
           if (keep[u0 + u])  // where nothing is allowed there is nothing to read
             data[u] = *reinterpret_cast<const uint4*>(in + s0 + ((u0 + u) * 32 + lane) * kVec);
+        if (!asked) {
+          next = take(keep_next);
+          asked = true;
+        }
 #pragma unroll
         for (int u = 0; u < kFlight; u++) {
           if (keep[u0 + u] != (1u << kVec) - 1) mask_vec<DT>(data[u], keep[u0 + u]);
@@ -236,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
         }
       }
     } else {
+      const int32_t* mask = P.allowed ? mask_of(row) : nullptr;
       // vectors that begin before the segment and end behind it go by elements
       const int lead = kLayout == kSingle ? 0
                                           : static_cast<int>(reinterpret_cast<uintptr_t>(in + s0) /
@@ -263,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
               out[at + e] = keep >> e & 1 ? in[at + e] : static_cast<T>(E::kNegInf);
         }
       }
+      next = take(keep_next);
     }
   }
   __syncthreads();
