@@ -49,8 +49,7 @@ template <> struct Elt<SPECV_BF16> {
   static __device__ uint16_t store(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 };
 
-constexpr int kThreads = 256;
-constexpr int kTextThreads = 128;  // of them, the ones that count the text first
+constexpr int kTextThreads = 128;  // threads of a block that count the text first
 constexpr int kSegment = 1024;     // entries of a row that a warp takes at a time
 
 // What a block needs of one request's text, for its chunk of the vocabulary.
@@ -59,9 +58,9 @@ template <int kChunk> struct Text {
   uint64_t path[kMaxNodes];
   float bias[SPECV_MAX_BIAS];       // sums of the biases in this chunk ...
   uint16_t biased[SPECV_MAX_BIAS];  // ... and their entries
-  uint16_t list[kChunk];            // touched entries
   int drafted[kMaxNodes];  // entry of node i's token, -1 where it is another chunk's
   int num_biased, touched, ticket, bad;
+  uint16_t list[8];  // touched entries: at most kChunk, and the text's, drafts' and biases' number
 };
 
 // How a row's elements lie against 16 bytes: every row begins there, rows
@@ -71,13 +70,21 @@ enum Layout { kAligned, kShifted, kSingle };
 // -inf where keep's bit is 0.
 template <int DT> __device__ __forceinline__ void mask_vec(uint4& v, uint32_t keep) {
   uint32_t* w = &v.x;
+  if (DT == SPECV_F32) {
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    if (DT == SPECV_F32) {
+    for (int i = 0; i < 4; i++)
       if (!(keep >> i & 1)) w[i] = 0xff800000u;
-    } else {
-      const uint32_t m = (keep >> 2 * i & 1) * 0xffffu | (keep >> (2 * i + 1) & 1) * 0xffff0000u;
-      w[i] = (w[i] & m) | (0xff80ff80u & ~m);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      // four bits to the tops of four bytes (the shifted copies do not meet), which
+      // prmt then spreads over two bytes each
+      const uint32_t tops = (keep >> 4 * i & 15u) * 0x10204080u;
+      uint32_t lo, hi;
+      asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(lo) : "r"(tops));
+      asm("prmt.b32 %0, %1, 0, 0xbbaa;" : "=r"(hi) : "r"(tops));
+      w[2 * i] = (w[2 * i] & lo) | (0xff80ff80u & ~lo);
+      w[2 * i + 1] = (w[2 * i + 1] & hi) | (0xff80ff80u & ~hi);
     }
   }
 }
@@ -89,8 +96,8 @@ template <int DT> __device__ __forceinline__ void mask_vec(uint4& v, uint32_t ke
 // list the entries they touch; those join the streaming when they are done.
 // Then the listed entries are computed from the input, one to a thread, and
 // stored over the copies.
-template <int DT, int kChunk, Layout kLayout>
-__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
+template <int DT, int kChunk, int kThreads, Layout kLayout>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const Params P) {
   using E = Elt<DT>;
   using T = typename E::T;
   constexpr int kVec = kLayout == kSingle ? 1 : 16 / sizeof(T);
@@ -158,15 +165,16 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
     }
     asm volatile("bar.sync 1, %0;" ::"n"(kTextThreads) : "memory");
     if (!s.bad) {
+      unsigned largest = 0;
       // Counts are whole numbers: the order in which the threads add does not
       // show.  Whoever finds an untouched word lists its entry.
       auto touch = [&](int e, uint32_t old) {
         if (old == 0) s.list[atomicAdd(&s.touched, 1)] = static_cast<uint16_t>(e);
       };
       auto count = [&](int i, int token) {
-        bad_token |= static_cast<unsigned>(token) >= static_cast<unsigned>(P.V);
+        largest = max(largest, static_cast<unsigned>(token));
         const int e = token - c0;
-        if (e < 0 || token >= c1) return;
+        if (static_cast<unsigned>(e) >= static_cast<unsigned>(c1 - c0)) return;
         touch(e, i < prompt ? atomicOr(&s.count[e], kInPrompt) : atomicAdd(&s.count[e], 1u));
       };
       auto count4 = [&](int i, const int4& t) {
@@ -182,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
       for (int i = tid + kAhead * kTextThreads; i < vectors; i += kTextThreads)
         count4(i, reinterpret_cast<const int4*>(hist)[i]);
       for (int i = 4 * vectors + tid; i < total; i += kTextThreads) count(i, hist[i]);
+      bad_token |= largest >= static_cast<unsigned>(P.V);
       if (tid < n && s.drafted[tid] >= 0)
         touch(s.drafted[tid], atomicOr(&s.count[s.drafted[tid]], kDrafted));
       const int32_t* names = P.bias_tokens + static_cast<int64_t>(b) * P.num_bias;
@@ -215,8 +224,8 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
   auto mask_of = [&](int row) { return P.allowed + (static_cast<int64_t>(b) * P.R + row) * words; };
 
   // Copies and masks.  A segment's mask is read while the one before is copied.
-  const int segments = (c1 - c0 + kSegment - 1) / kSegment;
-  const int tickets = (last_row - first_row) * segments;
+  constexpr int kSegments = kChunk / kSegment;
+  const int tickets = (last_row - first_row) * kSegments;
   struct Segment {
     int row, s0, s1;
   };
@@ -225,9 +234,9 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
     ticket = __shfl_sync(kFullMask, ticket, 0);
     Segment g{-1, 0, 0};
     if (ticket >= tickets) return g;
-    g.row = first_row + ticket / segments;
-    g.s0 = c0 + ticket % segments * kSegment;
-    g.s1 = min(c1, g.s0 + kSegment);
+    g.row = first_row + ticket / kSegments;
+    g.s0 = c0 + ticket % kSegments * kSegment;
+    g.s1 = min(c1, g.s0 + kSegment);  // nothing left in the last chunk's last segments
     if (kLayout == kAligned && g.s1 - g.s0 == kSegment) {
 #pragma unroll
       for (int u = 0; u < kMine; u++) {
@@ -309,9 +318,11 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
 
   // The entries that the text, a draft or a bias touches.  (In place, the copy
   // left them as they were, or masked.)
-  const int touched = s.touched;
-  for (int i = tid; i < touched * (last_row - first_row); i += kThreads) {
-    const int k = i / touched, row = first_row + k, e = s.list[i - k * touched], t = c0 + e;
+  const int touched = s.touched, blocks = (touched + 31) / 32;
+  for (int unit = tid / 32; unit < blocks * (last_row - first_row); unit += kThreads / 32) {
+    const int row = first_row + unit / blocks, k = unit % blocks * 32 + lane;
+    if (k >= touched) continue;
+    const int e = s.list[k], t = c0 + e;
     if (P.allowed && !(mask_of(row)[t >> 5] >> (t & 31) & 1)) continue;
     float z = E::load(in0[row * P.row_stride + t]);
     const uint32_t w = s.count[e];
@@ -330,17 +341,18 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const Params P) {
   }
 }
 
-template <int DT, int kChunk, Layout kLayout>
+template <int DT, int kChunk, int kThreads, Layout kLayout>
 cudaError_t run(const Params& P, int B, cudaStream_t stream) {
-  constexpr int kSmem = sizeof(Text<kChunk>);
-  if (kSmem > 48 * 1024) {
+  const int most = P.L + P.R + P.num_bias;
+  const int smem = static_cast<int>(sizeof(Text<kChunk>)) + 2 * (most < kChunk ? most : kChunk);
+  if (smem > 48 * 1024) {
     const cudaError_t e =
-        cudaFuncSetAttribute(logits_kernel<DT, kChunk, kLayout>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaFuncSetAttribute(logits_kernel<DT, kChunk, kThreads, kLayout>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
   const dim3 grid((P.V + kChunk - 1) / kChunk, B, (P.R + P.rows - 1) / P.rows);
-  logits_kernel<DT, kChunk, kLayout><<<grid, kThreads, kSmem, stream>>>(P);
+  logits_kernel<DT, kChunk, kThreads, kLayout><<<grid, kThreads, smem, stream>>>(P);
   return cudaSuccess;
 }
 
@@ -349,8 +361,8 @@ cudaError_t launch(Params& P, int B, cudaStream_t stream) {
   // Large chunks read the text less often; small ones fill the machine where
   // requests are few.
   P.rows = P.R < 8 ? P.R : 8;
-  return static_cast<int64_t>(B) * ((P.V + 8191) / 8192) >= 304 ? run<DT, 8192, kLayout>(P, B, stream)
-                                                                : run<DT, 1024, kLayout>(P, B, stream);
+  return static_cast<int64_t>(B) * ((P.V + 8191) / 8192) >= 304 ? run<DT, 8192, 256, kLayout>(P, B, stream)
+                                                                : run<DT, 1024, 256, kLayout>(P, B, stream);
 }
 
 template <int DT> cudaError_t launch(Params& P, int B, Layout layout, cudaStream_t stream) {
