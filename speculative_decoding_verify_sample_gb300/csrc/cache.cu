@@ -7,13 +7,9 @@ using namespace specv_cache_ops;
 
 namespace {
 
-constexpr double kTwoPi = 6.283185307179586476925286766559;
-constexpr double kInvTwoPi = 0.15915494309189533576888376337251;
-
 // ------------------------------------------------------------------ append
 
-constexpr int kAppendThreads = 256;
-constexpr int kTokens = 4;                  // nodes a block takes
+constexpr int kAppendWarps = 8;
 constexpr int kHalfMax = SPECV_MAX_HEAD_DIM / 2;
 
 struct AppendParams {
@@ -26,151 +22,232 @@ struct AppendParams {
   const float* inv_freq;
   int32_t* status;
   float eps, rope_scale;
-  int N, q_heads, rot_dim, interleaved;
+  int B, N, q_heads, rot_dim, interleaved;
 };
 
-// A row of head_dim values is a group's: one lane to eight values, so that
-// every load and store is 16 bytes.
-template <class E, int kLanes>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams P) {
-  constexpr int kGroups = kAppendThreads / kLanes;
-  __shared__ int s_n, s_bad;
-  __shared__ int s_pos[kMaxNodes];
-  __shared__ float2 s_turn[kTokens][kHalfMax];
-  __shared__ __align__(16) float s_x[kGroups][kLanes * 8];
+// cos and sin of pos * freq.  The angle of a far position loses its last digits
+// in 32 bits (near 131072 radians they are 2^-7 apart), so it is taken in turns:
+// the frequency's fraction of a turn as a 64-bit whole number, whose product
+// with the position drops whole turns by itself and keeps the top 32 bits.
+__device__ __forceinline__ float2 turn(int pos, float freq, float scale) {
+  const double turns = static_cast<double>(freq) * 0.15915494309189533576888;
+  const double part = turns - floor(turns);  // [0, 1): 1 itself, by rounding, is no turn
+  const uint64_t steps = part < 1.0 ? static_cast<uint64_t>(part * 18446744073709551616.0) : 0;
+  const int top = static_cast<int>(static_cast<uint32_t>(steps * static_cast<uint64_t>(pos) >> 32));
+  float sn, cs;
+  sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31 half turns
+  if (!isfinite(freq)) sn = cs = NAN;
+  return make_float2(cs * scale, sn * scale);
+}
 
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int tiles = (P.N + kTokens - 1) / kTokens;
-  const int b = blockIdx.x / tiles, first = (blockIdx.x % tiles) * kTokens;
+// A warp has a node and goes through its heads, 32 / kLanes rows at a time.  A
+// lane has two 16-byte pieces of a row, the two that a rotation in halves
+// joins, and their cosines and sines stay in its registers for all heads.
+// kOdd: the halves do not begin at a piece; their elements meet in shared memory.
+template <class E, int kLanes, bool kOdd>
+__global__ void __launch_bounds__(kAppendWarps * 32, 3) append_kernel(const AppendParams P) {
+  constexpr int kRowsAtOnce = 32 / kLanes;
+  __shared__ float2 s_turn[kAppendWarps][kHalfMax];
+  __shared__ __align__(16) float s_x[kOdd ? kAppendWarps * kRowsAtOnce : 1][kOdd ? kLanes * 16 : 4];
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int token = blockIdx.x * kAppendWarps + warp;
+  const int b = token / P.N, i = token - b * P.N;
+  if (b >= P.B) return;
   const Cache& C = P.cache;
-  const int D = C.head_dim;
-
-  if (tid < 32) {
-    const int64_t slots = static_cast<int64_t>(C.max_pages) * C.page_size;
-    Tree t = read_tree(P.parents, P.n_nodes, C.lens, b, P.N, slots, lane);
-    if (!t.bad && __any_sync(kFullMask, bad_pages(C, b, t.len, t.len + t.n, lane, 32)))
-      t.bad |= SPECV_DEV_BAD_CACHE;
-    if (!t.bad) {
-      int depth[2];
-      depths(t, depth);
-      s_pos[lane] = t.len + depth[0];
-      s_pos[lane + 32] = t.len + depth[1];
-    }
-    if (lane == 0) {
-      s_n = t.n;
-      s_bad = t.bad;
-      if (first == 0) P.status[b] = static_cast<int32_t>(t.bad);
-    }
+  const int pieces = C.head_dim / 8, half = P.rot_dim / 2;
+  const int sub = lane % kLanes, group = lane / kLanes;
+  // this lane's pieces of a row; behind the last: none
+  int piece[2];
+  if (!kOdd && !P.interleaved && sub < half / 8) {
+    piece[0] = sub;
+    piece[1] = sub + half / 8;
+  } else {
+    const int done = kOdd || P.interleaved ? 0 : half / 8, left = pieces - 2 * done;
+    piece[0] = sub - done < (left + 1) / 2 ? done + sub : pieces;
+    piece[1] = sub - done < left / 2 ? piece[0] + (left + 1) / 2 : pieces;
   }
-  __syncthreads();
-  const bool bad = s_bad != 0;
-  const int n = s_n ? s_n : P.N;
-  const int count = min(kTokens, n - first);
-  if (count <= 0) return;
+  const bool mine[2] = {piece[0] < pieces, piece[1] < pieces};
 
-  // The angle of a far position loses its last digits in 32 bits (131072 radians
-  // are known to 2^-7): the product and its remainder by 2 pi are taken in 64,
-  // once for all heads; sincosf then sees at most pi.
-  const int half = P.rot_dim / 2;
-  if (!bad) {
-    for (int e = tid; e < count * half; e += kAppendThreads) {
-      const int t = e / half, j = e - t * half;
-      const double a = static_cast<double>(s_pos[first + t]) * static_cast<double>(P.inv_freq[j]);
-      const double r = fma(-rint(a * kInvTwoPi), kTwoPi, a);
-      float sn, cs;
-      sincosf(static_cast<float>(r), &sn, &cs);
-      s_turn[t][j] = make_float2(cs * P.rope_scale, sn * P.rope_scale);
-    }
-  }
-  __syncthreads();
-
-  const int sub = tid % kLanes, group = tid / kLanes;
-  const int d = sub * 8;
-  const bool mine = d < D;
-  float* x_row = s_x[group];
-  const int heads = P.q_heads + 2 * C.heads;
-  for (int r = group; r < count * heads; r += kGroups) {
-    const int t = r / heads, h = r - t * heads, i = first + t;
-    const bool is_q = h < P.q_heads, is_v = h >= P.q_heads + C.heads;
-    const Rows& in = is_q ? P.q : is_v ? P.v : P.k;
-    const int hh = is_q ? h : is_v ? h - P.q_heads - C.heads : h - P.q_heads;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (bad) {
-      if (is_q && mine)
-        *reinterpret_cast<uint4*>(P.q_out.data + b * P.q_out.batch_stride +
-                                  i * P.q_out.node_stride + hh * P.q_out.head_stride + d) = w;
-      continue;
-    }
-    if (mine)
-      w = *reinterpret_cast<const uint4*>(in.data + b * in.batch_stride + i * in.node_stride +
-                                          hh * in.head_stride + d);
-    if (!is_v) {
-      float x[8];
-      const uint32_t* words = &w.x;
+  // Passes over the heads: queries, keys, values, each kRowsAtOnce rows.
+  const int q_passes = (P.q_heads + kRowsAtOnce - 1) / kRowsAtOnce;
+  const int kv_passes = (C.heads + kRowsAtOnce - 1) / kRowsAtOnce;
+  const int passes = q_passes + 2 * kv_passes;
+  auto load = [&](int p, uint4 (&w)[2]) {
+    const bool is_q = p < q_passes, is_k = p < q_passes + kv_passes;
+    const Rows& in = is_q ? P.q : is_k ? P.k : P.v;
+    const int h = (is_q ? p : is_k ? p - q_passes : p - q_passes - kv_passes) * kRowsAtOnce + group;
+    const uint16_t* from = in.data + b * in.batch_stride + i * in.node_stride + h * in.head_stride;
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const float2 f = E::unpack(words[e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
+    for (int k = 0; k < 2; k++) {
+      w[k] = make_uint4(0, 0, 0, 0);
+      if (mine[k] && h < (is_q ? P.q_heads : C.heads))
+        w[k] = *reinterpret_cast<const uint4*>(from + piece[k] * 8);
+    }
+  };
+  int p = blockIdx.y;
+  uint4 ahead[2];
+  if (p < passes) load(p, ahead);  // on its way while the request is checked
+
+  Tree t = read_tree(P.parents, P.n_nodes, C.lens, b, P.N,
+                     static_cast<int64_t>(C.max_pages) * C.page_size, lane);
+  if (!t.bad && __any_sync(kFullMask, bad_pages(C, b, t.len, t.len + t.n, lane, 32)))
+    t.bad |= SPECV_DEV_BAD_CACHE;
+  if (i == 0 && blockIdx.y == 0 && lane == 0) P.status[b] = static_cast<int32_t>(t.bad);
+  if (i >= (t.n ? t.n : P.N)) return;
+  if (t.bad) {  // a flagged request: queries become 0, the cache stays
+    for (; p < q_passes; p += gridDim.y)
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        const int h = p * kRowsAtOnce + group;
+        if (mine[k] && h < P.q_heads)
+          *reinterpret_cast<uint4*>(P.q_out.data + b * P.q_out.batch_stride +
+                                    i * P.q_out.node_stride + h * P.q_out.head_stride +
+                                    piece[k] * 8) = make_uint4(0, 0, 0, 0);
       }
-      const uint16_t* weight = is_q ? P.q_weight : P.k_weight;
-      const unsigned mask = kLanes == 32 ? kFullMask
-                                         : ((1u << kLanes) - 1u) << (lane / kLanes * kLanes);
+    return;
+  }
+
+  float2 cs[2][4];  // of this lane's pairs: four of each piece, or eight of both
+  if (half) {
+    int depth[2];
+    depths(t, depth);
+    const int pos = t.len + at_node(depth, i);
+    for (int j = lane; j < half; j += 32) s_turn[warp][j] = turn(pos, P.inv_freq[j], P.rope_scale);
+    __syncwarp();
+    if (!kOdd) {
+#pragma unroll
+      for (int k = 0; k < 2; k++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const int j = P.interleaved ? piece[k] * 4 + e : piece[0] * 8 + 4 * k + e;
+          cs[k][e] = mine[k] && j < half ? s_turn[warp][j] : make_float2(1.0f, 0.0f);
+        }
+    }
+  }
+  const bool joined = !kOdd && !P.interleaved && sub < half / 8;
+
+  const int64_t slot = C.slot(b, t.len + i);
+  int kind = -1;  // 0 queries, 1 keys, 2 values
+  const uint16_t* weight = nullptr;
+  uint4 g[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  for (; p < passes; p += gridDim.y) {
+    uint4 w[2] = {ahead[0], ahead[1]};
+    if (p + static_cast<int>(gridDim.y) < passes) load(p + gridDim.y, ahead);
+    const int now = p < q_passes ? 0 : p < q_passes + kv_passes ? 1 : 2;
+    const int h = (now == 0 ? p : now == 1 ? p - q_passes : p - q_passes - kv_passes) * kRowsAtOnce + group;
+    if (now != kind) {
+      kind = now;
+      weight = kind == 0 ? P.q_weight : kind == 1 ? P.k_weight : nullptr;
+      if (weight)
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+          if (mine[k]) g[k] = *reinterpret_cast<const uint4*>(weight + piece[k] * 8);
+    }
+    if (kind < 2 && (weight || half)) {
+      float x[2][8];
+#pragma unroll
+      for (int k = 0; k < 2; k++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const float2 f = E::unpack((&w[k].x)[e]);
+          x[k][2 * e] = f.x;
+          x[k][2 * e + 1] = f.y;
+        }
       if (weight) {
         float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; e++) sum = fmaf(x[e], x[e], sum);
+        for (int k = 0; k < 2; k++)
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o /= 2) sum += __shfl_xor_sync(mask, sum, o);
-        const float inv = rsqrtf(sum / static_cast<float>(D) + P.eps);
-        if (mine) {
-          const uint4 g = *reinterpret_cast<const uint4*>(weight + d);
-          const uint32_t* gw = &g.x;
+          for (int e = 0; e < 8; e++) sum = fmaf(x[k][e], x[k][e], sum);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
+        const float inv = rsqrtf(sum / static_cast<float>(C.head_dim) + P.eps);
+#pragma unroll
+        for (int k = 0; k < 2; k++)
 #pragma unroll
           for (int e = 0; e < 4; e++) {
-            const float2 f = E::unpack(gw[e]);
-            x[2 * e] = x[2 * e] * inv * f.x;
-            x[2 * e + 1] = x[2 * e + 1] * inv * f.y;
+            const float2 f = E::unpack((&g[k].x)[e]);
+            x[k][2 * e] = x[k][2 * e] * inv * f.x;
+            x[k][2 * e + 1] = x[k][2 * e + 1] * inv * f.y;
           }
-        }
       }
-      if (P.interleaved) {
+      if (kOdd) {
+        float* row = s_x[warp * kRowsAtOnce + group];
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 4; e++)
-          if (d + 2 * e < P.rot_dim) {
-            const float2 cs = s_turn[t][d / 2 + e];
-            const float a = x[2 * e], c = x[2 * e + 1];
-            x[2 * e] = a * cs.x - c * cs.y;
-            x[2 * e + 1] = c * cs.x + a * cs.y;
+        for (int k = 0; k < 2; k++)
+          if (mine[k]) {
+            *reinterpret_cast<float4*>(row + piece[k] * 8) =
+                make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
+            *reinterpret_cast<float4*>(row + piece[k] * 8 + 4) =
+                make_float4(x[k][4], x[k][5], x[k][6], x[k][7]);
           }
-      } else if (half) {
-        // the partner half a rotation away is another lane's
-        __syncwarp(mask);
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 8; e++) x_row[d + e] = x[e];
-        __syncwarp(mask);
+        for (int k = 0; k < 2; k++)
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const int d = piece[k] * 8 + e;
+            if (!mine[k] || d >= P.rot_dim) continue;
+            const float2 c = s_turn[warp][d < half ? d : d - half];
+            x[k][e] = d < half ? x[k][e] * c.x - row[d + half] * c.y
+                               : x[k][e] * c.x + row[d - half] * c.y;
+          }
+      } else if (P.interleaved) {
+        if (half)
+#pragma unroll
+          for (int k = 0; k < 2; k++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              const float a = x[k][2 * e], c = x[k][2 * e + 1];
+              if (piece[k] * 4 + e < half) {
+                x[k][2 * e] = a * cs[k][e].x - c * cs[k][e].y;
+                x[k][2 * e + 1] = c * cs[k][e].x + a * cs[k][e].y;
+              }
+            }
+      } else if (joined) {
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-          const int at = d + e;
-          if (at < half) {
-            const float2 cs = s_turn[t][at];
-            x[e] = x[e] * cs.x - x_row[at + half] * cs.y;
-          } else if (at < P.rot_dim) {
-            const float2 cs = s_turn[t][at - half];
-            x[e] = x[e] * cs.x + x_row[at - half] * cs.y;
-          }
+          const float2 f = cs[e / 4][e % 4];
+          const float a = x[0][e], c = x[1][e];
+          x[0][e] = a * f.x - c * f.y;
+          x[1][e] = c * f.x + a * f.y;
         }
       }
 #pragma unroll
-      for (int e = 0; e < 4; e++) (&w.x)[e] = E::pack(x[2 * e], x[2 * e + 1]);
+      for (int k = 0; k < 2; k++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) (&w[k].x)[e] = E::pack(x[k][2 * e], x[k][2 * e + 1]);
     }
-    uint16_t* to;
-    if (is_q)
-      to = P.q_out.data + b * P.q_out.batch_stride + i * P.q_out.node_stride +
-           hh * P.q_out.head_stride;
-    else
-      to = (is_v ? C.v : C.k) + C.slot(b, C.lens[b] + i) + hh * C.head_stride;
-    if (mine) *reinterpret_cast<uint4*>(to + d) = w;
+    uint16_t* to = kind == 0 ? P.q_out.data + b * P.q_out.batch_stride + i * P.q_out.node_stride +
+                                   h * P.q_out.head_stride
+                             : (kind == 1 ? C.k : C.v) + slot + h * C.head_stride;
+#pragma unroll
+    for (int k = 0; k < 2; k++)
+      if (mine[k] && h < (kind == 0 ? P.q_heads : C.heads))
+        *reinterpret_cast<uint4*>(to + piece[k] * 8) = w[k];
+  }
+}
+
+template <class E>
+void run_append(const AppendParams& P, cudaStream_t stream) {
+  const int half = P.rot_dim / 2;
+  const bool odd = half % 8 != 0 && !P.interleaved, narrow = P.cache.head_dim <= 64;
+  const int rows_at_once = narrow ? 8 : 4;
+  const int passes = (P.q_heads + rows_at_once - 1) / rows_at_once +
+                     2 * ((P.cache.heads + rows_at_once - 1) / rows_at_once);
+  // Few nodes: their heads are shared out over several warps, 16 to an SM.
+  const int tokens = P.B * P.N;
+  const int splits = tokens >= 2432 ? 1 : (2432 + tokens - 1) / tokens;
+  const dim3 grid((tokens + kAppendWarps - 1) / kAppendWarps, splits < passes ? splits : passes);
+  constexpr int kThreads = kAppendWarps * 32;
+  if (narrow) {
+    if (odd) append_kernel<E, 4, true><<<grid, kThreads, 0, stream>>>(P);
+    else append_kernel<E, 4, false><<<grid, kThreads, 0, stream>>>(P);
+  } else {
+    if (odd) append_kernel<E, 8, true><<<grid, kThreads, 0, stream>>>(P);
+    else append_kernel<E, 8, false><<<grid, kThreads, 0, stream>>>(P);
   }
 }
 
@@ -300,20 +377,14 @@ specv_status spec_append_nodes(const specv_cache* cache, const specv_rows* q, co
                        status,
                        eps,
                        rope_scale,
+                       B,
                        N,
                        q_heads,
                        rot_dim,
                        interleaved};
-  const unsigned grid = static_cast<unsigned>(B) * ((N + kTokens - 1) / kTokens);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool narrow = cache->head_dim <= 64;
-  if (cache->dtype == SPECV_BF16) {
-    if (narrow) append_kernel<Bf16, 8><<<grid, kAppendThreads, 0, st>>>(P);
-    else append_kernel<Bf16, 16><<<grid, kAppendThreads, 0, st>>>(P);
-  } else {
-    if (narrow) append_kernel<F16, 8><<<grid, kAppendThreads, 0, st>>>(P);
-    else append_kernel<F16, 16><<<grid, kAppendThreads, 0, st>>>(P);
-  }
+  if (cache->dtype == SPECV_BF16) run_append<Bf16>(P, st);
+  else run_append<F16>(P, st);
   return launched();
 }
 
