@@ -29,10 +29,13 @@ struct AppendParams {
 // in 32 bits (near 131072 radians they are 2^-7 apart), so it is taken in turns:
 // the frequency's fraction of a turn as a 64-bit whole number, whose product
 // with the position drops whole turns by itself and keeps the top 32 bits.
-__device__ __forceinline__ float2 turn(int pos, float freq, float scale) {
+__device__ __forceinline__ uint64_t steps_of(float freq) {
   const double turns = static_cast<double>(freq) * 0.15915494309189533576888;
   const double part = turns - floor(turns);  // [0, 1): 1 itself, by rounding, is no turn
-  const uint64_t steps = part < 1.0 ? static_cast<uint64_t>(part * 18446744073709551616.0) : 0;
+  return part < 1.0 ? static_cast<uint64_t>(part * 18446744073709551616.0) : 0;
+}
+
+__device__ __forceinline__ float2 turn(int pos, float freq, uint64_t steps, float scale) {
   const int top = static_cast<int>(static_cast<uint32_t>(steps * static_cast<uint64_t>(pos) >> 32));
   float sn, cs;
   sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31 half turns
@@ -47,7 +50,9 @@ __device__ __forceinline__ float2 turn(int pos, float freq, float scale) {
 template <class E, int kLanes, bool kOdd>
 __global__ void __launch_bounds__(kAppendWarps * 32, 3) append_kernel(const AppendParams P) {
   constexpr int kRowsAtOnce = 32 / kLanes;
+  constexpr int kStages = kOdd ? 2 : 4;  // passes of a warp in shared memory
   __shared__ float2 s_turn[kAppendWarps][kHalfMax];
+  __shared__ uint4 s_in[kAppendWarps][kStages][2][32];
   __shared__ __align__(16) float s_x[kOdd ? kAppendWarps * kRowsAtOnce : 1][kOdd ? kLanes * 16 : 4];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -73,27 +78,40 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 3) append_kernel(const Appe
   const int q_passes = (P.q_heads + kRowsAtOnce - 1) / kRowsAtOnce;
   const int kv_passes = (C.heads + kRowsAtOnce - 1) / kRowsAtOnce;
   const int passes = q_passes + 2 * kv_passes;
-  auto load = [&](int p, uint4 (&w)[2]) {
+  // A lane copies and reads its own places, so nothing but its own wait orders them.
+  auto load = [&](int p, int stage) {
     const bool is_q = p < q_passes, is_k = p < q_passes + kv_passes;
     const Rows& in = is_q ? P.q : is_k ? P.k : P.v;
     const int h = (is_q ? p : is_k ? p - q_passes : p - q_passes - kv_passes) * kRowsAtOnce + group;
+    const bool real = p < passes && h < (is_q ? P.q_heads : C.heads);
     const uint16_t* from = in.data + b * in.batch_stride + i * in.node_stride + h * in.head_stride;
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-      w[k] = make_uint4(0, 0, 0, 0);
-      if (mine[k] && h < (is_q ? P.q_heads : C.heads))
-        w[k] = *reinterpret_cast<const uint4*>(from + piece[k] * 8);
+      const bool some = real && mine[k];
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(
+                       __cvta_generic_to_shared(&s_in[warp][stage][k][lane]))),
+                   "l"(some ? from + piece[k] * 8 : in.data), "r"(some ? 16 : 0)
+                   : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int p = blockIdx.y;
-  uint4 ahead[2];
-  if (p < passes) load(p, ahead);  // on its way while the request is checked
+#pragma unroll
+  for (int k = 0; k < kStages - 1; k++) load(p + k * gridDim.y, k);  // while the request is checked
 
+  float freq[2];
+  uint64_t steps[2];
+#pragma unroll
+  for (int k = 0; k < 2; k++) {
+    freq[k] = lane + 32 * k < half ? P.inv_freq[lane + 32 * k] : 0.0f;
+    steps[k] = steps_of(freq[k]);
+  }
   Tree t = read_tree(P.parents, P.n_nodes, C.lens, b, P.N,
                      static_cast<int64_t>(C.max_pages) * C.page_size, lane);
   if (!t.bad && __any_sync(kFullMask, bad_pages(C, b, t.len, t.len + t.n, lane, 32)))
     t.bad |= SPECV_DEV_BAD_CACHE;
   if (i == 0 && blockIdx.y == 0 && lane == 0) P.status[b] = static_cast<int32_t>(t.bad);
+  if (t.bad || i >= t.n) asm volatile("cp.async.wait_all;" ::: "memory");
   if (i >= (t.n ? t.n : P.N)) return;
   if (t.bad) {  // a flagged request: queries become 0, the cache stays
     for (; p < q_passes; p += gridDim.y)
@@ -108,12 +126,16 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 3) append_kernel(const Appe
     return;
   }
 
+  const int64_t slot = C.slot(b, t.len + i);
   float2 cs[2][4];  // of this lane's pairs: four of each piece, or eight of both
   if (half) {
     int depth[2];
     depths(t, depth);
     const int pos = t.len + at_node(depth, i);
-    for (int j = lane; j < half; j += 32) s_turn[warp][j] = turn(pos, P.inv_freq[j], P.rope_scale);
+#pragma unroll
+    for (int k = 0; k < 2; k++)
+      if (lane + 32 * k < half)
+        s_turn[warp][lane + 32 * k] = turn(pos, freq[k], steps[k], P.rope_scale);
     __syncwarp();
     if (!kOdd) {
 #pragma unroll
@@ -127,13 +149,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 3) append_kernel(const Appe
   }
   const bool joined = !kOdd && !P.interleaved && sub < half / 8;
 
-  const int64_t slot = C.slot(b, t.len + i);
   int kind = -1;  // 0 queries, 1 keys, 2 values
   const uint16_t* weight = nullptr;
   uint4 g[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  for (; p < passes; p += gridDim.y) {
-    uint4 w[2] = {ahead[0], ahead[1]};
-    if (p + static_cast<int>(gridDim.y) < passes) load(p + gridDim.y, ahead);
+  for (int stage = 0; p < passes; p += gridDim.y, stage = (stage + 1) % kStages) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    uint4 w[2] = {s_in[warp][stage][0][lane], s_in[warp][stage][1][lane]};
+    load(p + (kStages - 1) * gridDim.y, (stage + kStages - 1) % kStages);  // read a pass ago
     const int now = p < q_passes ? 0 : p < q_passes + kv_passes ? 1 : 2;
     const int h = (now == 0 ? p : now == 1 ? p - q_passes : p - q_passes - kv_passes) * kRowsAtOnce + group;
     if (now != kind) {
@@ -228,6 +250,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 3) append_kernel(const Appe
       if (mine[k] && h < (kind == 0 ? P.q_heads : C.heads))
         *reinterpret_cast<uint4*>(to + piece[k] * 8) = w[k];
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <class E>
