@@ -41,24 +41,7 @@ _i64 = ctypes.c_int64
 _f = ctypes.c_float
 
 
-class CacheArg(ctypes.Structure):
-    """specv_cache of the header."""
-    _fields_ = [("k", _vp), ("v", _vp), ("page_table", _vp), ("lens", _vp),
-                ("layer_stride", _i64), ("page_stride", _i64), ("row_stride", _i64),
-                ("head_stride", _i64), ("layers", ctypes.c_int32), ("pages", ctypes.c_int32),
-                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
-                ("table_stride", ctypes.c_int32), ("heads", ctypes.c_int32),
-                ("head_dim", ctypes.c_int32), ("dtype", _i)]
-
-
-class RowsArg(ctypes.Structure):
-    """specv_rows of the header."""
-    _fields_ = [("data", _vp), ("batch_stride", _i64), ("node_stride", _i64),
-                ("head_stride", _i64)]
-
-
-_pc = ctypes.POINTER(CacheArg)
-_pr = ctypes.POINTER(RowsArg)
+_bytes = ctypes.c_char_p  # a struct of the header, packed
 _VERIFY_ARGS = [_vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _sz]
 SIGNATURES = {
     "specv_version": (_i, []),
@@ -83,11 +66,11 @@ SIGNATURES = {
     "spec_verify_tree_greedy": (_i, [_vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _sz,
                                      _vp, _vp]),
     "spec_insert_accepted": (_i, [_vp, _vp, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp]),
-    "spec_append_nodes": (_i, [_pc, _pr, _pr, _pr, _vp, _vp, _i, _i, _i, _vp, _vp, _f, _vp, _i, _i,
-                               _f, _pr, _vp, _vp]),
+    "spec_append_nodes": (_i, [_bytes, _bytes, _bytes, _bytes, _vp, _vp, _i, _i, _i, _vp, _vp, _f,
+                               _vp, _i, _i, _f, _bytes, _vp, _vp]),
     "specv_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
-    "spec_tree_attention": (_i, [_pc, _pr, _vp, _vp, _i, _i, _i, _f, _pr, _vp, _vp, _sz, _vp]),
-    "spec_keep_path": (_i, [_pc, _vp, _vp, _i, _i, _vp, _vp, _vp]),
+    "spec_tree_attention": (_i, [_bytes, _bytes, _vp, _vp, _i, _i, _i, _f, _bytes, _vp, _vp, _sz, _vp]),
+    "spec_keep_path": (_i, [_bytes, _vp, _vp, _i, _i, _vp, _vp, _vp]),
     "spec_process_logits": (_i, [_vp, _i64, _i64, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i64, _i, _vp,
                                  _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i64, _i64, _vp, _vp]),
 }

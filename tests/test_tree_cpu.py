@@ -1,7 +1,9 @@
 """The operators on a drafted tree without a GPU: what the entry points refuse
 before they touch the device, and the plain forms the GPU tests compare with."""
 
-import ctypes
+import os
+import struct
+import subprocess
 
 import numpy as np
 import pytest
@@ -10,7 +12,6 @@ torch = pytest.importorskip("torch")
 
 import speculative_decoding_verify_sample_gb300 as sv  # noqa: E402
 import tree_reference as ref  # noqa: E402
-from speculative_decoding_verify_sample_gb300 import _native  # noqa: E402
 
 FAKE = 0x10000  # a 64 KB-aligned non-null address: host checks never dereference it
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
@@ -27,11 +28,11 @@ def cache(**over):
              row_stride=128, head_stride=64, layers=1, pages=9, page_size=16, max_pages=4,
              table_stride=4, heads=2, head_dim=64, dtype=1)
     a.update(over)
-    return _native.CacheArg(*[a[n] for n, _ in _native.CacheArg._fields_])
+    return struct.pack("@4P4q8i", *[x or 0 for x in a.values()])  # specv_cache
 
 
 def rows(data=FAKE, b=64 * 32, n=64 * 8, h=64):
-    return _native.RowsArg(data, b, n, h)
+    return struct.pack("@P3q", data or 0, b, n, h)  # specv_rows
 
 
 BAD_CACHES = [
@@ -148,9 +149,19 @@ def test_attention_workspace_sizes(L):
         sv.AttentionWorkspace(1, 65, 8, 8, 128)
 
 
-def test_struct_layout_matches_the_header(L):
-    assert ctypes.sizeof(_native.CacheArg) == 4 * 8 + 4 * 8 + 8 * 4
-    assert ctypes.sizeof(_native.RowsArg) == 32
+def test_struct_layouts_match_the_header(tmp_path):
+    """The packed bytes are the header's structs: sizes and offsets by the C compiler."""
+    probe = tmp_path / "probe.c"
+    probe.write_text('#include <stdio.h>\n#include "specverify.h"\n'
+                     'int main(void) { printf("%zu %zu %zu %zu %zu", sizeof(specv_cache), '
+                     'offsetof(specv_cache, layer_stride), offsetof(specv_cache, layers), '
+                     'offsetof(specv_cache, dtype), sizeof(specv_rows)); return 0; }')
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "probe")
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(probe), "-o", exe], check=True)
+    said = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    assert said == [struct.calcsize("@4P4q8i"), struct.calcsize("@4P"), struct.calcsize("@4P4q"),
+                    struct.calcsize("@4P4q7i"), struct.calcsize("@P3q")]
 
 
 def _tensors(B=2, N=3, Hq=4, Hkv=2, D=64, page=16, P=3, dtype=torch.bfloat16):
