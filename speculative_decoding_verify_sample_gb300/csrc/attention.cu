@@ -34,9 +34,14 @@ constexpr int kKeys = 128;     // keys of a tile
 constexpr int kRows = 128;     // query rows of a stream
 constexpr int kMaxCtas = 152;  // SMs of a GB300
 constexpr int kLoadWarps = 4;
-constexpr int kSoftmaxThreads = 256;
-constexpr int kMmaWarp = 8;
-constexpr int kThreads = kSoftmaxThreads + 32 + 32 * kLoadWarps;
+constexpr int kLoadWarp = 8;  // the first of them
+constexpr int kMmaWarp = 12;  // the last three warps of its warpgroup have no work
+constexpr int kThreads = 512;
+// Registers a thread of each warpgroup: 2 * 200 + 64 + 48 = 512 = 4 * 128, what
+// the block is launched with.  The softmax keeps a row of scores in them.
+#define SPECV_REGS_SOFTMAX "200"
+#define SPECV_REGS_LOAD "64"
+#define SPECV_REGS_MMA "48"
 constexpr float kRise = 8.0f;  // log2 of how far a maximum may rise before O is rescaled
 
 // ----------------------------------------------------------------- prepare
@@ -133,7 +138,7 @@ __device__ __forceinline__ uint64_t now_ns() {
 // Waits for a phase, two seconds at most: then, and from then on in the whole
 // CTA, nothing waits any more.  The roles run their loops out (every address
 // they form is in bounds whatever the data), and the request is flagged.
-__device__ __noinline__ void barrier_wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+__device__ __forceinline__ void barrier_wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   const uint64_t start = now_ns();
   while (!barrier_try(bar, parity)) {
     if (*gave_up) return;
@@ -199,28 +204,53 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 #define SPECV_R8(x, i)                                                                   \
   "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]),            \
       "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define SPECV_R32(x, i) \
+  SPECV_R8(x, i), SPECV_R8(x, i + 8), SPECV_R8(x, i + 16), SPECV_R8(x, i + 24)
 #define SPECV_I8(x, i)                                                                   \
   "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]),  \
       "r"(x[i + 6]), "r"(x[i + 7])
 
-// 32 columns of this warp's 32 lanes: a register to a column.
+// 32 columns of this warp's 32 lanes, a register to a column, waited for.
 __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&x)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
       "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
       "tcgen05.wait::ld.sync.aligned;"
-      : SPECV_R8(x, 0), SPECV_R8(x, 8), SPECV_R8(x, 16), SPECV_R8(x, 24)
+      : SPECV_R32(x, 0)
       : "r"(at)
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&x)[32]) {
+// 128 columns, waited for.
+__device__ __forceinline__ void tmem_load128(uint32_t at, uint32_t (&x)[128]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-      "%24,%25,%26,%27,%28,%29,%30,%31};" ::SPECV_I8(x, 0),
-      SPECV_I8(x, 8), SPECV_I8(x, 16), SPECV_I8(x, 24), "r"(at)
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+      "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SPECV_R32(x, 0), SPECV_R32(x, 32), SPECV_R32(x, 64), SPECV_R32(x, 96)
+      : "r"(at), "r"(at + 32), "r"(at + 64), "r"(at + 96)
+      : "memory");
+}
+
+// 16 columns, waited for.
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SPECV_R8(x, 0), SPECV_R8(x, 8)
+      : "r"(at)
       : "memory");
 }
 
@@ -234,6 +264,28 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&x)[16
 
 __device__ __forceinline__ void tmem_store_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Two 32-bit operations in one instruction, each rounded as by itself.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(lo), "r"(hi));
+  return p;
+}
+__device__ __forceinline__ float2 halves_of(uint64_t p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 __device__ __forceinline__ float exp2_of(float x) {
@@ -264,7 +316,8 @@ template <int DP, bool kPair> struct Shape {
 };
 
 struct Tail {
-  uint64_t kv_full[10], kv_empty[10], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t kv_full[10], kv_empty[10], q_full[2], q_empty[2], s_full[2], o_full[2];
+  uint64_t p_full[2][2];   // by stream and half of the keys
   uint64_t odd_values[2];  // nodes whose values were not finite, by parity of the item
   int64_t base;            // work units before request `first`
   int64_t total;
@@ -347,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       barrier_init(smem_of(&s.q_full[i]), 32 * kLoadWarps);
       barrier_init(smem_of(&s.q_empty[i]), 1);
       barrier_init(smem_of(&s.s_full[i]), 1);
-      barrier_init(smem_of(&s.p_full[i]), 4);
+      barrier_init(smem_of(&s.p_full[i][0]), 4);
+      barrier_init(smem_of(&s.p_full[i][1]), 4);
       barrier_init(smem_of(&s.o_full[i]), 1);
       s.odd_values[i] = 0;
     }
@@ -409,24 +463,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
   const uint32_t tO[2] = {tmem + 256, tmem + 256 + DP};
   volatile int* gave_up = &s.gave_up;
 
-  if (warp > kMmaWarp) {
+  if (warp >= kLoadWarp && warp < kMmaWarp) {
     // ------------------------------------------------------------- copies
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_REGS_LOAD ";");
     // Copies of 16 bytes, so that pages of any size and strides of any kind will
     // do; places without a key (behind the last, past the head) become 0.
     constexpr int kPieces = DP / 8;            // 16-byte pieces of a row
     constexpr int kRowsAtOnce = 32 / kPieces;  // rows of one warp instruction
-    const int lw = warp - kMmaWarp - 1, piece = lane % kPieces, sub = lane / kPieces;
+    const int lw = warp - kLoadWarp, piece = lane % kPieces, sub = lane / kPieces;
     const bool inside = piece * 8 < C.head_dim;
     uint32_t job = 0, item = 0;
-    auto tile_copy = [&](uint32_t to, const uint16_t* from, int64_t off, bool real) {
-      // this lane's row is 32 lw + lane of the tile, at from + off
+    // 128-byte rows, their 16-byte pieces swapped by the row's number: rows
+    // kRowsAtOnce apart, and sub < kRowsAtOnce, so r and sub set bits of their own
+    const uint32_t lane_at = (piece / 8) * (kKeys * 128) + (32 * lw + sub) * 128;
+    const uint32_t swap = (piece % 8) ^ sub;
+    auto tile_copy = [&](uint32_t to, const uint16_t* from, int64_t off) {
+      // this lane's row is 32 lw + lane of the tile, at from + off (off < 0: none)
 #pragma unroll
       for (int r = 0; r < 32; r += kRowsAtOnce) {
         const int64_t o = __shfl_sync(kFullMask, off, r + sub);
-        const bool ok = __shfl_sync(kFullMask, real, r + sub);
-        const int row = 32 * lw + r + sub;
-        copy16(to + (piece / 8) * (kKeys * 128) + row * 128 + ((piece % 8) ^ (row % 8)) * 16,
-               from + (ok && inside ? o + piece * 8 : 0), ok && inside);
+        const bool ok = o >= 0 && inside;
+        copy16(to + lane_at + r * 128 + (swap ^ (r % 8)) * 16, from + (ok ? o + piece * 8 : 0), ok);
       }
     };
     while (w.next(P)) {
@@ -441,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         const int node = at / P.group, g = at - node * P.group;
         const int64_t off = w.b * P.q.batch_stride + node * P.q.node_stride +
                             (w.h * P.group + g) * P.q.head_stride;
-        tile_copy(base + (kPair ? half : q_buffer) * S::kTileBytes, P.q.data, off, real);
+        tile_copy(base + (kPair ? half : q_buffer) * S::kTileBytes, P.q.data, real ? off : -1);
       }
       copies_arrive(smem_of(&s.q_full[q_buffer]));
       item++;
@@ -457,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         for (int kv = 0; kv < 2; kv++, job++) {
           const uint32_t stage = job % kStages, use = job / kStages;
           barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
-          tile_copy(base + S::kStageAt + stage * S::kTileBytes, kv ? C.v : C.k, off, off >= 0);
+          tile_copy(base + S::kStageAt + stage * S::kTileBytes, kv ? C.v : C.k, off);
           copies_arrive(smem_of(&s.kv_full[stage]));
           if (kv == 0 && t + 1 < w.t1) next = offset_of(t + 1);
         }
@@ -471,13 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       barrier_wait(smem_of(&s.q_empty[kPair ? 0 : item & 1]), ((kPair ? item : item / 2) & 1) ^ 1,
                    gave_up);
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // --------------------------------------------------------------- MMAs
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_REGS_MMA ";");
     constexpr uint32_t kType = std::is_same<E, Bf16>::value ? 1 : 0;
     constexpr uint32_t kIdesc = 1u << 4 | kType << 7 | kType << 10 | (kRows >> 4) << 24;
     constexpr uint32_t kIdescS = kIdesc | (kKeys >> 3) << 17;
     constexpr uint32_t kIdescO = kIdesc | 1u << 16 | (DP >> 3) << 17;
-    if (lane == 0) {
+    if (warp == kMmaWarp && lane == 0) {
       const int steps = (C.head_dim + 15) / 16;
       uint32_t tile = 0, item = 0;       // key tiles and items so far
       uint32_t weighted[2] = {0, 0};  // O updates of each stream so far
@@ -495,12 +553,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         mma_commit(smem_of(&s.s_full[st]));
       };
       auto pv = [&](int st, uint32_t v_at, bool first) {
-        barrier_wait(smem_of(&s.p_full[st]), weighted[st] & 1, gave_up);
-        tmem_fence_after();
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; k++)
-          mma_ts(tO[st], tS[st] + 8 * k, operand(v_at + k * 2048, kKeys * 128), kIdescO,
-                 !first || k > 0);
+        for (int half = 0; half < 2; half++) {
+          barrier_wait(smem_of(&s.p_full[st][half]), weighted[st] & 1, gave_up);
+          tmem_fence_after();
+#pragma unroll
+          for (int k = half * kKeys / 32; k < (half + 1) * kKeys / 32; k++)
+            mma_ts(tO[st], tS[st] + 8 * k, operand(v_at + k * 2048, kKeys * 128), kIdescO,
+                   !first || k > 0);
+        }
         mma_commit(smem_of(&s.o_full[st]));
         weighted[st]++;
       };
@@ -570,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 " SPECV_REGS_SOFTMAX ";");
     const int st = warp / 4, quarter = warp % 4;
     const int row = quarter * 32 + lane;  // of the stream's tile
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -633,25 +695,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         tmem_fence_after();
         const bool first = taken[st] == 1;
         if (working) {
-          uint32_t seen[4];
+          uint32_t x[kKeys];
+          tmem_load128(tS[st] + lanes, x);
+          if (mixed) {
 #pragma unroll
-          for (int k = 0; k < 4; k++)
-            seen[k] = mixed ? seen_of(t * kKeys + 32 * k - w.len, visible) : ~0u;
-          float top = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 4; k++) {
-            uint32_t x[32];
-            tmem_load32(tS[st] + lanes + 32 * k, x);
-            if (mixed) {
+            for (int k = 0; k < kKeys; k += 32) {
+              const uint32_t seen = seen_of(t * kKeys + k - w.len, visible);
 #pragma unroll
               for (int e = 0; e < 32; e++)
-                if (seen[k] >> e & 1) top = fmaxf(top, __uint_as_float(x[e]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e++) top = fmaxf(top, __uint_as_float(x[e]));
+                if (!(seen >> e & 1)) x[k + e] = 0xff800000u;  // -inf
             }
           }
-          top *= c;
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < kKeys; e += 8)
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+              tops[k] = fmaxf(fmaxf(tops[k], __uint_as_float(x[e + 2 * k])),
+                              __uint_as_float(x[e + 2 * k + 1]));
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * c;
           const bool rise = first || top > m + kRise;
           float by = 1.0f;
           if (rise) {
@@ -665,43 +727,48 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             __syncwarp();
             tmem_fence_after();
             l *= by;
+#pragma unroll 1
+            for (int k = 0; k < DP; k += 16) {
+              uint32_t o[16];
+              tmem_load16(tO[st] + lanes + k, o);
 #pragma unroll
-            for (int k = 0; k < DP; k += 32) {
-              uint32_t x[32];
-              tmem_load32(tO[st] + lanes + k, x);
-#pragma unroll
-              for (int e = 0; e < 32; e++) x[e] = __float_as_uint(__uint_as_float(x[e]) * by);
-              tmem_store32(tO[st] + lanes + k, x);
+              for (int e = 0; e < 16; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+              tmem_store16(tO[st] + lanes + k, o);
             }
           }
-          const float shift = (m == -INFINITY ? 0.0f : m) - kLift;
-          float sum[2] = {0.0f, 0.0f};
+          const float shift = kLift - (m == -INFINITY ? 0.0f : m);
+          const uint64_t c2 = pair_of(__float_as_uint(c), __float_as_uint(c));
+          const uint64_t shift2 = pair_of(__float_as_uint(shift), __float_as_uint(shift));
+          uint64_t sums[2] = {0, 0};
 #pragma unroll
-          for (int k = 0; k < 4; k++) {
-            uint32_t x[32], p[16];
-            tmem_load32(tS[st] + lanes + 32 * k, x);
+          for (int k = 0; k < kKeys; k += 32) {
+            uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              float a = exp2_of(fmaf(__uint_as_float(x[e]), c, -shift));
-              float b = exp2_of(fmaf(__uint_as_float(x[e + 1]), c, -shift));
-              if (mixed) {
-                a = seen[k] >> e & 1 ? a : 0.0f;
-                b = seen[k] >> (e + 1) & 1 ? b : 0.0f;
-              }
-              sum[0] += a;
-              sum[1] += b;
+              const float2 y = halves_of(fma2(pair_of(x[k + e], x[k + e + 1]), c2, shift2));
+              const float a = exp2_of(y.x), b = exp2_of(y.y);
+              sums[e / 2 % 2] =
+                  add2(sums[e / 2 % 2], pair_of(__float_as_uint(a), __float_as_uint(b)));
               // the weights' one rounding, to the type of the values they meet
               p[e / 2] = E::pack(a, b);
             }
-            // over scores of this row that are read already
-            tmem_store16(tS[st] + lanes + 16 * k, p);
+            tmem_store16(tS[st] + lanes + k / 2, p);  // over scores of this row, all read
+            if (k == kKeys / 2 - 32) {  // half of the keys can be summed up
+              tmem_store_wait();
+              tmem_fence_before();
+              __syncwarp();
+              if (lane == 0) barrier_arrive(smem_of(&s.p_full[st][0]));
+            }
           }
-          l += sum[0] + sum[1];
+          const float2 sum = halves_of(add2(sums[0], sums[1]));
+          l += sum.x + sum.y;
           tmem_store_wait();
+        } else if (lane == 0) {
+          barrier_arrive(smem_of(&s.p_full[st][0]));
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) barrier_arrive(smem_of(&s.p_full[st]));
+        if (lane == 0) barrier_arrive(smem_of(&s.p_full[st][1]));
         scores[st]++;
       }
 
@@ -746,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         const int64_t part = static_cast<int64_t>(slot) * S::kRowTile + first_row + row;
         constexpr int kCols = kPair ? DP : DP / 2;
         const int col0 = kPair ? 0 : st * kCols;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < kCols; k += 32) {
           float o[32];
           uint32_t x[32];

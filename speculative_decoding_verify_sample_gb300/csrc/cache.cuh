@@ -176,7 +176,9 @@ __device__ __forceinline__ bool bad_pages(const Cache& c, int b, int first, int 
 
 inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-inline bool strides_ok(int64_t a, int64_t b, int64_t c) { return a % 8 == 0 && b % 8 == 0 && c % 8 == 0; }
+inline bool strides_ok(int64_t a, int64_t b, int64_t c) {
+  return a >= 0 && b >= 0 && c >= 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
+}
 
 // The documented limits of a cache for B requests of N nodes.
 inline specv_status check_cache(const specv_cache* c, int B, int N) {
