@@ -503,22 +503,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       copies_arrive(smem_of(&s.q_full[q_buffer]));
       item++;
       const int keys = w.len + w.n;
-      auto offset_of = [&](int t) {
-        const int key = t * kKeys + 32 * lw + lane;
-        return key < keys ? C.slot(w.b, key) + w.h * C.head_stride : static_cast<int64_t>(-1);
+      // A lane's key of a tile: its page's number is read a tile ahead of its use.
+      const int32_t* table = C.page_table + static_cast<int64_t>(w.b) * C.table_stride;
+      auto key_of = [&](int t) { return t * kKeys + 32 * lw + lane; };
+      auto page_of = [&](int t) {
+        const int key = key_of(t);
+        return t < w.t1 && key < keys ? table[key / C.page_size] : -1;
       };
-      int64_t off = offset_of(w.t0);
+      int page = page_of(w.t0), page_next = page_of(w.t0 + 1);
       for (int t = w.t0; t < w.t1; t++) {
-        int64_t next = -1;
+        const int64_t off = page < 0 ? static_cast<int64_t>(-1)
+                                     : page * C.page_stride +
+                                           key_of(t) % C.page_size * C.row_stride +
+                                           w.h * C.head_stride;
+        page = page_next;
+        page_next = page_of(t + 2);
 #pragma unroll
         for (int kv = 0; kv < 2; kv++, job++) {
           const uint32_t stage = job % kStages, use = job / kStages;
           barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
           tile_copy(base + S::kStageAt + stage * S::kTileBytes, kv ? C.v : C.k, off);
           copies_arrive(smem_of(&s.kv_full[stage]));
-          if (kv == 0 && t + 1 < w.t1) next = offset_of(t + 1);
         }
-        off = next;
       }
     }
     // The MMAs' last arrivals must find this CTA's shared memory.
