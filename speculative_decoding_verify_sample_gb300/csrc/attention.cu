@@ -172,26 +172,31 @@ __device__ __forceinline__ void tmem_fence_after() {
 }
 
 // Shared-memory operand with 128-byte swizzle: rows of 128 bytes, eight of
-// them a 1024-byte group.  `lead` is the distance of the next 64 columns where
-// the operand's contiguous dimension is not the summed one.
-__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
-  return static_cast<uint64_t>((at & 0x3ffff) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 |
-         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// them a 1024-byte group.  The low word holds the address and `lead`, the
+// distance of the next 64 columns where the operand's contiguous dimension is
+// not the summed one; a step along the operand is an addition to it.
+__device__ __forceinline__ uint32_t operand_low(uint32_t at, uint32_t lead) {
+  return (at & 0x3ffff) >> 4 | (lead >> 4) << 16;
 }
+constexpr uint32_t kOperandHigh = 1024 >> 4 | 1u << 14 | 2u << 29;
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+template <bool kAdd>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n .reg .b64 a, b;\n .reg .pred p;\n"
+      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n setp.ne.u32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}" ::"r"(d),
+      "r"(a_low), "r"(b_low), "r"(kOperandHigh), "r"(idesc), "n"(kAdd ? 1 : 0)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_low, uint32_t idesc,
+                                       uint32_t add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n .reg .b64 b;\n .reg .pred p;\n"
+      " mov.b64 b, {%2, %3};\n setp.ne.u32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}" ::"r"(d),
+      "r"(a), "r"(b_low), "r"(kOperandHigh), "r"(idesc), "r"(add)
       : "memory");
 }
 
@@ -552,21 +557,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       };
       auto qk = [&](int st, uint32_t q_at, uint32_t k_at) {
-        for (int k = 0; k < steps; k++) {
-          const uint32_t at = (k / 4) * (kKeys * 128) + (k % 4) * 32;
-          mma_ss(tS[st], operand(q_at + at, 16), operand(k_at + at, 16), kIdescS, k > 0);
+        const uint32_t a = operand_low(q_at, 16), b = operand_low(k_at, 16);
+        mma_ss<false>(tS[st], a, b, kIdescS);
+#pragma unroll
+        for (int k = 1; k < DP / 16; k++) {
+          const uint32_t step = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
+          if (k < steps) mma_ss<true>(tS[st], a + step, b + step, kIdescS);
         }
         mma_commit(smem_of(&s.s_full[st]));
       };
       auto pv = [&](int st, uint32_t v_at, bool first) {
+        const uint32_t b = operand_low(v_at, kKeys * 128);
 #pragma unroll
         for (int half = 0; half < 2; half++) {
           barrier_wait(smem_of(&s.p_full[st][half]), weighted[st] & 1, gave_up);
           tmem_fence_after();
 #pragma unroll
           for (int k = half * kKeys / 32; k < (half + 1) * kKeys / 32; k++)
-            mma_ts(tO[st], tS[st] + 8 * k, operand(v_at + k * 2048, kKeys * 128), kIdescO,
-                   !first || k > 0);
+            mma_ts(tO[st], tS[st] + 8 * k, b + (k * 2048 >> 4), kIdescO, k > 0 || !first);
         }
         mma_commit(smem_of(&s.o_full[st]));
         weighted[st]++;
