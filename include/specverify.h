@@ -439,9 +439,11 @@ size_t specv_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, 
  * rounded to the cache's dtype before the product with the values.
  *   q, out    [B, N, q_heads, head_dim]; q_heads a multiple of cache->heads.
  *   scale     > 0 and finite (1/sqrt(head_dim) as a rule).
- *   workspace specv_attention_workspace_bytes bytes, 256-byte aligned.  It
- *             needs no initialisation and keeps nothing between calls; calls
- *             that may run at the same time need one each.
+ *   workspace specv_attention_workspace_bytes bytes, 256-byte aligned, its
+ *             first 256 bytes zeroed once with specv_workspace_init (every
+ *             call leaves them ready for the next).  Calls that may run at
+ *             the same time need one each.
+ * Enqueues two kernels, the second as a programmatic dependent launch.
  */
 specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
                                  const int32_t* parents, const int32_t* n_nodes, int B, int N,

@@ -12,15 +12,20 @@
 // and O is rescaled only when the maximum has risen by more than 2^8, which
 // no result shows: m is whatever both O and the sum l were taken with.
 //
-// The work is the list of (request, key head, row tile, 128-key tile), cut
-// into equal runs, one to a CTA and a CTA to an SM, so ragged lengths and few
-// requests fill the machine alike.  A row tile whose keys one CTA has whole is
-// written out; pieces leave (m, l, O) in the workspace for combine_kernel.
+// The work is the list of (request, key head, row tile, 128-key tile), a unit
+// each, cut into runs: one for every CTA (one to an SM), and the rest in short
+// runs that the CTAs take off a counter as they finish, for equal runs do not
+// take equal time (with 80 units each, 121 to 172 us).  A row tile whose keys
+// one run has whole is written out; pieces leave (m, l, O) in the workspace for
+// finish_kernel.
 //
 // Two streams share an SM, each with its S and O in TMEM and its four softmax
 // warps: with up to 128 rows they take the key tiles in turn and are joined
 // at the end (kPair false), with more they are two row tiles on the same keys
-// (kPair true).  One thread issues the MMAs, four warps the copies.
+// (kPair true).  Of the other warps four copy, one thread issues the MMAs, one
+// warp deals out the work and two check the requests' data beside it all.
+
+#include <cuda.h>
 
 #include <type_traits>
 
@@ -35,72 +40,88 @@ constexpr int kRows = 128;     // query rows of a stream
 constexpr int kMaxCtas = 152;  // SMs of a GB300
 constexpr int kLoadWarps = 4;
 constexpr int kLoadWarp = 8;  // the first of them
-constexpr int kMmaWarp = 12;  // the last three warps of its warpgroup have no work
+constexpr int kMmaWarp = 12;
+constexpr int kDealWarp = 13;
+constexpr int kCheckWarp = 14;  // and 15
 constexpr int kThreads = 512;
-// Registers a thread of each warpgroup: 2 * 200 + 64 + 48 = 512 = 4 * 128, what
+constexpr int kItems = 4;  // items dealt out ahead
+// Registers a thread of each warpgroup: 2 * 200 + 56 + 56 = 512 = 4 * 128, what
 // the block is launched with.  The softmax keeps a row of scores in them.
 #define SPECV_REGS_SOFTMAX "200"
-#define SPECV_REGS_LOAD "64"
-#define SPECV_REGS_MMA "48"
+#define SPECV_REGS_LOAD "56"
+#define SPECV_REGS_OTHER "56"
 constexpr float kRise = 8.0f;  // log2 of how far a maximum may rise before O is rescaled
 
-// ----------------------------------------------------------------- prepare
+// ---------------------------------------------------------------- the work
 
-constexpr int kPrepThreads = 128;
-
-// What the attention kernel reads of a request (0 nodes where it is flagged).
-struct Plan {
-  int32_t* len;       // [B] verified tokens
-  int32_t* nodes;     // [B]
-  uint64_t* visible;  // [B][kMaxNodes] bit j: node sees node j
-  int64_t* share;     // units of a CTA's run
-  int4* starts;       // [ctas] request, head, row tile and key tile where a CTA begins
-  float* parts;       // [2 ctas][rows][dim] pieces' O ...
-  float2* stats;      // [2 ctas][rows]      ... and their m c and l
+struct Header {
+  int32_t next;     // dealt runs so far; 0 between calls
+  int32_t timeout;  // a wait gave up in this call
+  int64_t total;    // units of this call
 };
 
-__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const Cache C, const int32_t* parents,
-                                                               const int32_t* n_nodes, int N,
-                                                               Plan plan, const Rows out,
-                                                               int q_heads, int32_t* status) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ int s_n, s_len, s_bad;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  Tree t;
-  if (tid < 32) {
-    t = read_tree(parents, n_nodes, C.lens, b, N, static_cast<int64_t>(C.max_pages) * C.page_size,
-                  lane);
-    if (lane == 0) {
-      s_n = t.n;
-      s_len = t.len;
-      s_bad = t.bad;
+// Where a run begins: the item, its key tile, and what the item is.
+struct Start {
+  int32_t b, h, row_tile, t0, tiles, n, pad[2];
+};
+
+struct Workspace {
+  Header* header;
+  int32_t* bad;   // [B] SPECV_DEV_* bits
+  Start* starts;  // [runs]
+  float2* stats;  // [2 runs][part_rows] pieces' m c and l: of an item that began before the
+  float* parts;   // [2 runs][part_rows][dim]   run, then of one that goes on behind it; their O
+};
+
+struct AttnParams {
+  Cache cache;
+  Rows q, out;
+  Workspace ws;
+  const int32_t* parents;
+  const int32_t* n_nodes;
+  int32_t* status;
+  int B, N, q_heads, group;  // group: query heads to a key head
+  int ctas, dealt;           // runs: one for each CTA, and at most `dealt` more
+  int part_rows;             // rows of a piece in the workspace
+  int box_rows;              // rows that one tensor copy brings; 0: copies of 16 bytes
+  float scale_log2;
+};
+
+// How the units are cut into runs.  Few units (under 8 for each CTA) are cut
+// evenly; of more, a share is cut evenly and the rest is dealt out.
+struct Runs {
+  int64_t total, even, dealt;  // lengths of the two kinds of runs
+  int ctas, count;
+
+  __device__ __forceinline__ Runs(const AttnParams& P, int64_t units) : total(units), ctas(P.ctas) {
+    even = (total + ctas - 1) / ctas;
+    dealt = 1;
+    if (total >= 8 * ctas && P.dealt > 0) {
+      // about 3/4 and, where pieces are small and more of them cost little, 3/5
+      even = P.dealt > ctas ? total * 3 / (5 * ctas) : total * 3 / (4 * ctas);
+      dealt = (total - even * ctas + P.dealt - 1) / P.dealt;
+      count = ctas + static_cast<int>((total - even * ctas + dealt - 1) / dealt);
+    } else {
+      count = total ? static_cast<int>((total + even - 1) / even) : 0;
     }
   }
-  __syncthreads();
-  const bool bad_page = !s_bad && bad_pages(C, b, 0, s_len + s_n, tid, kPrepThreads);
-  const bool any = __syncthreads_or(bad_page);
-  if (tid < 32) {
-    if (any) t.bad |= SPECV_DEV_BAD_CACHE;
-    if (!t.bad) {
-      uint64_t bits[2];
-      ancestors(t, lane, bits);
-      plan.visible[static_cast<int64_t>(b) * kMaxNodes + lane] = bits[0];
-      plan.visible[static_cast<int64_t>(b) * kMaxNodes + lane + 32] = bits[1];
-    }
-    if (lane == 0) {
-      plan.len[b] = t.bad ? 0 : t.len;
-      plan.nodes[b] = t.bad ? 0 : t.n;
-      status[b] = static_cast<int32_t>(t.bad);
-    }
+  __device__ __forceinline__ int64_t start(int run) const {
+    return run < ctas ? run * even : ctas * even + (run - ctas) * dealt;
   }
-  if (s_bad || any) {  // a flagged request's rows become 0
-    const int n = s_n ? s_n : N, words = C.head_dim / 8;
-    for (int e = tid; e < n * q_heads * words; e += kPrepThreads) {
-      const int i = e / (q_heads * words), h = e / words % q_heads, d = e % words * 8;
-      *reinterpret_cast<uint4*>(out.data + b * out.batch_stride + i * out.node_stride +
-                                h * out.head_stride + d) = make_uint4(0, 0, 0, 0);
-    }
+  __device__ __forceinline__ int64_t length(int run) const {
+    return min(run < ctas ? even : dealt, total - start(run));
   }
+};
+
+// Nodes of request b, 0 where its count or length is out of range.
+__device__ __forceinline__ int nodes_of(const AttnParams& P, int b, int& len) {
+  const int n = P.n_nodes ? P.n_nodes[b] : P.N;
+  len = P.cache.lens[b];
+  const int64_t slots = static_cast<int64_t>(P.cache.max_pages) * P.cache.page_size;
+  return n < 1 || n > P.N || len < 0 || len > INT_MAX - 4 * kMaxNodes ||
+                 static_cast<int64_t>(len) + n > slots
+             ? 0
+             : n;
 }
 
 // ------------------------------------------------------------- PTX wrappers
@@ -153,10 +174,31 @@ __device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, vola
   if (!barrier_try(bar, parity)) barrier_wait_slow(bar, parity, gave_up);
 }
 
+// Waits for this thread's own work in flight, a second at most, whatever gave up.
+__device__ __forceinline__ void barrier_wait_own(uint32_t bar, uint32_t parity) {
+  const uint64_t start = now_ns();
+  while (!barrier_try(bar, parity) && now_ns() - start < 1000000000ull) {
+  }
+}
+
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
                "r"(real ? 16 : 0)
                : "memory");
+}
+
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void tensor_copy(uint32_t to, const CUtensorMap* map, int d, int row,
+                                            int head, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
+      "l"(map), "r"(d), "r"(row), "r"(head), "r"(page), "r"(bar)
+      : "memory");
 }
 
 // Arrives on the barrier when this thread's copies so far have landed.
@@ -293,6 +335,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// Whether it holds for one of the 256 threads of the softmax, which wait for one another.
+__device__ __forceinline__ bool any_of_softmax(bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " barrier.cta.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return any;
+}
+
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -300,15 +354,6 @@ __device__ __forceinline__ float exp2_of(float x) {
 }
 
 // --------------------------------------------------------------- attention
-
-struct AttnParams {
-  Cache cache;
-  Rows q, out;
-  Plan plan;
-  int32_t* status;
-  int B, q_heads, group;  // group: query heads to a key head
-  float scale_log2;
-};
 
 template <int DP, bool kPair> struct Shape {
   static constexpr int kTileBytes = kKeys * DP * 2;  // of keys, of values or of queries
@@ -320,60 +365,38 @@ template <int DP, bool kPair> struct Shape {
   static constexpr int kTailAt = kStageAt + kStages * kTileBytes;
 };
 
-struct Tail {
-  uint64_t kv_full[10], kv_empty[10], q_full[2], q_empty[2], s_full[2], o_full[2];
-  uint64_t p_full[2][2];   // by stream and half of the keys
+// All key tiles t0 .. t1-1 of a row tile that one run has.
+struct Item {
+  int32_t b, h, row_tile, t0, t1, tiles, len, n, run;  // t0 < 0: no more items
+  uint8_t parents[kMaxNodes];                          // each below its node, whatever the input
+
+  __device__ __forceinline__ int rows(int group, int row_tile_rows) const {
+    return n * group - row_tile * row_tile_rows;
+  }
+};
+
+template <int kStages> struct Tail {
+  uint64_t kv_full[kStages], kv_empty[kStages], q_full[2], q_empty[2], s_full[2], o_full[2];
+  uint64_t p_full[2][2];  // by stream and half of the keys
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t drained;
   uint64_t odd_values[2];  // nodes whose values were not finite, by parity of the item
-  int64_t base;            // work units before request `first`
-  int64_t total;
-  int first;
+  unsigned long long total;
   int gave_up;
   uint32_t tmem;
+  Item items[kItems];
   float2 stats[2][kRows];
 };
 
 // The work units (128-key tiles of a row tile of a key head) of request b.
 template <int kRowTile>
-__device__ __forceinline__ int64_t units_of(const AttnParams& P, int b, int& tiles, int& row_tiles) {
-  const int n = P.plan.nodes[b];
-  tiles = n ? (P.plan.len[b] + n + kKeys - 1) / kKeys : 0;
+__device__ __forceinline__ int64_t units_of(const AttnParams& P, int b, int& tiles, int& row_tiles,
+                                            int& len, int& n) {
+  n = nodes_of(P, b, len);
+  tiles = n ? (len + n + kKeys - 1) / kKeys : 0;
   row_tiles = (n * P.group + kRowTile - 1) / kRowTile;
   return static_cast<int64_t>(tiles) * row_tiles * P.cache.heads;
 }
-
-// A CTA's run of units, item by item (an item: all key tiles of a row tile).
-template <int kRowTile> struct Walk {
-  int64_t at, end, base, units;
-  int b, tiles, row_tiles;
-  // the current item, and which of its key tiles are this CTA's
-  int h, row_tile, t0, t1, len, n;
-
-  __device__ __forceinline__ void start(const AttnParams& P, const Tail& s, int64_t share) {
-    at = static_cast<int64_t>(blockIdx.x) * share;
-    end = min(at + share, s.total);
-    b = s.first;
-    base = s.base;
-    if (at < end) units = units_of<kRowTile>(P, b, tiles, row_tiles);
-  }
-  __device__ __forceinline__ bool next(const AttnParams& P) {
-    if (at >= end) return false;
-    while (at >= base + units) {
-      base += units;
-      units = units_of<kRowTile>(P, ++b, tiles, row_tiles);
-    }
-    const int64_t off = at - base;
-    const int64_t item = off / tiles;
-    t0 = static_cast<int>(off - item * tiles);
-    h = static_cast<int>(item / row_tiles);
-    row_tile = static_cast<int>(item - static_cast<int64_t>(h) * row_tiles);
-    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (end - at)));
-    len = P.plan.len[b];
-    n = P.plan.nodes[b];
-    at += t1 - t0;
-    return true;
-  }
-  __device__ __forceinline__ int rows(int group) const { return n * group - row_tile * kRowTile; }
-};
 
 // Bits of the 32 columns from `first` (a key's number less len): which of them
 // a row sees whose nodes are `visible`.
@@ -384,21 +407,24 @@ __device__ __forceinline__ uint32_t seen_of(int first, uint64_t visible) {
 }
 
 template <class E, int DP, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams P) {
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_kernel(const AttnParams P, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map) {
   using S = Shape<DP, kPair>;
   constexpr int kStages = S::kStages;
   // weights in f16 go below 2^-14, where its steps stop shrinking: taken 2^7 larger
   // they reach 2^15 at most (2^kRise more than the maximum's)
   constexpr float kLift = std::is_same<E, F16>::value ? 7.0f : 0.0f;
   extern __shared__ __align__(1024) char smem[];
-  Tail& s = *reinterpret_cast<Tail*>(smem + S::kTailAt);
+  Tail<kStages>& s = *reinterpret_cast<Tail<kStages>*>(smem + S::kTailAt);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   const uint32_t base = smem_of(smem);
   const Cache& C = P.cache;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int i = 0; i < kStages; i++) {
-      barrier_init(smem_of(&s.kv_full[i]), 32 * kLoadWarps);
+      barrier_init(smem_of(&s.kv_full[i]), P.box_rows ? 1 : 32 * kLoadWarps);
       barrier_init(smem_of(&s.kv_empty[i]), 1);
     }
     for (int i = 0; i < 2; i++) {
@@ -410,10 +436,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       barrier_init(smem_of(&s.o_full[i]), 1);
       s.odd_values[i] = 0;
     }
+    for (int i = 0; i < kItems; i++) {
+      barrier_init(smem_of(&s.item_full[i]), 1);
+      barrier_init(smem_of(&s.item_empty[i]), kLoadWarps + 1 + 8);
+    }
+    barrier_init(smem_of(&s.drained), 1);
     s.gave_up = 0;
-    s.first = 0;
-    s.base = 0;
     s.total = 0;
+    if (blockIdx.x == 0) P.ws.header->timeout = 0;  // set two seconds from now at the earliest
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -422,51 +452,34 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  int64_t mine = 0;
+  for (int b = tid; b < P.B; b += kThreads) {
+    int tiles, row_tiles, len, n;
+    mine += units_of<S::kRowTile>(P, b, tiles, row_tiles, len, n);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) mine += __shfl_xor_sync(kFullMask, mine, o);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
+  if (lane == 0 && mine) atomicAdd(&s.total, static_cast<unsigned long long>(mine));
+  __syncthreads();
   const uint32_t tmem = s.tmem;
-
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-  // Where this CTA's run begins: the units of all requests, then the request
-  // that holds the first of this CTA's.
-  int64_t share;
-  {
-    int64_t mine = 0;
-    int tiles, row_tiles;
-    for (int b = tid; b < P.B; b += kThreads) mine += units_of<S::kRowTile>(P, b, tiles, row_tiles);
-    atomicAdd(reinterpret_cast<unsigned long long*>(&s.total), static_cast<unsigned long long>(mine));
-    __syncthreads();
-    share = (s.total + gridDim.x - 1) / gridDim.x;
-    const int64_t want = static_cast<int64_t>(blockIdx.x) * share;
-    if (warp == 0 && want < s.total) {
-      int64_t before = 0;
-      for (int b0 = 0; b0 < P.B; b0 += 32) {
-        const int64_t u =
-            b0 + lane < P.B ? units_of<S::kRowTile>(P, b0 + lane, tiles, row_tiles) : 0;
-        int64_t upto = u;
-        for (int o = 1; o < 32; o *= 2) {
-          const int64_t x = __shfl_up_sync(kFullMask, upto, o);
-          if (lane >= o) upto += x;
-        }
-        if (want >= before + upto - u && want < before + upto) {
-          s.first = b0 + lane;
-          s.base = before + upto - u;
-        }
-        before += __shfl_sync(kFullMask, upto, 31);
-        if (want < before) break;
-      }
-    }
-    __syncthreads();
-  }
-  Walk<S::kRowTile> w;
-  w.start(P, s, share);
-
   const uint32_t tS[2] = {tmem, tmem + 128};
   const uint32_t tO[2] = {tmem + 256, tmem + 256 + DP};
   volatile int* gave_up = &s.gave_up;
+  // The next item of this thread's warp; lane 0 gives it back when it is done.
+  uint32_t items = 0;
+  auto next_item = [&]() -> const Item& {
+    const uint32_t slot = items % kItems;
+    barrier_wait(smem_of(&s.item_full[slot]), items / kItems & 1, gave_up);
+    return s.items[slot];
+  };
+  auto done_item = [&]() {
+    if (lane == 0) barrier_arrive(smem_of(&s.item_empty[items % kItems]));
+    items++;
+  };
+  auto over = [&](const Item& w) { return w.t0 < 0 || *gave_up; };
 
   if (warp >= kLoadWarp && warp < kMmaWarp) {
     // ------------------------------------------------------------- copies
@@ -477,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     constexpr int kRowsAtOnce = 32 / kPieces;  // rows of one warp instruction
     const int lw = warp - kLoadWarp, piece = lane % kPieces, sub = lane / kPieces;
     const bool inside = piece * 8 < C.head_dim;
-    uint32_t job = 0, item = 0;
+    uint32_t job = 0;
     // 128-byte rows, their 16-byte pieces swapped by the row's number: rows
     // kRowsAtOnce apart, and sub < kRowsAtOnce, so r and sub set bits of their own
     const uint32_t lane_at = (piece / 8) * (kKeys * 128) + (32 * lw + sub) * 128;
@@ -491,14 +504,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         copy16(to + lane_at + r * 128 + (swap ^ (r % 8)) * 16, from + (ok ? o + piece * 8 : 0), ok);
       }
     };
-    while (w.next(P)) {
+    while (true) {
+      const uint32_t item = items;
+      const Item& w = next_item();
+      if (__any_sync(kFullMask, over(w))) break;
       const int q_buffer = kPair ? 0 : item & 1;
       const uint32_t q_use = kPair ? item : item / 2;
+      const int rows = w.rows(P.group, S::kRowTile);
       barrier_wait(smem_of(&s.q_empty[q_buffer]), (q_use & 1) ^ 1, gave_up);
 #pragma unroll
       for (int half = 0; half < (kPair ? 2 : 1); half++) {
         const int row = half * kRows + 32 * lw + lane;
-        const bool real = row < w.rows(P.group);
+        const bool real = row < rows;
         const int at = w.row_tile * S::kRowTile + (real ? row : 0);
         const int node = at / P.group, g = at - node * P.group;
         const int64_t off = w.b * P.q.batch_stride + node * P.q.node_stride +
@@ -506,55 +523,89 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         tile_copy(base + (kPair ? half : q_buffer) * S::kTileBytes, P.q.data, real ? off : -1);
       }
       copies_arrive(smem_of(&s.q_full[q_buffer]));
-      item++;
-      const int keys = w.len + w.n;
-      // A lane's key of a tile: its page's number is read a tile ahead of its use.
+      const int keys = w.len + w.n, t1 = w.t1;
       const int32_t* table = C.page_table + static_cast<int64_t>(w.b) * C.table_stride;
-      auto key_of = [&](int t) { return t * kKeys + 32 * lw + lane; };
-      auto page_of = [&](int t) {
-        const int key = key_of(t);
-        return t < w.t1 && key < keys ? table[key / C.page_size] : -1;
+      // Page numbers are read a tile ahead of their use; one out of range (its
+      // request is flagged elsewhere) is no page.
+      auto page_at = [&](int key) {
+        int page = -1;
+        if (key < keys) page = table[key / C.page_size];
+        return page < C.pages ? page : -1;
       };
-      int page = page_of(w.t0), page_next = page_of(w.t0 + 1);
-      for (int t = w.t0; t < w.t1; t++) {
-        const int64_t off = page < 0 ? static_cast<int64_t>(-1)
-                                     : page * C.page_stride +
-                                           key_of(t) % C.page_size * C.row_stride +
-                                           w.h * C.head_stride;
-        page = page_next;
-        page_next = page_of(t + 2);
+      if (P.box_rows) {
+        // Tensor copies: lane l < boxes brings box l % per_half of 64-column half
+        // l / per_half.  A page's rows behind the last key come along; the
+        // softmax clears their values.
+        if (lw == 0) {
+          const int per_half = kKeys / P.box_rows, boxes = per_half * (DP / 64);
+          const int box = lane % per_half, half = lane / per_half;
+          const int at = box * P.box_rows;
+          auto page_of = [&](int t) {
+            return t < t1 && lane < boxes ? page_at(t * kKeys + at) : -1;
+          };
+          const int in_page = C.page_size > kKeys ? C.page_size : kKeys;
+          int page = page_of(w.t0), page_next = page_of(w.t0 + 1);
+          for (int t = w.t0; t < t1; t++) {
+            const int count = __popc(__ballot_sync(kFullMask, page >= 0));
 #pragma unroll
-        for (int kv = 0; kv < 2; kv++, job++) {
-          const uint32_t stage = job % kStages, use = job / kStages;
-          barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
-          tile_copy(base + S::kStageAt + stage * S::kTileBytes, kv ? C.v : C.k, off);
-          copies_arrive(smem_of(&s.kv_full[stage]));
+            for (int kv = 0; kv < 2; kv++, job++) {
+              const uint32_t stage = job % kStages, use = job / kStages;
+              const uint32_t bar = smem_of(&s.kv_full[stage]);
+              barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
+              if (lane == 0) barrier_expect(bar, count * P.box_rows * 128);
+              __syncwarp();
+              if (page >= 0)
+                tensor_copy(base + S::kStageAt + stage * S::kTileBytes + half * (kKeys * 128) + at * 128,
+                            kv ? &v_map : &k_map, half * 64, t * kKeys % in_page, w.h, page, bar);
+            }
+            page = page_next;
+            page_next = page_of(t + 2);
+          }
+        }
+      } else {
+        auto key_of = [&](int t) { return t * kKeys + 32 * lw + lane; };
+        auto page_of = [&](int t) { return t < t1 ? page_at(key_of(t)) : -1; };
+        int page = page_of(w.t0), page_next = page_of(w.t0 + 1);
+        for (int t = w.t0; t < t1; t++) {
+          const int64_t off = page < 0 ? static_cast<int64_t>(-1)
+                                       : page * C.page_stride +
+                                             key_of(t) % C.page_size * C.row_stride +
+                                             w.h * C.head_stride;
+          page = page_next;
+          page_next = page_of(t + 2);
+#pragma unroll
+          for (int kv = 0; kv < 2; kv++, job++) {
+            const uint32_t stage = job % kStages, use = job / kStages;
+            barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
+            tile_copy(base + S::kStageAt + stage * S::kTileBytes, kv ? C.v : C.k, off);
+            copies_arrive(smem_of(&s.kv_full[stage]));
+          }
         }
       }
+      __syncwarp();
+      done_item();
     }
-    // The MMAs' last arrivals must find this CTA's shared memory.
-    for (int i = 0; i < kStages; i++, job++)
-      barrier_wait(smem_of(&s.kv_empty[job % kStages]), (job / kStages & 1) ^ 1, gave_up);
-    for (int i = 0; i < (kPair ? 1 : 2); i++, item++)
-      barrier_wait(smem_of(&s.q_empty[kPair ? 0 : item & 1]), ((kPair ? item : item / 2) & 1) ^ 1,
-                   gave_up);
+    // Copies still in flight must find this CTA's shared memory.
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (P.box_rows && *gave_up)
+      for (uint32_t k = job < kStages ? 0 : job - kStages; k < job; k++)
+        barrier_wait_own(smem_of(&s.kv_full[k % kStages]), k / kStages & 1);
   } else if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_REGS_OTHER ";");
     // --------------------------------------------------------------- MMAs
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_REGS_MMA ";");
     constexpr uint32_t kType = std::is_same<E, Bf16>::value ? 1 : 0;
     constexpr uint32_t kIdesc = 1u << 4 | kType << 7 | kType << 10 | (kRows >> 4) << 24;
     constexpr uint32_t kIdescS = kIdesc | (kKeys >> 3) << 17;
     constexpr uint32_t kIdescO = kIdesc | 1u << 16 | (DP >> 3) << 17;
     if (warp == kMmaWarp && lane == 0) {
       const int steps = (C.head_dim + 15) / 16;
-      uint32_t tile = 0, item = 0;       // key tiles and items so far
+      uint32_t tile = 0;              // key tiles so far
       uint32_t weighted[2] = {0, 0};  // O updates of each stream so far
       auto stage_at = [&](uint32_t job) { return base + S::kStageAt + job % kStages * S::kTileBytes; };
       auto kv_wait = [&](uint32_t job) {
         barrier_wait(smem_of(&s.kv_full[job % kStages]), job / kStages & 1, gave_up);
-        // the copies wrote through the generic proxy, the MMA reads through the other
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        // copies of 16 bytes wrote through the generic proxy, the MMA reads through the other
+        if (!P.box_rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       };
       auto qk = [&](int st, uint32_t q_at, uint32_t k_at) {
         const uint32_t a = operand_low(q_at, 16), b = operand_low(k_at, 16);
@@ -588,17 +639,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         if (due_second) pv(1, stage_at(v_job), due_first);
         mma_commit(smem_of(&s.kv_empty[v_job % kStages]));
       };
-      while (w.next(P)) {
+      while (true) {
+        const uint32_t item = items;
+        const Item& w = next_item();
+        if (over(w)) break;
         const int q_buffer = kPair ? 0 : item & 1;
         const uint32_t q_use = kPair ? item : item / 2;
-        const bool second = kPair && w.rows(P.group) > kRows;
+        const bool second = kPair && w.rows(P.group, S::kRowTile) > kRows;
+        const int t0 = w.t0, t1 = w.t1;
+        done_item();
         bool started[2] = {false, false};
         if (kPair && due) {  // the queries have one buffer: nothing to issue before they are there
           last_pair(2 * tile - 1);
           due = false;
         }
         barrier_wait(smem_of(&s.q_full[q_buffer]), q_use & 1, gave_up);
-        for (int t = w.t0; t < w.t1; t++, tile++) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        for (int t = t0; t < t1; t++, tile++) {
           const uint32_t k_job = 2 * tile, v_job = 2 * tile - 1;  // this tile's keys, the last's values
           if (kPair) {
             if (due) {
@@ -611,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             if (due) mma_commit(smem_of(&s.kv_empty[v_job % kStages]));
             if (second) qk(1, base + S::kTileBytes, stage_at(k_job));
             mma_commit(smem_of(&s.kv_empty[k_job % kStages]));
-            due_first = t == w.t0;
+            due_first = t == t0;
             due_second = second;
           } else {
             const int st = tile & 1;
@@ -629,7 +686,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
           due = true;
         }
         mma_commit(smem_of(&s.q_empty[q_buffer]));
-        item++;
       }
       if (due) {
         const uint32_t v_job = 2 * tile - 1;
@@ -641,8 +697,124 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
           mma_commit(smem_of(&s.kv_empty[v_job % kStages]));
         }
       }
+      // every MMA and every arrival that waits for one must find this CTA's memory
+      mma_commit(smem_of(&s.drained));
+      barrier_wait_own(smem_of(&s.drained), 0);
     }
     __syncwarp();
+    // ------------------------------------------------------------ dealing
+    if (warp == kDealWarp) {
+      const Runs runs(P, static_cast<int64_t>(s.total));
+      if (blockIdx.x == 0 && lane == 0) P.ws.header->total = runs.total;
+      int b = 0;         // the request where the search is, ...
+      int64_t before = 0;  // ... and the units before it
+      bool stop = false;
+      for (int run = blockIdx.x; run < runs.count && !stop;) {
+        int64_t u = runs.start(run);
+        const int64_t end = u + runs.length(run);
+        bool first = true;
+        while (u < end && !stop) {
+          // the request with unit u: 32 requests at a time
+          int tiles, row_tiles, len, n;
+          int64_t units;
+          while (true) {
+            units = b + lane < P.B ? units_of<S::kRowTile>(P, b + lane, tiles, row_tiles, len, n) : 0;
+            int64_t upto = units;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+              const int64_t x = __shfl_up_sync(kFullMask, upto, o);
+              if (lane >= o) upto += x;
+            }
+            const uint32_t past = __ballot_sync(kFullMask, before + upto > u);
+            const int from = past ? __ffs(past) - 1 : 31;
+            if (past) {
+              before += __shfl_sync(kFullMask, upto - units, from);
+              b += from;
+              tiles = __shfl_sync(kFullMask, tiles, from);
+              row_tiles = __shfl_sync(kFullMask, row_tiles, from);
+              len = __shfl_sync(kFullMask, len, from);
+              n = __shfl_sync(kFullMask, n, from);
+              units = __shfl_sync(kFullMask, units, from);
+              break;
+            }
+            before += __shfl_sync(kFullMask, upto, 31);
+            b += 32;
+            if (b >= P.B) {  // the lengths changed meanwhile
+              stop = true;
+              break;
+            }
+          }
+          if (stop) break;
+          uint8_t up[2];
+#pragma unroll
+          for (int k = 0; k < 2; k++) {
+            const int i = lane + 32 * k;
+            int parent = i - 1;
+            if (P.parents && i < n) parent = P.parents[static_cast<int64_t>(b) * P.N + i];
+            up[k] = static_cast<uint8_t>(parent >= 0 && parent < i ? parent : 0);
+          }
+          while (u < end && u < before + units) {
+            const int64_t off = u - before, of = off / tiles;
+            const int t0 = static_cast<int>(off - of * tiles), h = static_cast<int>(of / row_tiles);
+            const int row_tile = static_cast<int>(of - static_cast<int64_t>(h) * row_tiles);
+            const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (end - u)));
+            if (first && lane == 0)
+              P.ws.starts[run] = Start{b, h, row_tile, t0, tiles, n, {0, 0}};
+            first = false;
+            const uint32_t slot = items % kItems;
+            barrier_wait(smem_of(&s.item_empty[slot]), (items / kItems & 1) ^ 1, gave_up);
+            stop = __any_sync(kFullMask, *gave_up != 0);
+            if (stop) break;
+            Item& to = s.items[slot];
+            to.parents[lane] = up[0];
+            to.parents[lane + 32] = up[1];
+            if (lane == 0) {
+              to.b = b;
+              to.h = h;
+              to.row_tile = row_tile;
+              to.t0 = t0;
+              to.t1 = t1;
+              to.tiles = tiles;
+              to.len = len;
+              to.n = n;
+              to.run = run;
+            }
+            __syncwarp();
+            if (lane == 0) barrier_arrive(smem_of(&s.item_full[slot]));
+            items++;
+            u += t1 - t0;
+          }
+        }
+        // Not before the copies of this run's last item are on their way: a run taken
+        // early is one that an idle CTA does not find.
+        barrier_wait(smem_of(&s.item_empty[(items - 1) % kItems]), (items - 1) / kItems & 1, gave_up);
+        const int dealt =
+            __shfl_sync(kFullMask, lane == 0 ? atomicAdd(&P.ws.header->next, 1) : 0, 0);
+        if (dealt < 0) break;  // a workspace that was not zeroed
+        run = dealt < INT_MAX - P.ctas ? P.ctas + dealt : INT_MAX;
+      }
+      {
+        const uint32_t slot = items % kItems;
+        barrier_wait(smem_of(&s.item_empty[slot]), (items / kItems & 1) ^ 1, gave_up);
+        if (lane == 0 && !*gave_up) {
+          s.items[slot].t0 = -1;
+          barrier_arrive(smem_of(&s.item_full[slot]));
+        }
+      }
+    }
+    // ----------------------------------------------------------- checking
+    if (warp >= kCheckWarp) {
+      for (int b = blockIdx.x * 2 + warp - kCheckWarp; b < P.B; b += 2 * gridDim.x) {
+        Tree t = read_tree(P.parents, P.n_nodes, C.lens, b, P.N,
+                           static_cast<int64_t>(C.max_pages) * C.page_size, lane);
+        if (!t.bad && __any_sync(kFullMask, bad_pages(C, b, 0, t.len + t.n, lane, 32)))
+          t.bad |= SPECV_DEV_BAD_CACHE;
+        if (lane == 0) {
+          P.ws.bad[b] = static_cast<int32_t>(t.bad);
+          P.status[b] = static_cast<int32_t>(t.bad);
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 " SPECV_REGS_SOFTMAX ";");
@@ -650,16 +822,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     const int row = quarter * 32 + lane;  // of the stream's tile
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const float c = P.scale_log2;
-    uint32_t tile = 0, item = 0, scores[2] = {0, 0};  // scores: tiles of each stream so far
-    bool told = false;
-    while (w.next(P)) {
-      const int rows = w.rows(P.group);
+    uint32_t tile = 0, scores[2] = {0, 0};  // scores: tiles of each stream so far
+    while (true) {
+      const uint32_t item = items;
+      const Item& given = next_item();
+      if (any_of_softmax(over(given))) break;  // all leave together
+      const struct {
+        int b, h, row_tile, t0, t1, tiles, len, n, run;
+      } w = {given.b,     given.h,   given.row_tile, given.t0, given.t1,
+             given.tiles, given.len, given.n,        given.run};
+      const int rows = given.rows(P.group, S::kRowTile);
       const int first_row = kPair ? st * kRows : 0;
       const bool second = !kPair || rows > kRows;
       const bool working = first_row + quarter * 32 < rows;  // this warp has rows
       const int at = w.row_tile * S::kRowTile + min(first_row + row, rows - 1);
       const int node = at / P.group, g = at - node * P.group;
-      const uint64_t visible = P.plan.visible[static_cast<int64_t>(w.b) * kMaxNodes + node];
+      uint64_t visible = 1;  // nodes that this row sees: its own and those above it
+      if (w.t1 * kKeys > w.len)
+        for (int i = node; i > 0; i = given.parents[i]) visible |= 1ull << i;
+      __syncwarp();
+      done_item();
       const int keys = w.len + w.n;
       uint64_t* odd = &s.odd_values[item & 1];
       int taken[2] = {0, 0};  // tiles of this item that each stream took
@@ -682,6 +864,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
           barrier_wait(smem_of(&s.kv_full[stage]), job / kStages & 1, gave_up);
           char* v = smem + S::kStageAt + stage * S::kTileBytes;
           const int from = max(w.len - t * kKeys, 0), to = min(keys - t * kKeys, kKeys);
+          // (and a tensor copy's rows behind the last key hold whatever the page has)
+          const int stale = P.box_rows ? kKeys - to : 0;
           constexpr uint32_t kExp = std::is_same<E, Bf16>::value ? 0x7f80u : 0x7c00u;
           bool changed = false;
           for (int e = (quarter * 32 + lane); e < (to - from) * (DP / 8); e += 128) {
@@ -702,7 +886,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
               changed = true;
             }
           }
-          if (changed) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          for (int e = quarter * 32 + lane; e < stale * (DP / 8); e += 128) {
+            const int r = to + e / (DP / 8), p = e % (DP / 8);
+            *reinterpret_cast<uint4*>(v + (p / 8) * (kKeys * 128) + r * 128 + (p % 8) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          if (changed || stale) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         barrier_wait(smem_of(&s.s_full[st]), scores[st] & 1, gave_up);
         __syncwarp();
@@ -799,10 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
       const uint64_t fix = *odd & visible;
       const float2 other = s.stats[st ^ 1][row];
       if (tid == 0) s.odd_values[(item & 1) ^ 1] = 0;
-      if (*gave_up && !told) {
-        told = true;
-        if (tid == 0) atomicOr(P.status + w.b, SPECV_DEV_TIMEOUT);
-      }
+      if (tid == 0 && *gave_up) P.ws.header->timeout = 1;
       // kPair: this stream's rows, all columns; else half of the columns of both streams' sum
       const int my_rows = rows - first_row;
       if (quarter * 32 < my_rows) {
@@ -823,8 +1009,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         const bool mine = row < my_rows;
         uint16_t* out = P.out.data + w.b * P.out.batch_stride + node * P.out.node_stride +
                         (w.h * P.group + g) * P.out.head_stride;
-        const int slot = 2 * blockIdx.x + (w.t0 == 0);
-        const int64_t part = static_cast<int64_t>(slot) * S::kRowTile + first_row + row;
+        const int64_t part =
+            static_cast<int64_t>(2 * w.run + (w.t0 == 0)) * P.part_rows + first_row + row;
         constexpr int kCols = kPair ? DP : DP / 2;
         const int col0 = kPair ? 0 : st * kCols;
 #pragma unroll 1
@@ -873,29 +1059,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
           } else if (mine) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(P.plan.parts + part * DP + col0 + k + e) =
+              *reinterpret_cast<float4*>(P.ws.parts + part * DP + col0 + k + e) =
                   make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
           __syncwarp();
         }
-        if (!whole && mine && (kPair || st == 0)) P.plan.stats[part] = make_float2(m, l);
+        if (!whole && mine && (kPair || st == 0)) P.ws.stats[part] = make_float2(m, l);
       }
-      item++;
       tmem_fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");
       tmem_fence_after();
     }
   }
 
-  // Where this CTA began, for combine_kernel.
-  if (tid == 0) {
-    Walk<S::kRowTile> v;
-    v.start(P, s, share);
-    int4 at = make_int4(0, 0, 0, 0);
-    if (v.next(P)) at = make_int4(v.b, v.h, v.row_tile, v.t0);
-    P.plan.starts[blockIdx.x] = at;
-    if (blockIdx.x == 0) *P.plan.share = share;
-  }
+  if (tid == 0 && *gave_up) P.ws.header->timeout = 1;
   tmem_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -904,117 +1081,185 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
   }
 }
 
-// ----------------------------------------------------------------- combine
+// ------------------------------------------------------------------ finish
 
-constexpr int kCombineWarps = 8;
+constexpr int kFinishWarps = 8;
+constexpr int kFinishRows = 4;  // rows of a warp
 
-// Joins the pieces of the items that runs of units cut.  Block x stands for the
-// cut before CTA x's run; the first cut of an item joins all its pieces:
+// Block x < B: a flagged request's rows become 0.  The others, B + y: the cut
+// before run 1 + y / groups, for 32 of its item's rows.  The first cut of an
+// item joins all its pieces:
 //   m = max m_i, O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i, in order.
-// A warp has a row, a lane four of its columns.
+// A lane has four columns of a row.
 template <class E, int DP, int kRowTile>
-__global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const AttnParams P) {
+__global__ void __launch_bounds__(kFinishWarps * 32) finish_kernel(const AttnParams P, int groups) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int cta = blockIdx.x + 1, lane = threadIdx.x & 31;
-  const int4 at = P.plan.starts[cta];
-  const int t0 = at.w;
-  if (t0 == 0) return;  // no cut here
-  const int row = blockIdx.y * kCombineWarps + threadIdx.x / 32;
-  const int b = at.x, h = at.y, n = P.plan.nodes[b];
-  const int flat = at.z * kRowTile + row;
-  if (row >= kRowTile || flat >= n * P.group) return;
-  // runs are of equal length: the one before began `share` units earlier
-  const int4 before = P.plan.starts[cta - 1];
-  if (before.x == b && before.y == h && before.z == at.z && before.w != 0) return;  // not the first
-  const int tiles = (P.plan.len[b] + n + kKeys - 1) / kKeys;
-  const int share = static_cast<int>(min(*P.plan.share, static_cast<int64_t>(INT_MAX)));
-  const int pieces = 1 + (tiles - t0 - 1) / share + 1;
-  auto index = [&](int i) {  // piece 0 ends CTA cta - 1's run, the others begin theirs
-    const int slot = i == 0 ? 2 * (cta - 1) + 1 : 2 * (cta + i - 1);
-    return static_cast<int64_t>(slot) * kRowTile + row;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const Header* header = P.ws.header;
+  if (blockIdx.x == 0 && tid == 0) P.ws.header->next = 0;  // for the next call
+  if (static_cast<int>(blockIdx.x) < P.B) {
+    const int b = blockIdx.x;
+    if (header->timeout && tid == 0) P.status[b] = P.ws.bad[b] | SPECV_DEV_TIMEOUT;
+    if (P.ws.bad[b] == 0) return;
+    const int given = P.n_nodes ? P.n_nodes[b] : P.N;
+    const int n = given < 1 || given > P.N ? P.N : given, words = P.cache.head_dim / 8;
+    for (int e = tid; e < n * P.q_heads * words; e += kFinishWarps * 32) {
+      const int i = e / (P.q_heads * words), h = e / words % P.q_heads, d = e % words * 8;
+      *reinterpret_cast<uint4*>(P.out.data + b * P.out.batch_stride + i * P.out.node_stride +
+                                h * P.out.head_stride + d) = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const int block = blockIdx.x - P.B, run = 1 + block / groups;
+  const Start at = P.ws.starts[run], before = P.ws.starts[run - 1];
+  const Runs runs(P, header->total);
+  if (run >= runs.count || at.t0 == 0) return;  // no cut here
+  if (before.b == at.b && before.h == at.h && before.row_tile == at.row_tile && before.t0 != 0)
+    return;  // not the item's first
+  const int row0 = (block % groups * kFinishWarps + tid / 32) * kFinishRows;
+  const int rows = min(kRowTile, at.n * P.group - at.row_tile * kRowTile);
+  if (row0 >= rows || P.ws.bad[at.b]) return;
+  int pieces = 2;  // one ends the run before, the others begin a run each
+  for (int64_t left = at.tiles - at.t0; left > runs.length(run + pieces - 2); pieces++)
+    left -= runs.length(run + pieces - 2);
+  auto index = [&](int i, int r) {
+    const int slot = i == 0 ? 2 * (run - 1) + 1 : 2 * (run + i - 1);
+    return static_cast<int64_t>(slot) * P.part_rows + min(row0 + r, rows - 1);
   };
-  float m = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) m = fmaxf(m, P.plan.stats[index(i)].x);
+  float m[kFinishRows], l[kFinishRows];
+  float4 o[kFinishRows];
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+  for (int r = 0; r < kFinishRows; r++) {
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+    o[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
   const int d = 4 * lane;
-  float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
+  // pieces one by one, the sums rescaled where the maximum rises
+#pragma unroll 2
   for (int i = 0; i < pieces; i++) {
-    const float2 ml = P.plan.stats[index(i)];
-    const float weight = ml.x == m ? 1.0f : exp2_of(ml.x - m);
-    l = fmaf(weight, ml.y, l);
-    if (d < DP) {
-      const float4 x = *reinterpret_cast<const float4*>(P.plan.parts + index(i) * DP + d);
-      o[0] = fmaf(weight, x.x, o[0]);
-      o[1] = fmaf(weight, x.y, o[1]);
-      o[2] = fmaf(weight, x.z, o[2]);
-      o[3] = fmaf(weight, x.w, o[3]);
+    float2 ml[kFinishRows];
+    float4 x[kFinishRows];
+#pragma unroll
+    for (int r = 0; r < kFinishRows; r++) {
+      ml[r] = P.ws.stats[index(i, r)];
+      if (d < DP) x[r] = *reinterpret_cast<const float4*>(P.ws.parts + index(i, r) * DP + d);
+    }
+#pragma unroll
+    for (int r = 0; r < kFinishRows; r++) {
+      const float top = fmaxf(m[r], ml[r].x);
+      const float old = m[r] == top ? 1.0f : exp2_of(m[r] - top);
+      const float weight = ml[r].x == top ? 1.0f : exp2_of(ml[r].x - top);
+      m[r] = top;
+      l[r] = l[r] * old + weight * ml[r].y;
+      o[r].x = o[r].x * old + weight * x[r].x;
+      o[r].y = o[r].y * old + weight * x[r].y;
+      o[r].z = o[r].z * old + weight * x[r].z;
+      o[r].w = o[r].w * old + weight * x[r].w;
     }
   }
   if (d >= P.cache.head_dim) return;
-  const float inv = 1.0f / l;
-  const int node = flat / P.group, g = flat - node * P.group;
-  *reinterpret_cast<uint2*>(P.out.data + b * P.out.batch_stride + node * P.out.node_stride +
-                            (h * P.group + g) * P.out.head_stride + d) =
-      make_uint2(E::pack(o[0] * inv, o[1] * inv), E::pack(o[2] * inv, o[3] * inv));
+#pragma unroll
+  for (int r = 0; r < kFinishRows; r++) {
+    if (row0 + r >= rows) break;
+    const float inv = 1.0f / l[r];
+    const int flat = at.row_tile * kRowTile + row0 + r, node = flat / P.group, g = flat - node * P.group;
+    *reinterpret_cast<uint2*>(P.out.data + at.b * P.out.batch_stride + node * P.out.node_stride +
+                              (at.h * P.group + g) * P.out.head_stride + d) =
+        make_uint2(E::pack(o[r].x * inv, o[r].y * inv), E::pack(o[r].z * inv, o[r].w * inv));
+  }
 }
 
 // ------------------------------------------------------------------- host
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-struct Layout {
-  size_t nodes, visible, share, starts, stats, parts, total;
+// The shape of the work that B, N and the heads give, whatever the lengths are.
+struct Plan {
+  bool pair;
+  int dim, part_rows, dealt;
+  size_t bad, starts, stats, parts, total;  // offsets in the workspace
+
+  Plan(int B, int N, int group, int head_dim) {
+    const int rows = N * group;
+    pair = rows > kRows;
+    dim = head_dim <= 64 ? 64 : 128;
+    const int row_tile = pair ? 2 * kRows : kRows;
+    part_rows = (rows < row_tile ? rows : row_tile) + 7 & ~7;
+    // a piece of many rows is as large as a key tile: then fewer of them
+    dealt = part_rows > 64 ? kMaxCtas : 3 * kMaxCtas;
+    const size_t runs = kMaxCtas + dealt;
+    bad = 256;
+    starts = bad + align256(static_cast<size_t>(B) * 4);
+    stats = starts + align256(runs * sizeof(Start));
+    parts = stats + align256(2 * runs * part_rows * sizeof(float2));
+    total = parts + align256(2 * runs * part_rows * dim * sizeof(float));
+  }
 };
 
-Layout layout(int B, int row_tile, int dim) {
-  Layout w;
-  w.nodes = align256(static_cast<size_t>(B) * 4);
-  w.visible = w.nodes + align256(static_cast<size_t>(B) * 4);
-  w.share = w.visible + align256(static_cast<size_t>(B) * kMaxNodes * 8);
-  w.starts = w.share + 256;
-  w.stats = w.starts + align256(kMaxCtas * sizeof(int4));
-  w.parts = w.stats + align256(2 * kMaxCtas * sizeof(float2) * static_cast<size_t>(row_tile));
-  w.total = w.parts + align256(2 * kMaxCtas * sizeof(float) * static_cast<size_t>(row_tile) * dim);
-  return w;
+// The tensor map of a cache: [page, head, row, d], boxes of 64 columns and
+// box_rows rows of a page.  Swizzled groups are eight rows, so pages of a
+// multiple of eight that divide a tile or are divided by it go this way.
+bool tensor_map(CUtensorMap* map, const specv_cache* c, void* data, int box_rows) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static const Encode encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<Encode>(fn);
+  }();
+  if (!encode) return false;
+  const int64_t row = static_cast<int64_t>(c->head_dim) * 2;
+  const cuuint64_t size[4] = {static_cast<cuuint64_t>(c->head_dim), static_cast<cuuint64_t>(c->page_size),
+                              static_cast<cuuint64_t>(c->heads), static_cast<cuuint64_t>(c->pages)};
+  const int64_t bytes[3] = {c->row_stride * 2, c->head_stride * 2, c->page_stride * 2};
+  cuuint64_t stride[3];
+  for (int i = 0; i < 3; i++) {
+    if (size[i + 1] > 1 && (bytes[i] < row || bytes[i] >= 1ll << 40)) return false;
+    stride[i] = size[i + 1] > 1 ? static_cast<cuuint64_t>(bytes[i]) : static_cast<cuuint64_t>(row);
+  }
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1}, step[4] = {1, 1, 1, 1};
+  return encode(map, c->dtype == SPECV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                4, data, size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int padded(int head_dim) { return head_dim <= 64 ? 64 : 128; }
-bool paired(int N, int group) { return N * group > kRows; }
-
 template <class E, int DP, bool kPair>
-cudaError_t run(const AttnParams& P, int N, int ctas, cudaStream_t stream) {
+cudaError_t run(const AttnParams& P, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                cudaStream_t stream) {
   using S = Shape<DP, kPair>;
-  constexpr int kSmem = S::kTailAt + static_cast<int>(sizeof(Tail));
+  constexpr int kSmem = S::kTailAt + static_cast<int>(sizeof(Tail<S::kStages>));
   static_assert(kSmem <= 232448, "one CTA's shared memory");
   cudaError_t e = cudaFuncSetAttribute(attention_kernel<E, DP, kPair>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  attention_kernel<E, DP, kPair><<<P.ctas, kThreads, kSmem, stream>>>(P, k_map, v_map);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  const int groups = (P.part_rows + kFinishWarps * kFinishRows - 1) / (kFinishWarps * kFinishRows);
+  cfg.gridDim = dim3(P.B + (P.ctas + P.dealt - 1) * groups);
+  cfg.blockDim = dim3(kFinishWarps * 32);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attention_kernel<E, DP, kPair>, P);
-  if (e != cudaSuccess || ctas == 1) return e;
-  const int rows = N * P.group < S::kRowTile ? N * P.group : S::kRowTile;
-  cfg.gridDim = dim3(ctas - 1, (rows + kCombineWarps - 1) / kCombineWarps);
-  cfg.blockDim = dim3(kCombineWarps * 32);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<E, DP, S::kRowTile>, P);
+  return cudaLaunchKernelEx(&cfg, finish_kernel<E, DP, S::kRowTile>, P, groups);
 }
 
 template <class E>
-cudaError_t run_any(const AttnParams& P, bool pair, int dim, int N, int ctas, cudaStream_t stream) {
-  if (dim == 64)
-    return pair ? run<E, 64, true>(P, N, ctas, stream) : run<E, 64, false>(P, N, ctas, stream);
-  return pair ? run<E, 128, true>(P, N, ctas, stream) : run<E, 128, false>(P, N, ctas, stream);
+cudaError_t run_any(const AttnParams& P, const Plan& plan, const CUtensorMap& k, const CUtensorMap& v,
+                    cudaStream_t stream) {
+  if (plan.dim == 64)
+    return plan.pair ? run<E, 64, true>(P, k, v, stream) : run<E, 64, false>(P, k, v, stream);
+  return plan.pair ? run<E, 128, true>(P, k, v, stream) : run<E, 128, false>(P, k, v, stream);
 }
 
 }  // namespace
@@ -1026,7 +1271,7 @@ size_t specv_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, 
       q_heads < kv_heads || q_heads > 1024 || q_heads % kv_heads != 0 || head_dim < 8 ||
       head_dim > SPECV_MAX_HEAD_DIM || head_dim % 8 != 0)
     return 0;
-  return layout(B, paired(N, q_heads / kv_heads) ? 2 * kRows : kRows, padded(head_dim)).total;
+  return Plan(B, N, q_heads / kv_heads, head_dim).total;
 }
 
 specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
@@ -1043,36 +1288,54 @@ specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
     return SPECV_ERR_INVALID_ARG;
   if (q_heads > 1024) return SPECV_ERR_UNSUPPORTED;
   const int group = q_heads / cache->heads;
-  const bool pair = paired(N, group);
-  const int dim = padded(cache->head_dim);
-  const Layout w = layout(B, pair ? 2 * kRows : kRows, dim);
-  if (workspace_bytes < w.total) return SPECV_ERR_WORKSPACE;
+  const Plan plan(B, N, group, cache->head_dim);
+  if (workspace_bytes < plan.total) return SPECV_ERR_WORKSPACE;
   int device = 0, ctas = 0;
   if (cudaGetDevice(&device) != cudaSuccess ||
       cudaDeviceGetAttribute(&ctas, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return SPECV_ERR_CUDA;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
   char* base = static_cast<char*>(workspace);
-  const Plan plan{reinterpret_cast<int32_t*>(base),
-                  reinterpret_cast<int32_t*>(base + w.nodes),
-                  reinterpret_cast<uint64_t*>(base + w.visible),
-                  reinterpret_cast<int64_t*>(base + w.share),
-                  reinterpret_cast<int4*>(base + w.starts),
-                  reinterpret_cast<float*>(base + w.parts),
-                  reinterpret_cast<float2*>(base + w.stats)};
-  const Cache C = to_cache(cache);
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  prepare_kernel<<<B, kPrepThreads, 0, st>>>(C, parents, n_nodes, N, plan, to_rows(out), q_heads,
-                                             status);
-  const AttnParams P{C,       to_rows(q), to_rows(out), plan, status, B, q_heads, group,
+  const Workspace ws{reinterpret_cast<Header*>(base), reinterpret_cast<int32_t*>(base + plan.bad),
+                     reinterpret_cast<Start*>(base + plan.starts),
+                     reinterpret_cast<float2*>(base + plan.stats),
+                     reinterpret_cast<float*>(base + plan.parts)};
+  const int page = cache->page_size;
+  int box_rows = page % 8 == 0 && (page >= kKeys ? page % kKeys == 0 : kKeys % page == 0)
+                     ? (page < kKeys ? page : kKeys)
+                     : 0;
+  CUtensorMap k_map = {}, v_map = {};
+  if (box_rows && (!tensor_map(&k_map, cache, cache->k, box_rows) ||
+                   !tensor_map(&v_map, cache, cache->v, box_rows)))
+    box_rows = 0;
+  // Where no length can give eight units to a CTA, no run is dealt out.
+  const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * page + kKeys - 1) / kKeys;
+  const int row_tiles = (N * group + (plan.pair ? 2 * kRows : kRows) - 1) / (plan.pair ? 2 * kRows : kRows);
+  const bool deals = static_cast<int64_t>(B) * cache->heads * row_tiles * tiles >= 8 * ctas;
+  const AttnParams P{to_cache(cache),
+                     to_rows(q),
+                     to_rows(out),
+                     ws,
+                     parents,
+                     n_nodes,
+                     status,
+                     B,
+                     N,
+                     q_heads,
+                     group,
+                     ctas,
+                     deals ? plan.dealt : 0,
+                     plan.part_rows,
+                     box_rows,
                      scale * 1.4426950408889634f};
-  const cudaError_t e = cache->dtype == SPECV_BF16 ? run_any<Bf16>(P, pair, dim, N, ctas, st)
-                                                   : run_any<F16>(P, pair, dim, N, ctas, st);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = cache->dtype == SPECV_BF16 ? run_any<Bf16>(P, plan, k_map, v_map, st)
+                                                   : run_any<F16>(P, plan, k_map, v_map, st);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return SPECV_ERR_CUDA;
   }
-  return launched();
+  return SPECV_OK;
 }
 
 }  // extern "C"

@@ -184,17 +184,23 @@ def append_nodes(q, k, v, k_cache, v_cache, page_table, cache_lens, inv_freq=Non
 
 
 class AttentionWorkspace:
-    """Device workspace for tree_attention over B requests of up to N nodes.
-    It keeps nothing between calls; calls that may run at the same time (on
-    two streams, or two captured graphs that may be replayed together) need
-    one each."""
+    """Device workspace for tree_attention over B requests of up to N nodes,
+    zeroed once on creation (every call leaves it ready for the next).  Calls
+    that may run at the same time (on two streams, or two captured graphs that
+    may be replayed together) need one each."""
 
-    def __init__(self, B: int, N: int, q_heads: int, kv_heads: int, head_dim: int, device=None):
+    def __init__(self, B: int, N: int, q_heads: int, kv_heads: int, head_dim: int, device=None,
+                 stream=None):
         self.nbytes = int(lib().specv_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim))
         if self.nbytes == 0:
             raise ValueError(f"unsupported attention shape B={B} N={N} q_heads={q_heads} "
                              f"kv_heads={kv_heads} head_dim={head_dim}")
         self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        dev = self.tensor.device
+        with torch.cuda.device(dev):
+            check("specv_workspace_init", lib().specv_workspace_init(
+                self.tensor.data_ptr(), 256,  # its header
+                _raw_stream(dev.index) if stream is None else getattr(stream, "cuda_stream", stream)))
 
 
 def tree_attention(q, k_cache, v_cache, page_table, cache_lens, parents=None, n_nodes=None, *,
