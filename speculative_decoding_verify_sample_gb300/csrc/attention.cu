@@ -363,6 +363,17 @@ template <int DP, bool kPair> struct Shape {
   // then the barriers and what the warps tell one another
   static constexpr int kStageAt = 2 * kTileBytes;
   static constexpr int kTailAt = kStageAt + kStages * kTileBytes;
+
+  // The order of an item's tiles in the ring, that of the MMAs that read them.
+  // One stream: keys a tile ahead of values, K0 K1 V0 K2 V1 .. Kn Vn-1 Vn, so that
+  // values do not wait in the ring through their tile's softmax.  Two row tiles:
+  // K0 V0 K1 V1 ..
+  static __device__ __forceinline__ uint32_t key_job(int i) {
+    return kPair ? 2 * i : i ? 2 * i - 1 : 0;
+  }
+  static __device__ __forceinline__ uint32_t value_job(int i, int tiles) {
+    return kPair || i == tiles - 1 ? 2 * i + 1 : 2 * i + 2;
+  }
 };
 
 // All key tiles t0 .. t1-1 of a row tile that one run has.
@@ -490,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kRowsAtOnce = 32 / kPieces;  // rows of one warp instruction
     const int lw = warp - kLoadWarp, piece = lane % kPieces, sub = lane / kPieces;
     const bool inside = piece * 8 < C.head_dim;
-    uint32_t job = 0;
+    uint32_t jobs = 0;  // before this item
     // 128-byte rows, their 16-byte pieces swapped by the row's number: rows
     // kRowsAtOnce apart, and sub < kRowsAtOnce, so r and sub set bits of their own
     const uint32_t lane_at = (piece / 8) * (kKeys * 128) + (32 * lw + sub) * 128;
@@ -545,50 +556,63 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           const int in_page = C.page_size > kKeys ? C.page_size : kKeys;
           int page = page_of(w.t0), page_next = page_of(w.t0 + 1);
-          for (int t = w.t0; t < t1; t++) {
+          auto copy = [&](uint32_t job, const CUtensorMap* map, int page, int t) {
+            const uint32_t stage = (jobs + job) % kStages, use = (jobs + job) / kStages;
+            const uint32_t bar = smem_of(&s.kv_full[stage]);
             const int count = __popc(__ballot_sync(kFullMask, page >= 0));
-#pragma unroll
-            for (int kv = 0; kv < 2; kv++, job++) {
-              const uint32_t stage = job % kStages, use = job / kStages;
-              const uint32_t bar = smem_of(&s.kv_full[stage]);
-              barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
-              if (lane == 0) barrier_expect(bar, count * P.box_rows * 128);
-              __syncwarp();
-              if (page >= 0)
-                tensor_copy(base + S::kStageAt + stage * S::kTileBytes + half * (kKeys * 128) + at * 128,
-                            kv ? &v_map : &k_map, half * 64, t * kKeys % in_page, w.h, page, bar);
-            }
+            barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
+            if (lane == 0) barrier_expect(bar, count * P.box_rows * 128);
+            __syncwarp();
+            if (page >= 0)
+              tensor_copy(base + S::kStageAt + stage * S::kTileBytes + half * (kKeys * 128) + at * 128,
+                          map, half * 64, t * kKeys % in_page, w.h, page, bar);
+          };
+          int page_before = -1;
+          for (int t = w.t0; t < t1; t++) {
+            const int i = t - w.t0;
+            copy(S::key_job(i), &k_map, page, t);
+            if (kPair) copy(S::value_job(i, t1 - w.t0), &v_map, page, t);
+            else if (i > 0) copy(S::value_job(i - 1, t1 - w.t0), &v_map, page_before, t - 1);
+            page_before = page;
             page = page_next;
             page_next = page_of(t + 2);
           }
+          if (!kPair) copy(S::value_job(t1 - 1 - w.t0, t1 - w.t0), &v_map, page_before, t1 - 1);
         }
       } else {
         auto key_of = [&](int t) { return t * kKeys + 32 * lw + lane; };
         auto page_of = [&](int t) { return t < t1 ? page_at(key_of(t)) : -1; };
         int page = page_of(w.t0), page_next = page_of(w.t0 + 1);
+        auto copy = [&](uint32_t job, const uint16_t* from, int64_t off) {
+          const uint32_t stage = (jobs + job) % kStages, use = (jobs + job) / kStages;
+          barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
+          tile_copy(base + S::kStageAt + stage * S::kTileBytes, from, off);
+          copies_arrive(smem_of(&s.kv_full[stage]));
+        };
+        int64_t before = -1;
         for (int t = w.t0; t < t1; t++) {
+          const int i = t - w.t0;
           const int64_t off = page < 0 ? static_cast<int64_t>(-1)
                                        : page * C.page_stride +
                                              key_of(t) % C.page_size * C.row_stride +
                                              w.h * C.head_stride;
           page = page_next;
           page_next = page_of(t + 2);
-#pragma unroll
-          for (int kv = 0; kv < 2; kv++, job++) {
-            const uint32_t stage = job % kStages, use = job / kStages;
-            barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
-            tile_copy(base + S::kStageAt + stage * S::kTileBytes, kv ? C.v : C.k, off);
-            copies_arrive(smem_of(&s.kv_full[stage]));
-          }
+          copy(S::key_job(i), C.k, off);
+          if (kPair) copy(S::value_job(i, t1 - w.t0), C.v, off);
+          else if (i > 0) copy(S::value_job(i - 1, t1 - w.t0), C.v, before);
+          before = off;
         }
+        if (!kPair) copy(S::value_job(t1 - 1 - w.t0, t1 - w.t0), C.v, before);
       }
+      jobs += 2 * (t1 - w.t0);
       __syncwarp();
       done_item();
     }
     // Copies still in flight must find this CTA's shared memory.
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (P.box_rows && *gave_up)
-      for (uint32_t k = job < kStages ? 0 : job - kStages; k < job; k++)
+      for (uint32_t k = jobs < kStages ? 0 : jobs - kStages; k < jobs; k++)
         barrier_wait_own(smem_of(&s.kv_full[k % kStages]), k / kStages & 1);
   } else if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_REGS_OTHER ";");
@@ -599,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdescO = kIdesc | 1u << 16 | (DP >> 3) << 17;
     if (warp == kMmaWarp && lane == 0) {
       const int steps = (C.head_dim + 15) / 16;
-      uint32_t tile = 0;              // key tiles so far
+      uint32_t tile = 0, jobs = 0;    // key tiles so far, copies before this item
       uint32_t weighted[2] = {0, 0};  // O updates of each stream so far
       auto stage_at = [&](uint32_t job) { return base + S::kStageAt + job % kStages * S::kTileBytes; };
       auto kv_wait = [&](uint32_t job) {
@@ -632,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // the update that is due: a tile's values wait until the next tile's scores are issued
       bool due = false, due_first = false;
+      uint32_t due_job = 0;
       bool due_second = false;  // kPair: the item has rows for stream 1
       auto last_pair = [&](uint32_t v_job) {
         kv_wait(v_job);
@@ -650,13 +675,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         done_item();
         bool started[2] = {false, false};
         if (kPair && due) {  // the queries have one buffer: nothing to issue before they are there
-          last_pair(2 * tile - 1);
+          last_pair(due_job);
           due = false;
         }
         barrier_wait(smem_of(&s.q_full[q_buffer]), q_use & 1, gave_up);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         for (int t = t0; t < t1; t++, tile++) {
-          const uint32_t k_job = 2 * tile, v_job = 2 * tile - 1;  // this tile's keys, the last's values
+          // this tile's keys, the last one's values
+          const uint32_t k_job = jobs + S::key_job(t - t0), v_job = due_job;
           if (kPair) {
             if (due) {
               kv_wait(v_job);
@@ -684,17 +710,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             started[st] = true;
           }
           due = true;
+          due_job = jobs + S::value_job(t - t0, t1 - t0);
         }
+        jobs += 2 * (t1 - t0);
         mma_commit(smem_of(&s.q_empty[q_buffer]));
       }
       if (due) {
-        const uint32_t v_job = 2 * tile - 1;
         if (kPair) {
-          last_pair(v_job);
+          last_pair(due_job);
         } else {
-          kv_wait(v_job);
-          pv((tile - 1) & 1, stage_at(v_job), due_first);
-          mma_commit(smem_of(&s.kv_empty[v_job % kStages]));
+          kv_wait(due_job);
+          pv((tile - 1) & 1, stage_at(due_job), due_first);
+          mma_commit(smem_of(&s.kv_empty[due_job % kStages]));
         }
       }
       // every MMA and every arrival that waits for one must find this CTA's memory
@@ -754,9 +781,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             up[k] = static_cast<uint8_t>(parent >= 0 && parent < i ? parent : 0);
           }
           while (u < end && u < before + units) {
-            const int64_t off = u - before, of = off / tiles;
-            const int t0 = static_cast<int>(off - of * tiles), h = static_cast<int>(of / row_tiles);
-            const int row_tile = static_cast<int>(of - static_cast<int64_t>(h) * row_tiles);
+            const int64_t off = u - before;
+            const int64_t of = off >> 32 ? off / tiles : static_cast<uint32_t>(off) / tiles;
+            const int t0 = static_cast<int>(off - of * tiles);
+            const int h = static_cast<int>(of) / row_tiles;  // below 1024 heads * 512 row tiles
+            const int row_tile = static_cast<int>(of) - h * row_tiles;
             const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (end - u)));
             if (first && lane == 0)
               P.ws.starts[run] = Start{b, h, row_tile, t0, tiles, n, {0, 0}};
@@ -822,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quarter * 32 + lane;  // of the stream's tile
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const float c = P.scale_log2;
-    uint32_t tile = 0, scores[2] = {0, 0};  // scores: tiles of each stream so far
+    uint32_t tile = 0, jobs = 0, scores[2] = {0, 0};  // scores: tiles of each stream so far
     while (true) {
       const uint32_t item = items;
       const Item& given = next_item();
@@ -860,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mixed && (!kPair || st == 0)) {
           // A value that is not finite would pass through a weight of 0 into rows that do
           // not see its node: it becomes 0 here and comes back, at the end, for those that do.
-          const uint32_t job = 2 * tile + 1, stage = job % kStages;
+          const uint32_t job = jobs + S::value_job(t - w.t0, w.t1 - w.t0), stage = job % kStages;
           barrier_wait(smem_of(&s.kv_full[stage]), job / kStages & 1, gave_up);
           char* v = smem + S::kStageAt + stage * S::kTileBytes;
           const int from = max(w.len - t * kKeys, 0), to = min(keys - t * kKeys, kKeys);
@@ -974,6 +1003,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) barrier_arrive(smem_of(&s.p_full[st][1]));
         scores[st]++;
       }
+
+      jobs += 2 * (w.t1 - w.t0);
 
       // The item's end: both streams' last updates, and what they know.
       if (!kPair) scores[st ^ 1] += taken[st ^ 1];
@@ -1126,6 +1157,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) finish_kernel(const AttnPar
     const int slot = i == 0 ? 2 * (run - 1) + 1 : 2 * (run + i - 1);
     return static_cast<int64_t>(slot) * P.part_rows + min(row0 + r, rows - 1);
   };
+  // the pieces' weights, a piece to a lane, then their sums
   float m[kFinishRows], l[kFinishRows];
   float4 o[kFinishRows];
 #pragma unroll
@@ -1135,27 +1167,40 @@ __global__ void __launch_bounds__(kFinishWarps * 32) finish_kernel(const AttnPar
     o[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
   const int d = 4 * lane;
-  // pieces one by one, the sums rescaled where the maximum rises
-#pragma unroll 2
-  for (int i = 0; i < pieces; i++) {
+  for (int i0 = 0; i0 < pieces; i0 += 32) {
     float2 ml[kFinishRows];
-    float4 x[kFinishRows];
+    float weight[kFinishRows];
+#pragma unroll
+    for (int r = 0; r < kFinishRows; r++)
+      ml[r] = i0 + lane < pieces ? P.ws.stats[index(i0 + lane, r)] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
     for (int r = 0; r < kFinishRows; r++) {
-      ml[r] = P.ws.stats[index(i, r)];
-      if (d < DP) x[r] = *reinterpret_cast<const float4*>(P.ws.parts + index(i, r) * DP + d);
-    }
+      float top = ml[r].x, sum;
 #pragma unroll
-    for (int r = 0; r < kFinishRows; r++) {
-      const float top = fmaxf(m[r], ml[r].x);
+      for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
+      top = fmaxf(top, m[r]);
+      weight[r] = ml[r].x == top ? 1.0f : exp2_of(ml[r].x - top);
+      sum = weight[r] * ml[r].y;
+#pragma unroll
+      for (int x = 16; x > 0; x /= 2) sum += __shfl_xor_sync(kFullMask, sum, x);
       const float old = m[r] == top ? 1.0f : exp2_of(m[r] - top);
-      const float weight = ml[r].x == top ? 1.0f : exp2_of(ml[r].x - top);
       m[r] = top;
-      l[r] = l[r] * old + weight * ml[r].y;
-      o[r].x = o[r].x * old + weight * x[r].x;
-      o[r].y = o[r].y * old + weight * x[r].y;
-      o[r].z = o[r].z * old + weight * x[r].z;
-      o[r].w = o[r].w * old + weight * x[r].w;
+      l[r] = l[r] * old + sum;
+      o[r].x *= old, o[r].y *= old, o[r].z *= old, o[r].w *= old;
+    }
+    const int here = min(32, pieces - i0);
+#pragma unroll 4
+    for (int i = 0; i < here; i++) {
+#pragma unroll
+      for (int r = 0; r < kFinishRows; r++) {
+        const float by = __shfl_sync(kFullMask, weight[r], i);
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (d < DP) x = *reinterpret_cast<const float4*>(P.ws.parts + index(i0 + i, r) * DP + d);
+        o[r].x = fmaf(by, x.x, o[r].x);
+        o[r].y = fmaf(by, x.y, o[r].y);
+        o[r].z = fmaf(by, x.z, o[r].z);
+        o[r].w = fmaf(by, x.w, o[r].w);
+      }
     }
   }
   if (d >= P.cache.head_dim) return;
