@@ -21,9 +21,9 @@
 //
 // Two streams share an SM, each with its S and O in TMEM and its four softmax
 // warps: with up to 128 rows they take the key tiles in turn and are joined
-// at the end (kPair false), with more they are two row tiles on the same keys
-// (kPair true).  Of the other warps four copy, one thread issues the MMAs, one
-// warp deals out the work and two check the requests' data beside it all.
+// at the end, with more they are two row tiles on the same keys
+// (kPair).  Of the other warps four copy, two threads issue the MMAs, one
+// warp deals out the work and one checks the requests' data beside it all.
 
 #include <cuda.h>
 
@@ -39,12 +39,14 @@ constexpr int kKeys = 128;     // keys of a tile
 constexpr int kRows = 128;     // query rows of a stream
 constexpr int kMaxCtas = 152;  // SMs of a GB300
 constexpr int kLoadWarps = 4;
-constexpr int kLoadWarp = 8;  // the first of them
-constexpr int kMmaWarp = 12;
-constexpr int kDealWarp = 13;
-constexpr int kCheckWarp = 14;  // and 15
+constexpr int kLoadWarp = 8;  // the first of them; the last makes the tensor copies
+constexpr int kCheckWarp = 12;
+constexpr int kScoreWarp = 13;  // issues S = Q K^T
+constexpr int kSumWarp = 14;    // issues O += P V
+constexpr int kDealWarp = 15;
 constexpr int kThreads = 512;
 constexpr int kItems = 4;  // items dealt out ahead
+constexpr int kNear = 3;   // key tiles before an item's end at which the next run is called for
 // Registers a thread of each warpgroup: 2 * 200 + 56 + 56 = 512 = 4 * 128, what
 // the block is launched with.  The softmax keeps a row of scores in them.
 #define SPECV_REGS_SOFTMAX "200"
@@ -57,7 +59,7 @@ constexpr float kRise = 8.0f;  // log2 of how far a maximum may rise before O is
 struct Header {
   int32_t next;     // dealt runs so far; 0 between calls
   int32_t timeout;  // a wait gave up in this call
-  int64_t total;    // units of this call
+  int32_t count, even, dealt;  // of this call's runs (struct Runs)
 };
 
 // Where a run begins: the item, its key tile, and what the item is.
@@ -88,28 +90,40 @@ struct AttnParams {
 };
 
 // How the units are cut into runs.  Few units (under 8 for each CTA) are cut
-// evenly; of more, a share is cut evenly and the rest is dealt out.
+// evenly; of more, a share is cut evenly and the rest is dealt out.  An even
+// cut that falls into an item of at most half a run moves to the item's
+// beginning: what is uneven by that the dealing evens out.
 struct Runs {
-  int64_t total, even, dealt;  // lengths of the two kinds of runs
+  int64_t total;
+  int even, dealt;  // lengths of the two kinds of runs
   int ctas, count;
 
-  __device__ __forceinline__ Runs(const AttnParams& P, int64_t units) : total(units), ctas(P.ctas) {
-    even = (total + ctas - 1) / ctas;
-    dealt = 1;
+  __device__ __forceinline__ Runs(const AttnParams& P, int64_t units)
+      : total(units), dealt(1), ctas(P.ctas) {
     if (total >= 8 * ctas && P.dealt > 0) {
       // about 3/4 and, where pieces are small and more of them cost little, 3/5
-      even = P.dealt > ctas ? total * 3 / (5 * ctas) : total * 3 / (4 * ctas);
-      dealt = (total - even * ctas + P.dealt - 1) / P.dealt;
-      count = ctas + static_cast<int>((total - even * ctas + dealt - 1) / dealt);
+      even = quotient(total, ctas);
+      even = P.dealt > ctas ? even / 5 * 3 : even / 4 * 3;
+      const int64_t rest = total - static_cast<int64_t>(even) * ctas;
+      dealt = quotient(rest + P.dealt - 1, P.dealt);
+      count = ctas + quotient(rest + dealt - 1, dealt);
     } else {
-      count = total ? static_cast<int>((total + even - 1) / even) : 0;
+      even = quotient(total + ctas - 1, ctas);
+      count = total ? quotient(total + even - 1, even) : 0;
     }
   }
-  __device__ __forceinline__ int64_t start(int run) const {
-    return run < ctas ? run * even : ctas * even + (run - ctas) * dealt;
+  static __device__ __forceinline__ int quotient(int64_t a, int b) {
+    return a >> 32 ? static_cast<int>(a / b)
+                   : static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
   }
-  __device__ __forceinline__ int64_t length(int run) const {
-    return min(run < ctas ? even : dealt, total - start(run));
+  // Where run `run` begins, and run - 1 ends, but for the moves.
+  __device__ __forceinline__ int64_t start(int run) const {
+    return min(total, run < ctas ? static_cast<int64_t>(run) * even
+                                 : static_cast<int64_t>(ctas) * even +
+                                       static_cast<int64_t>(run - ctas) * dealt);
+  }
+  __device__ __forceinline__ bool moves(int run, int tiles) const {
+    return run <= ctas && count > ctas && 2 * tiles <= even;
   }
 };
 
@@ -355,13 +369,19 @@ __device__ __forceinline__ float exp2_of(float x) {
 
 // --------------------------------------------------------------- attention
 
-template <int DP, bool kPair> struct Shape {
-  static constexpr int kTileBytes = kKeys * DP * 2;  // of keys, of values or of queries
-  static constexpr int kStages = DP == 128 ? 5 : 10;
-  static constexpr int kRowTile = kPair ? 2 * kRows : kRows;
+// kMode: 0 at most 64 query rows, 1 at most 128, 2 more (kPair).
+template <int DP, int kMode> struct Shape {
+  static constexpr bool kPair = kMode == 2;
+  static constexpr int kTileBytes = kKeys * DP * 2;  // of keys or of values
+  // Few queries leave room for a sixth tile.  (The MMA reads 128 rows all the
+  // same: what lies behind makes scores of rows that nobody reads.)
+  static constexpr int kQueryRows = kMode == 0 ? 64 : kRows;
+  static constexpr int kQueryBytes = kQueryRows * DP * 2;
+  static constexpr int kStages = (kMode == 0 ? 6 : 5) * (128 / DP);
+  static constexpr int kRowTile = kPair ? 2 * kRows : kMode == 0 ? 64 : kRows;
   // shared memory: queries (two tiles: both row tiles, or this and the next item's), stages,
   // then the barriers and what the warps tell one another
-  static constexpr int kStageAt = 2 * kTileBytes;
+  static constexpr int kStageAt = 2 * kQueryBytes;
   static constexpr int kTailAt = kStageAt + kStages * kTileBytes;
 
   // The order of an item's tiles in the ring, that of the MMAs that read them.
@@ -394,6 +414,7 @@ template <int kStages> struct Tail {
   uint64_t odd_values[2];  // nodes whose values were not finite, by parity of the item
   unsigned long long total;
   int gave_up;
+  int ending;  // items whose copies are near their end
   uint32_t tmem;
   Item items[kItems];
   float2 stats[2][kRows];
@@ -417,11 +438,12 @@ __device__ __forceinline__ uint32_t seen_of(int first, uint64_t visible) {
   return first < 64 ? static_cast<uint32_t>(visible >> first) : 0u;
 }
 
-template <class E, int DP, bool kPair>
+template <class E, int DP, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const AttnParams P, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
-  using S = Shape<DP, kPair>;
+  using S = Shape<DP, kMode>;
+  constexpr bool kPair = S::kPair;
   constexpr int kStages = S::kStages;
   // weights in f16 go below 2^-14, where its steps stop shrinking: taken 2^7 larger
   // they reach 2^15 at most (2^kRise more than the maximum's)
@@ -449,15 +471,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; i++) {
       barrier_init(smem_of(&s.item_full[i]), 1);
-      barrier_init(smem_of(&s.item_empty[i]), kLoadWarps + 1 + 8);
+      barrier_init(smem_of(&s.item_empty[i]), kLoadWarps + 2 + 8);
     }
-    barrier_init(smem_of(&s.drained), 1);
+    s.ending = 0;
+    barrier_init(smem_of(&s.drained), 2);
     s.gave_up = 0;
     s.total = 0;
     if (blockIdx.x == 0) P.ws.header->timeout = 0;  // set two seconds from now at the earliest
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_of(&s.tmem))
                  : "memory");
@@ -479,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tS[2] = {tmem, tmem + 128};
   const uint32_t tO[2] = {tmem + 256, tmem + 256 + DP};
   volatile int* gave_up = &s.gave_up;
+  volatile int* near_end = &s.ending;
   // The next item of this thread's warp; lane 0 gives it back when it is done.
   uint32_t items = 0;
   auto next_item = [&]() -> const Item& {
@@ -492,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto over = [&](const Item& w) { return w.t0 < 0 || *gave_up; };
 
-  if (warp >= kLoadWarp && warp < kMmaWarp) {
+  if (warp >= kLoadWarp && warp < kCheckWarp) {
     // ------------------------------------------------------------- copies
     asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_REGS_LOAD ";");
     // Copies of 16 bytes, so that pages of any size and strides of any kind will
@@ -504,10 +528,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t jobs = 0;  // before this item
     // 128-byte rows, their 16-byte pieces swapped by the row's number: rows
     // kRowsAtOnce apart, and sub < kRowsAtOnce, so r and sub set bits of their own
-    const uint32_t lane_at = (piece / 8) * (kKeys * 128) + (32 * lw + sub) * 128;
     const uint32_t swap = (piece % 8) ^ sub;
-    auto tile_copy = [&](uint32_t to, const uint16_t* from, int64_t off) {
+    auto tile_copy = [&](uint32_t to, int tile_rows, const uint16_t* from, int64_t off) {
       // this lane's row is 32 lw + lane of the tile, at from + off (off < 0: none)
+      const uint32_t lane_at = (piece / 8) * (tile_rows * 128) + (32 * lw + sub) * 128;
 #pragma unroll
       for (int r = 0; r < 32; r += kRowsAtOnce) {
         const int64_t o = __shfl_sync(kFullMask, off, r + sub);
@@ -531,10 +555,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int node = at / P.group, g = at - node * P.group;
         const int64_t off = w.b * P.q.batch_stride + node * P.q.node_stride +
                             (w.h * P.group + g) * P.q.head_stride;
-        tile_copy(base + (kPair ? half : q_buffer) * S::kTileBytes, P.q.data, real ? off : -1);
+        if (32 * lw < S::kQueryRows)
+          tile_copy(base + (kPair ? half : q_buffer) * S::kQueryBytes, S::kQueryRows, P.q.data,
+                    real ? off : -1);
       }
       copies_arrive(smem_of(&s.q_full[q_buffer]));
       const int keys = w.len + w.n, t1 = w.t1;
+      const int ending = max(w.t0, t1 - kNear);  // the tile whose copy calls for the next run
       const int32_t* table = C.page_table + static_cast<int64_t>(w.b) * C.table_stride;
       // Page numbers are read a tile ahead of their use; one out of range (its
       // request is flagged elsewhere) is no page.
@@ -547,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Tensor copies: lane l < boxes brings box l % per_half of 64-column half
         // l / per_half.  A page's rows behind the last key come along; the
         // softmax clears their values.
-        if (lw == 0) {
+        if (lw == kLoadWarps - 1) {
           const int per_half = kKeys / P.box_rows, boxes = per_half * (DP / 64);
           const int box = lane % per_half, half = lane / per_half;
           const int at = box * P.box_rows;
@@ -570,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int page_before = -1;
           for (int t = w.t0; t < t1; t++) {
             const int i = t - w.t0;
+            if (t == ending && lane == 0) *near_end = items + 1;
             copy(S::key_job(i), &k_map, page, t);
             if (kPair) copy(S::value_job(i, t1 - w.t0), &v_map, page, t);
             else if (i > 0) copy(S::value_job(i - 1, t1 - w.t0), &v_map, page_before, t - 1);
@@ -586,12 +614,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto copy = [&](uint32_t job, const uint16_t* from, int64_t off) {
           const uint32_t stage = (jobs + job) % kStages, use = (jobs + job) / kStages;
           barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
-          tile_copy(base + S::kStageAt + stage * S::kTileBytes, from, off);
+          tile_copy(base + S::kStageAt + stage * S::kTileBytes, kKeys, from, off);
           copies_arrive(smem_of(&s.kv_full[stage]));
         };
         int64_t before = -1;
         for (int t = w.t0; t < t1; t++) {
           const int i = t - w.t0;
+          if (t == ending && lane == 0 && lw == kLoadWarps - 1) *near_end = items + 1;
           const int64_t off = page < 0 ? static_cast<int64_t>(-1)
                                        : page * C.page_stride +
                                              key_of(t) % C.page_size * C.row_stride +
@@ -614,55 +643,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (P.box_rows && *gave_up)
       for (uint32_t k = jobs < kStages ? 0 : jobs - kStages; k < jobs; k++)
         barrier_wait_own(smem_of(&s.kv_full[k % kStages]), k / kStages & 1);
-  } else if (warp >= kMmaWarp) {
+  } else if (warp >= kCheckWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_REGS_OTHER ";");
     // --------------------------------------------------------------- MMAs
     constexpr uint32_t kType = std::is_same<E, Bf16>::value ? 1 : 0;
     constexpr uint32_t kIdesc = 1u << 4 | kType << 7 | kType << 10 | (kRows >> 4) << 24;
     constexpr uint32_t kIdescS = kIdesc | (kKeys >> 3) << 17;
     constexpr uint32_t kIdescO = kIdesc | 1u << 16 | (DP >> 3) << 17;
-    if (warp == kMmaWarp && lane == 0) {
+    // Two threads, that neither waits for what the other issues: scores of a tile
+    // when its stream's last sum has left S, sums when the weights are there.
+    auto stage_at = [&](uint32_t job) { return base + S::kStageAt + job % kStages * S::kTileBytes; };
+    auto kv_wait = [&](uint32_t job) {
+      barrier_wait(smem_of(&s.kv_full[job % kStages]), job / kStages & 1, gave_up);
+      // copies of 16 bytes wrote through the generic proxy, the MMA reads through the other
+      if (!P.box_rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    };
+    uint32_t tile = 0, jobs = 0;  // key tiles so far, copies before this item
+    uint32_t issued[2] = {0, 0};  // scores or sums of each stream so far
+    if (warp == kScoreWarp && lane == 0) {
       const int steps = (C.head_dim + 15) / 16;
-      uint32_t tile = 0, jobs = 0;    // key tiles so far, copies before this item
-      uint32_t weighted[2] = {0, 0};  // O updates of each stream so far
-      auto stage_at = [&](uint32_t job) { return base + S::kStageAt + job % kStages * S::kTileBytes; };
-      auto kv_wait = [&](uint32_t job) {
-        barrier_wait(smem_of(&s.kv_full[job % kStages]), job / kStages & 1, gave_up);
-        // copies of 16 bytes wrote through the generic proxy, the MMA reads through the other
-        if (!P.box_rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      };
-      auto qk = [&](int st, uint32_t q_at, uint32_t k_at) {
+      auto scores = [&](int st, uint32_t q_at, uint32_t k_at) {
+        if (issued[st]) barrier_wait(smem_of(&s.o_full[st]), (issued[st] - 1) & 1, gave_up);
+        tmem_fence_after();
         const uint32_t a = operand_low(q_at, 16), b = operand_low(k_at, 16);
         mma_ss<false>(tS[st], a, b, kIdescS);
 #pragma unroll
         for (int k = 1; k < DP / 16; k++) {
-          const uint32_t step = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
-          if (k < steps) mma_ss<true>(tS[st], a + step, b + step, kIdescS);
+          const uint32_t q_step = ((k / 4) * (S::kQueryRows * 128) + (k % 4) * 32) >> 4;
+          const uint32_t k_step = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
+          if (k < steps) mma_ss<true>(tS[st], a + q_step, b + k_step, kIdescS);
         }
         mma_commit(smem_of(&s.s_full[st]));
-      };
-      auto pv = [&](int st, uint32_t v_at, bool first) {
-        const uint32_t b = operand_low(v_at, kKeys * 128);
-#pragma unroll
-        for (int half = 0; half < 2; half++) {
-          barrier_wait(smem_of(&s.p_full[st][half]), weighted[st] & 1, gave_up);
-          tmem_fence_after();
-#pragma unroll
-          for (int k = half * kKeys / 32; k < (half + 1) * kKeys / 32; k++)
-            mma_ts(tO[st], tS[st] + 8 * k, b + (k * 2048 >> 4), kIdescO, k > 0 || !first);
-        }
-        mma_commit(smem_of(&s.o_full[st]));
-        weighted[st]++;
-      };
-      // the update that is due: a tile's values wait until the next tile's scores are issued
-      bool due = false, due_first = false;
-      uint32_t due_job = 0;
-      bool due_second = false;  // kPair: the item has rows for stream 1
-      auto last_pair = [&](uint32_t v_job) {
-        kv_wait(v_job);
-        pv(0, stage_at(v_job), due_first);
-        if (due_second) pv(1, stage_at(v_job), due_first);
-        mma_commit(smem_of(&s.kv_empty[v_job % kStages]));
+        issued[st]++;
       };
       while (true) {
         const uint32_t item = items;
@@ -671,60 +683,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q_buffer = kPair ? 0 : item & 1;
         const uint32_t q_use = kPair ? item : item / 2;
         const bool second = kPair && w.rows(P.group, S::kRowTile) > kRows;
-        const int t0 = w.t0, t1 = w.t1;
+        const int tiles = w.t1 - w.t0;
         done_item();
-        bool started[2] = {false, false};
-        if (kPair && due) {  // the queries have one buffer: nothing to issue before they are there
-          last_pair(due_job);
-          due = false;
-        }
         barrier_wait(smem_of(&s.q_full[q_buffer]), q_use & 1, gave_up);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (int t = t0; t < t1; t++, tile++) {
-          // this tile's keys, the last one's values
-          const uint32_t k_job = jobs + S::key_job(t - t0), v_job = due_job;
+        for (int i = 0; i < tiles; i++, tile++) {
+          const uint32_t job = jobs + S::key_job(i);
+          kv_wait(job);
           if (kPair) {
-            if (due) {
-              kv_wait(v_job);
-              pv(0, stage_at(v_job), due_first);
-            }
-            kv_wait(k_job);
-            qk(0, base, stage_at(k_job));
-            if (due && due_second) pv(1, stage_at(v_job), due_first);
-            if (due) mma_commit(smem_of(&s.kv_empty[v_job % kStages]));
-            if (second) qk(1, base + S::kTileBytes, stage_at(k_job));
-            mma_commit(smem_of(&s.kv_empty[k_job % kStages]));
-            due_first = t == t0;
-            due_second = second;
+            scores(0, base, stage_at(job));
+            if (second) scores(1, base + S::kQueryBytes, stage_at(job));
           } else {
-            const int st = tile & 1;
-            kv_wait(k_job);
-            qk(st, base + q_buffer * S::kTileBytes, stage_at(k_job));
-            mma_commit(smem_of(&s.kv_empty[k_job % kStages]));
-            if (due) {
-              kv_wait(v_job);
-              pv(st ^ 1, stage_at(v_job), due_first);
-              mma_commit(smem_of(&s.kv_empty[v_job % kStages]));
-            }
-            due_first = !started[st];
-            started[st] = true;
+            scores(tile & 1, base + q_buffer * S::kQueryBytes, stage_at(job));
           }
-          due = true;
-          due_job = jobs + S::value_job(t - t0, t1 - t0);
+          mma_commit(smem_of(&s.kv_empty[job % kStages]));
         }
-        jobs += 2 * (t1 - t0);
+        jobs += 2 * tiles;
         mma_commit(smem_of(&s.q_empty[q_buffer]));
       }
-      if (due) {
-        if (kPair) {
-          last_pair(due_job);
-        } else {
-          kv_wait(due_job);
-          pv((tile - 1) & 1, stage_at(due_job), due_first);
-          mma_commit(smem_of(&s.kv_empty[due_job % kStages]));
-        }
-      }
       // every MMA and every arrival that waits for one must find this CTA's memory
+      mma_commit(smem_of(&s.drained));
+      barrier_wait_own(smem_of(&s.drained), 0);
+    }
+    if (warp == kSumWarp && lane == 0) {
+      auto sums = [&](int st, uint32_t v_at, bool first) {
+        const uint32_t b = operand_low(v_at, kKeys * 128);
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          barrier_wait(smem_of(&s.p_full[st][half]), issued[st] & 1, gave_up);
+          tmem_fence_after();
+#pragma unroll
+          for (int k = half * kKeys / 32; k < (half + 1) * kKeys / 32; k++)
+            mma_ts(tO[st], tS[st] + 8 * k, b + (k * 2048 >> 4), kIdescO, k > 0 || !first);
+        }
+        mma_commit(smem_of(&s.o_full[st]));
+        issued[st]++;
+      };
+      while (true) {
+        const Item& w = next_item();
+        if (over(w)) break;
+        const bool second = kPair && w.rows(P.group, S::kRowTile) > kRows;
+        const int tiles = w.t1 - w.t0;
+        done_item();
+        for (int i = 0; i < tiles; i++, tile++) {
+          const uint32_t job = jobs + S::value_job(i, tiles);
+          kv_wait(job);
+          if (kPair) {
+            sums(0, stage_at(job), i == 0);
+            if (second) sums(1, stage_at(job), i == 0);
+          } else {
+            sums(tile & 1, stage_at(job), i < 2);
+          }
+          mma_commit(smem_of(&s.kv_empty[job % kStages]));
+        }
+        jobs += 2 * tiles;
+      }
       mma_commit(smem_of(&s.drained));
       barrier_wait_own(smem_of(&s.drained), 0);
     }
@@ -732,13 +745,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ dealing
     if (warp == kDealWarp) {
       const Runs runs(P, static_cast<int64_t>(s.total));
-      if (blockIdx.x == 0 && lane == 0) P.ws.header->total = runs.total;
+      if (blockIdx.x == 0 && lane == 0) {
+        P.ws.header->count = runs.count;
+        P.ws.header->even = runs.even;
+        P.ws.header->dealt = runs.dealt;
+      }
       int b = 0;         // the request where the search is, ...
       int64_t before = 0;  // ... and the units before it
       bool stop = false;
       for (int run = blockIdx.x; run < runs.count && !stop;) {
         int64_t u = runs.start(run);
-        const int64_t end = u + runs.length(run);
+        const int64_t end = runs.start(run + 1);
         bool first = true;
         while (u < end && !stop) {
           // the request with unit u: 32 requests at a time
@@ -780,6 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (P.parents && i < n) parent = P.parents[static_cast<int64_t>(b) * P.N + i];
             up[k] = static_cast<uint8_t>(parent >= 0 && parent < i ? parent : 0);
           }
+          if (first && runs.moves(run, tiles)) {
+            const int64_t off = u - before;
+            u -= off >> 32 ? off % tiles : static_cast<uint32_t>(off) % tiles;
+          }
           while (u < end && u < before + units) {
             const int64_t off = u - before;
             const int64_t of = off >> 32 ? off / tiles : static_cast<uint32_t>(off) / tiles;
@@ -787,6 +808,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int h = static_cast<int>(of) / row_tiles;  // below 1024 heads * 512 row tiles
             const int row_tile = static_cast<int>(of) - h * row_tiles;
             const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (end - u)));
+            if (t1 < tiles && runs.moves(run + 1, tiles)) {  // the next run has all of it
+              u = end;
+              break;
+            }
             if (first && lane == 0)
               P.ws.starts[run] = Start{b, h, row_tile, t0, tiles, n, {0, 0}};
             first = false;
@@ -814,9 +839,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             u += t1 - t0;
           }
         }
-        // Not before the copies of this run's last item are on their way: a run taken
-        // early is one that an idle CTA does not find.
-        barrier_wait(smem_of(&s.item_empty[(items - 1) % kItems]), (items - 1) / kItems & 1, gave_up);
+        // Not before the copies are near this run's end: a run taken early is one that
+        // an idle CTA does not find.
+        for (const uint64_t since = now_ns(); *near_end < static_cast<int>(items) && !*gave_up;) {
+          __nanosleep(100);
+          if (now_ns() - since > 2000000000ull) *gave_up = 1;
+        }
+        __syncwarp();
         const int dealt =
             __shfl_sync(kFullMask, lane == 0 ? atomicAdd(&P.ws.header->next, 1) : 0, 0);
         if (dealt < 0) break;  // a workspace that was not zeroed
@@ -832,8 +861,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // ----------------------------------------------------------- checking
-    if (warp >= kCheckWarp) {
-      for (int b = blockIdx.x * 2 + warp - kCheckWarp; b < P.B; b += 2 * gridDim.x) {
+    if (warp == kCheckWarp) {
+      for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
         Tree t = read_tree(P.parents, P.n_nodes, C.lens, b, P.N,
                            static_cast<int64_t>(C.max_pages) * C.page_size, lane);
         if (!t.bad && __any_sync(kFullMask, bad_pages(C, b, 0, t.len + t.n, lane, 32)))
@@ -1106,7 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && *gave_up) P.ws.header->timeout = 1;
   tmem_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
@@ -1143,16 +1172,17 @@ __global__ void __launch_bounds__(kFinishWarps * 32) finish_kernel(const AttnPar
   }
   const int block = blockIdx.x - P.B, run = 1 + block / groups;
   const Start at = P.ws.starts[run], before = P.ws.starts[run - 1];
-  const Runs runs(P, header->total);
-  if (run >= runs.count || at.t0 == 0) return;  // no cut here
+  const int count = header->count, even = header->even, dealt = header->dealt;
+  if (run >= count || at.t0 == 0) return;  // no cut here
   if (before.b == at.b && before.h == at.h && before.row_tile == at.row_tile && before.t0 != 0)
     return;  // not the item's first
   const int row0 = (block % groups * kFinishWarps + tid / 32) * kFinishRows;
   const int rows = min(kRowTile, at.n * P.group - at.row_tile * kRowTile);
   if (row0 >= rows || P.ws.bad[at.b]) return;
-  int pieces = 2;  // one ends the run before, the others begin a run each
-  for (int64_t left = at.tiles - at.t0; left > runs.length(run + pieces - 2); pieces++)
-    left -= runs.length(run + pieces - 2);
+  // one piece ends the run before, the others begin a run each: even ones, then dealt ones
+  const int left = at.tiles - at.t0, evens = max(P.ctas - run, 0);
+  int pieces = 1 + min(evens, (left + even - 1) / even);
+  if (left > static_cast<int64_t>(evens) * even) pieces += (left - evens * even + dealt - 1) / dealt;
   auto index = [&](int i, int r) {
     const int slot = i == 0 ? 2 * (run - 1) + 1 : 2 * (run + i - 1);
     return static_cast<int64_t>(slot) * P.part_rows + min(row0 + r, rows - 1);
@@ -1221,15 +1251,14 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // The shape of the work that B, N and the heads give, whatever the lengths are.
 struct Plan {
-  bool pair;
-  int dim, part_rows, dealt;
+  int mode, dim, row_tile, part_rows, dealt;
   size_t bad, starts, stats, parts, total;  // offsets in the workspace
 
   Plan(int B, int N, int group, int head_dim) {
     const int rows = N * group;
-    pair = rows > kRows;
+    mode = rows <= 64 ? 0 : rows <= kRows ? 1 : 2;
     dim = head_dim <= 64 ? 64 : 128;
-    const int row_tile = pair ? 2 * kRows : kRows;
+    row_tile = mode == 0 ? 64 : mode == 1 ? kRows : 2 * kRows;
     part_rows = (rows < row_tile ? rows : row_tile) + 7 & ~7;
     // a piece of many rows is as large as a key tile: then fewer of them
     dealt = part_rows > 64 ? kMaxCtas : 3 * kMaxCtas;
@@ -1274,16 +1303,16 @@ bool tensor_map(CUtensorMap* map, const specv_cache* c, void* data, int box_rows
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class E, int DP, bool kPair>
+template <class E, int DP, int kMode>
 cudaError_t run(const AttnParams& P, const CUtensorMap& k_map, const CUtensorMap& v_map,
                 cudaStream_t stream) {
-  using S = Shape<DP, kPair>;
+  using S = Shape<DP, kMode>;
   constexpr int kSmem = S::kTailAt + static_cast<int>(sizeof(Tail<S::kStages>));
   static_assert(kSmem <= 232448, "one CTA's shared memory");
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<E, DP, kPair>,
+  cudaError_t e = cudaFuncSetAttribute(attention_kernel<E, DP, kMode>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  attention_kernel<E, DP, kPair><<<P.ctas, kThreads, kSmem, stream>>>(P, k_map, v_map);
+  attention_kernel<E, DP, kMode><<<P.ctas, kThreads, kSmem, stream>>>(P, k_map, v_map);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -1303,8 +1332,12 @@ template <class E>
 cudaError_t run_any(const AttnParams& P, const Plan& plan, const CUtensorMap& k, const CUtensorMap& v,
                     cudaStream_t stream) {
   if (plan.dim == 64)
-    return plan.pair ? run<E, 64, true>(P, k, v, stream) : run<E, 64, false>(P, k, v, stream);
-  return plan.pair ? run<E, 128, true>(P, k, v, stream) : run<E, 128, false>(P, k, v, stream);
+    return plan.mode == 0   ? run<E, 64, 0>(P, k, v, stream)
+           : plan.mode == 1 ? run<E, 64, 1>(P, k, v, stream)
+                            : run<E, 64, 2>(P, k, v, stream);
+  return plan.mode == 0   ? run<E, 128, 0>(P, k, v, stream)
+         : plan.mode == 1 ? run<E, 128, 1>(P, k, v, stream)
+                          : run<E, 128, 2>(P, k, v, stream);
 }
 
 }  // namespace
@@ -1355,7 +1388,7 @@ specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
     box_rows = 0;
   // Where no length can give eight units to a CTA, no run is dealt out.
   const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * page + kKeys - 1) / kKeys;
-  const int row_tiles = (N * group + (plan.pair ? 2 * kRows : kRows) - 1) / (plan.pair ? 2 * kRows : kRows);
+  const int row_tiles = (N * group + plan.row_tile - 1) / plan.row_tile;
   const bool deals = static_cast<int64_t>(B) * cache->heads * row_tiles * tiles >= 8 * ctas;
   const AttnParams P{to_cache(cache),
                      to_rows(q),
