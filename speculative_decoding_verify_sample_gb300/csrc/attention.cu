@@ -17,7 +17,7 @@
 // runs that the CTAs take off a counter as they finish, for equal runs do not
 // take equal time (with 80 units each, 121 to 172 us).  A row tile whose keys
 // one run has whole is written out; pieces leave (m, l, O) in the workspace for
-// finish_kernel.
+// join_kernel.
 //
 // Two streams share an SM, each with its S and O in TMEM and its four softmax
 // warps: with up to 128 rows they take the key tiles in turn and are joined
@@ -57,20 +57,20 @@ constexpr float kRise = 8.0f;  // log2 of how far a maximum may rise before O is
 // ---------------------------------------------------------------- the work
 
 struct Header {
-  int32_t next;     // dealt runs so far; 0 between calls
-  int32_t timeout;  // a wait gave up in this call
-  int32_t count, even, dealt;  // of this call's runs (struct Runs)
+  int32_t next;   // runs dealt out so far; 0 between calls
+  int32_t count;  // of this call's runs
 };
 
-// Where a run begins: the item, its key tile, and what the item is.
-struct Start {
-  int32_t b, h, row_tile, t0, tiles, n, pad[2];
+// Where a run begins in the middle of an item: the item's second piece.
+struct Cut {
+  int32_t b, h, row_tile, n;
+  int32_t pieces;  // of the item; 0: the run does not begin its second piece
+  int32_t pad[3];
 };
 
 struct Workspace {
   Header* header;
-  int32_t* bad;   // [B] SPECV_DEV_* bits
-  Start* starts;  // [runs]
+  Cut* cuts;      // [runs]
   float2* stats;  // [2 runs][part_rows] pieces' m c and l: of an item that began before the
   float* parts;   // [2 runs][part_rows][dim]   run, then of one that goes on behind it; their O
 };
@@ -90,9 +90,7 @@ struct AttnParams {
 };
 
 // How the units are cut into runs.  Few units (under 8 for each CTA) are cut
-// evenly; of more, a share is cut evenly and the rest is dealt out.  An even
-// cut that falls into an item of at most half a run moves to the item's
-// beginning: what is uneven by that the dealing evens out.
+// evenly; of more, a share is cut evenly and the rest is dealt out.
 struct Runs {
   int64_t total;
   int even, dealt;  // lengths of the two kinds of runs
@@ -116,14 +114,16 @@ struct Runs {
     return a >> 32 ? static_cast<int>(a / b)
                    : static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
   }
-  // Where run `run` begins, and run - 1 ends, but for the moves.
+  // Where run `run` begins, and run - 1 ends.
   __device__ __forceinline__ int64_t start(int run) const {
     return min(total, run < ctas ? static_cast<int64_t>(run) * even
                                  : static_cast<int64_t>(ctas) * even +
                                        static_cast<int64_t>(run - ctas) * dealt);
   }
-  __device__ __forceinline__ bool moves(int run, int tiles) const {
-    return run <= ctas && count > ctas && 2 * tiles <= even;
+  // Runs that units u .. are in, from `run` on, which has the first.
+  __device__ __forceinline__ int last(int run, int64_t end) const {
+    const int64_t evens = static_cast<int64_t>(ctas) * even;
+    return end <= evens ? quotient(end - 1, even) : max(run, ctas + quotient(end - 1 - evens, dealt));
   }
 };
 
@@ -157,6 +157,18 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
   asm volatile(
       "{\n .reg .pred p;\n"
       " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done;
+}
+
+__device__ __forceinline__ bool barrier_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}"
       : "=r"(done)
       : "r"(bar), "r"(parity)
@@ -398,7 +410,9 @@ template <int DP, int kMode> struct Shape {
 
 // All key tiles t0 .. t1-1 of a row tile that one run has.
 struct Item {
-  int32_t b, h, row_tile, t0, t1, tiles, len, n, run;  // t0 < 0: no more items
+  int32_t b, h, row_tile, t0, t1, tiles, len, n;  // t0 < 0: no more items
+  int32_t run, pieces;  // runs that have key tiles of it
+  int32_t bad;          // written by the checking warp
   uint8_t parents[kMaxNodes];                          // each below its node, whatever the input
 
   __device__ __forceinline__ int rows(int group, int row_tile_rows) const {
@@ -409,7 +423,7 @@ struct Item {
 template <int kStages> struct Tail {
   uint64_t kv_full[kStages], kv_empty[kStages], q_full[2], q_empty[2], s_full[2], o_full[2];
   uint64_t p_full[2][2];  // by stream and half of the keys
-  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t item_full[kItems], item_checked[kItems], item_empty[kItems];
   uint64_t drained;
   uint64_t odd_values[2];  // nodes whose values were not finite, by parity of the item
   unsigned long long total;
@@ -471,14 +485,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; i++) {
       barrier_init(smem_of(&s.item_full[i]), 1);
-      barrier_init(smem_of(&s.item_empty[i]), kLoadWarps + 2 + 8);
+      barrier_init(smem_of(&s.item_checked[i]), 1);
+      barrier_init(smem_of(&s.item_empty[i]), kLoadWarps + 3 + 8);
     }
     s.ending = 0;
     barrier_init(smem_of(&s.drained), 2);
     s.gave_up = 0;
     s.total = 0;
-    if (blockIdx.x == 0) P.ws.header->timeout = 0;  // set two seconds from now at the earliest
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 32 * kLoadWarp && P.box_rows) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
   }
   if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -745,18 +763,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ dealing
     if (warp == kDealWarp) {
       const Runs runs(P, static_cast<int64_t>(s.total));
-      if (blockIdx.x == 0 && lane == 0) {
-        P.ws.header->count = runs.count;
-        P.ws.header->even = runs.even;
-        P.ws.header->dealt = runs.dealt;
-      }
+      if (blockIdx.x == 0 && lane == 0) P.ws.header->count = runs.count;
       int b = 0;         // the request where the search is, ...
       int64_t before = 0;  // ... and the units before it
       bool stop = false;
       for (int run = blockIdx.x; run < runs.count && !stop;) {
         int64_t u = runs.start(run);
         const int64_t end = runs.start(run + 1);
-        bool first = true;
+        bool begins = true;
         while (u < end && !stop) {
           // the request with unit u: 32 requests at a time
           int tiles, row_tiles, len, n;
@@ -797,10 +811,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (P.parents && i < n) parent = P.parents[static_cast<int64_t>(b) * P.N + i];
             up[k] = static_cast<uint8_t>(parent >= 0 && parent < i ? parent : 0);
           }
-          if (first && runs.moves(run, tiles)) {
-            const int64_t off = u - before;
-            u -= off >> 32 ? off % tiles : static_cast<uint32_t>(off) % tiles;
-          }
           while (u < end && u < before + units) {
             const int64_t off = u - before;
             const int64_t of = off >> 32 ? off / tiles : static_cast<uint32_t>(off) / tiles;
@@ -808,13 +818,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int h = static_cast<int>(of) / row_tiles;  // below 1024 heads * 512 row tiles
             const int row_tile = static_cast<int>(of) - h * row_tiles;
             const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (end - u)));
-            if (t1 < tiles && runs.moves(run + 1, tiles)) {  // the next run has all of it
-              u = end;
-              break;
-            }
-            if (first && lane == 0)
-              P.ws.starts[run] = Start{b, h, row_tile, t0, tiles, n, {0, 0}};
-            first = false;
+            // runs before and behind with pieces of this item
+            int first_run = run, last_run = run;
+            if (t0 > 0) first_run = runs.last(0, u - t0 + 1);
+            if (t1 < tiles) last_run = runs.last(run, u - t0 + tiles);
             const uint32_t slot = items % kItems;
             barrier_wait(smem_of(&s.item_empty[slot]), (items / kItems & 1) ^ 1, gave_up);
             stop = __any_sync(kFullMask, *gave_up != 0);
@@ -832,10 +839,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               to.len = len;
               to.n = n;
               to.run = run;
+              to.pieces = last_run - first_run + 1;
+              if (begins)
+                P.ws.cuts[run] = Cut{b, h, row_tile, n,
+                                     t0 > 0 && first_run == run - 1 ? last_run - first_run + 1 : 0,
+                                     {0, 0, 0}};
             }
             __syncwarp();
             if (lane == 0) barrier_arrive(smem_of(&s.item_full[slot]));
             items++;
+            begins = false;
             u += t1 - t0;
           }
         }
@@ -861,16 +874,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // ----------------------------------------------------------- checking
+    // This CTA's share of all requests for their status, and every item's
+    // request for what its rows become, whenever an item is there.
     if (warp == kCheckWarp) {
-      for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
-        Tree t = read_tree(P.parents, P.n_nodes, C.lens, b, P.N,
-                           static_cast<int64_t>(C.max_pages) * C.page_size, lane);
+      const int64_t slots = static_cast<int64_t>(C.max_pages) * C.page_size;
+      auto check = [&](int b, int& n) {
+        Tree t = read_tree(P.parents, P.n_nodes, C.lens, b, P.N, slots, lane);
         if (!t.bad && __any_sync(kFullMask, bad_pages(C, b, 0, t.len + t.n, lane, 32)))
           t.bad |= SPECV_DEV_BAD_CACHE;
-        if (lane == 0) {
-          P.ws.bad[b] = static_cast<int32_t>(t.bad);
-          P.status[b] = static_cast<int32_t>(t.bad);
+        n = t.n;
+        return t.bad;
+      };
+      int next = blockIdx.x, last = -1, last_bad = 0, n;
+      auto report = [&]() {
+        const unsigned bad = check(next, n);
+        if (lane == 0) P.status[next] = static_cast<int32_t>(bad);
+        int len;
+        if (bad && nodes_of(P, next, len) == 0) {  // no item has its rows
+          n = n ? n : P.N;
+          const int words = C.head_dim / 8;
+          for (int e = lane; e < n * P.q_heads * words; e += 32) {
+            const int i = e / (P.q_heads * words), h = e / words % P.q_heads, d = e % words * 8;
+            *reinterpret_cast<uint4*>(P.out.data + next * P.out.batch_stride +
+                                      i * P.out.node_stride + h * P.out.head_stride + d) =
+                make_uint4(0, 0, 0, 0);
+          }
         }
+        next += gridDim.x;
+      };
+      while (true) {
+        const uint32_t slot = items % kItems;
+        if (next < P.B &&
+            !__any_sync(kFullMask, barrier_test(smem_of(&s.item_full[slot]), items / kItems & 1))) {
+          report();
+          continue;
+        }
+        Item& w = s.items[slot];
+        barrier_wait(smem_of(&s.item_full[slot]), items / kItems & 1, gave_up);
+        if (__any_sync(kFullMask, over(w))) {
+          while (next < P.B && !__any_sync(kFullMask, *gave_up != 0)) report();
+          break;
+        }
+        if (w.b != last) last_bad = static_cast<int>(check(w.b, n));
+        last = w.b;
+        if (lane == 0) w.bad = last_bad;
+        __syncwarp();
+        if (lane == 0) barrier_arrive(smem_of(&s.item_checked[slot]));
+        done_item();
       }
     }
   } else {
@@ -886,9 +936,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item& given = next_item();
       if (any_of_softmax(over(given))) break;  // all leave together
       const struct {
-        int b, h, row_tile, t0, t1, tiles, len, n, run;
-      } w = {given.b,     given.h,   given.row_tile, given.t0, given.t1,
-             given.tiles, given.len, given.n,        given.run};
+        int b, h, row_tile, t0, t1, tiles, len, n;
+      } w = {given.b, given.h, given.row_tile, given.t0, given.t1, given.tiles, given.len, given.n};
       const int rows = given.rows(P.group, S::kRowTile);
       const int first_row = kPair ? st * kRows : 0;
       const bool second = !kPair || rows > kRows;
@@ -898,8 +947,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t visible = 1;  // nodes that this row sees: its own and those above it
       if (w.t1 * kKeys > w.len)
         for (int i = node; i > 0; i = given.parents[i]) visible |= 1ull << i;
-      __syncwarp();
-      done_item();
       const int keys = w.len + w.n;
       uint64_t* odd = &s.odd_values[item & 1];
       int taken[2] = {0, 0};  // tiles of this item that each stream took
@@ -1048,10 +1095,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t fix = *odd & visible;
       const float2 other = s.stats[st ^ 1][row];
       if (tid == 0) s.odd_values[(item & 1) ^ 1] = 0;
-      if (tid == 0 && *gave_up) P.ws.header->timeout = 1;
+      if (tid == 0 && *gave_up) atomicOr(P.status + w.b, SPECV_DEV_TIMEOUT);
+      barrier_wait(smem_of(&s.item_checked[items % kItems]), items / kItems & 1, gave_up);
+      const bool bad = given.bad != 0;
+      const int run = given.run, pieces = given.pieces;
+      __syncwarp();
+      done_item();
       // kPair: this stream's rows, all columns; else half of the columns of both streams' sum
       const int my_rows = rows - first_row;
-      if (quarter * 32 < my_rows) {
+      if (quarter * 32 < my_rows && !(bad && w.t0 > 0)) {
         float weight[2] = {1.0f, 1.0f};
         if (!kPair) {
           const float m_of[2] = {st ? other.x : m, st ? m : other.x};
@@ -1064,13 +1116,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += weight[k] * l_of[k];
           }
         }
-        const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+        const bool whole = pieces == 1 || bad;  // of a flagged request the first piece clears the rows
         const float inv = 1.0f / l;
         const bool mine = row < my_rows;
         uint16_t* out = P.out.data + w.b * P.out.batch_stride + node * P.out.node_stride +
                         (w.h * P.group + g) * P.out.head_stride;
         const int64_t part =
-            static_cast<int64_t>(2 * w.run + (w.t0 == 0)) * P.part_rows + first_row + row;
+            static_cast<int64_t>(2 * run + (w.t0 == 0)) * P.part_rows + first_row + row;
         constexpr int kCols = kPair ? DP : DP / 2;
         const int col0 = kPair ? 0 : st * kCols;
 #pragma unroll 1
@@ -1106,15 +1158,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (mine && whole) {
+            if (bad)
+#pragma unroll
+              for (int e = 0; e < 32; e++) o[e] = 0.0f;
+            const float by = bad ? 0.0f : inv;
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
               const int d = col0 + k + e;
               if (d < C.head_dim)
                 *reinterpret_cast<uint4*>(out + d) =
-                    make_uint4(E::pack(o[e] * inv, o[e + 1] * inv),
-                               E::pack(o[e + 2] * inv, o[e + 3] * inv),
-                               E::pack(o[e + 4] * inv, o[e + 5] * inv),
-                               E::pack(o[e + 6] * inv, o[e + 7] * inv));
+                    make_uint4(E::pack(o[e] * by, o[e + 1] * by),
+                               E::pack(o[e + 2] * by, o[e + 3] * by),
+                               E::pack(o[e + 4] * by, o[e + 5] * by),
+                               E::pack(o[e + 6] * by, o[e + 7] * by));
             }
           } else if (mine) {
 #pragma unroll
@@ -1132,7 +1188,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  if (tid == 0 && *gave_up) P.ws.header->timeout = 1;
   tmem_fence_before();
   __syncthreads();
   if (warp == kScoreWarp) {
@@ -1141,107 +1196,122 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------ finish
+// -------------------------------------------------------------------- join
 
-constexpr int kFinishWarps = 8;
-constexpr int kFinishRows = 4;  // rows of a warp
-
-// Block x < B: a flagged request's rows become 0.  The others, B + y: the cut
-// before run 1 + y / groups, for 32 of its item's rows.  The first cut of an
-// item joins all its pieces:
+// Joins the pieces of the items that runs cut:
 //   m = max m_i, O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i, in order.
-// A lane has four columns of a row.
-template <class E, int DP, int kRowTile>
-__global__ void __launch_bounds__(kFinishWarps * 32) finish_kernel(const AttnParams P, int groups) {
+// A block to a cut.  A warp takes eight rows and kPieces pieces at a time, all of
+// their loads in flight, and where rows are few (then pieces are many) the warps
+// share out the pieces.  A lane has four columns of each row, and the weight of
+// one row and piece.  The code is short on purpose: it runs once, and fetching
+// it was most of the time of an unrolled form (5.7 of 8 us).
+constexpr int kJoinWarps = 8, kJoinRows = 8;
+
+template <class E, int DP, int kRowTile, int kRowGroups>
+__global__ void __launch_bounds__(kJoinWarps * 32, kRowGroups == kJoinWarps ? 2 : 1)
+    join_kernel(const AttnParams P) {
+  constexpr int kShares = kJoinWarps / kRowGroups;
+  constexpr int kJoinPieces = kShares > 1 ? 4 : 2;
+  __shared__ float4 s_o[kShares > 1 ? kJoinWarps : 1][kJoinRows][32];
+  __shared__ float2 s_ml[kJoinWarps][kJoinRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int group = warp % kRowGroups, share = warp / kRowGroups;
+  const int run = 1 + blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31;
-  const Header* header = P.ws.header;
-  if (blockIdx.x == 0 && tid == 0) P.ws.header->next = 0;  // for the next call
-  if (static_cast<int>(blockIdx.x) < P.B) {
-    const int b = blockIdx.x;
-    if (header->timeout && tid == 0) P.status[b] = P.ws.bad[b] | SPECV_DEV_TIMEOUT;
-    if (P.ws.bad[b] == 0) return;
-    const int given = P.n_nodes ? P.n_nodes[b] : P.N;
-    const int n = given < 1 || given > P.N ? P.N : given, words = P.cache.head_dim / 8;
-    for (int e = tid; e < n * P.q_heads * words; e += kFinishWarps * 32) {
-      const int i = e / (P.q_heads * words), h = e / words % P.q_heads, d = e % words * 8;
-      *reinterpret_cast<uint4*>(P.out.data + b * P.out.batch_stride + i * P.out.node_stride +
-                                h * P.out.head_stride + d) = make_uint4(0, 0, 0, 0);
-    }
-    return;
-  }
-  const int block = blockIdx.x - P.B, run = 1 + block / groups;
-  const Start at = P.ws.starts[run], before = P.ws.starts[run - 1];
-  const int count = header->count, even = header->even, dealt = header->dealt;
-  if (run >= count || at.t0 == 0) return;  // no cut here
-  if (before.b == at.b && before.h == at.h && before.row_tile == at.row_tile && before.t0 != 0)
-    return;  // not the item's first
-  const int row0 = (block % groups * kFinishWarps + tid / 32) * kFinishRows;
-  const int rows = min(kRowTile, at.n * P.group - at.row_tile * kRowTile);
-  if (row0 >= rows || P.ws.bad[at.b]) return;
-  // one piece ends the run before, the others begin a run each: even ones, then dealt ones
-  const int left = at.tiles - at.t0, evens = max(P.ctas - run, 0);
-  int pieces = 1 + min(evens, (left + even - 1) / even);
-  if (left > static_cast<int64_t>(evens) * even) pieces += (left - evens * even + dealt - 1) / dealt;
-  auto index = [&](int i, int r) {
-    const int slot = i == 0 ? 2 * (run - 1) + 1 : 2 * (run + i - 1);
-    return static_cast<int64_t>(slot) * P.part_rows + min(row0 + r, rows - 1);
-  };
-  // the pieces' weights, a piece to a lane, then their sums
-  float m[kFinishRows], l[kFinishRows];
-  float4 o[kFinishRows];
+  const Cut cut = P.ws.cuts[run];
+  const int count = P.ws.header->count;
+  if (blockIdx.x == 0 && threadIdx.x == 0) P.ws.header->next = 0;  // for the next call
+  if (run >= count || cut.pieces == 0) return;
+  const int rows = min(kRowTile, cut.n * P.group - cut.row_tile * kRowTile);
+  if (P.status[cut.b]) return;
+  const int d = 4 * lane, my_row = lane / kJoinPieces % kJoinRows, my_piece = lane % kJoinPieces;
+#pragma unroll 1
+  for (int row0 = group * kJoinRows; row0 < (kShares > 1 ? kRowGroups * kJoinRows : rows);
+       row0 += kRowGroups * kJoinRows) {
+    // the first piece ends a run, the others begin theirs (slots have whole eights of rows)
+    auto index = [&](int i) {
+      const int slot = 2 * (run - 1 + i) + (i == 0);
+      return static_cast<int64_t>(slot) * P.part_rows + min(row0, P.part_rows - kJoinRows);
+    };
+    float m = -INFINITY, l = 0.0f;  // of row my_row
+    float4 o[kJoinRows];
 #pragma unroll
-  for (int r = 0; r < kFinishRows; r++) {
-    m[r] = -INFINITY;
-    l[r] = 0.0f;
-    o[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  }
-  const int d = 4 * lane;
-  for (int i0 = 0; i0 < pieces; i0 += 32) {
-    float2 ml[kFinishRows];
-    float weight[kFinishRows];
+    for (int r = 0; r < kJoinRows; r++) o[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int i0 = share * kJoinPieces; i0 < cut.pieces; i0 += kShares * kJoinPieces) {
+      float4 x[kJoinPieces][kJoinRows];
 #pragma unroll
-    for (int r = 0; r < kFinishRows; r++)
-      ml[r] = i0 + lane < pieces ? P.ws.stats[index(i0 + lane, r)] : make_float2(-INFINITY, 0.0f);
+      for (int i = 0; i < kJoinPieces; i++) {
+        const float4* from =
+            reinterpret_cast<const float4*>(P.ws.parts + index(i0 + i) * DP + d % DP);
 #pragma unroll
-    for (int r = 0; r < kFinishRows; r++) {
-      float top = ml[r].x, sum;
+        for (int r = 0; r < kJoinRows; r++)
+          x[i][r] = i0 + i < cut.pieces ? from[r * (DP / 4)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (i0 + my_piece < cut.pieces) ml = P.ws.stats[index(i0 + my_piece) + my_row];
+      float top = ml.x;
 #pragma unroll
-      for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
-      top = fmaxf(top, m[r]);
-      weight[r] = ml[r].x == top ? 1.0f : exp2_of(ml[r].x - top);
-      sum = weight[r] * ml[r].y;
+      for (int s = 1; s < kJoinPieces; s *= 2) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, s));
+      top = fmaxf(top, m);
+      const float weight =
+          i0 + my_piece >= cut.pieces ? 0.0f : ml.x == top ? 1.0f : exp2_of(ml.x - top);
+      const float old = m == top ? 1.0f : exp2_of(m - top);
+      float sum = weight * ml.y;
 #pragma unroll
-      for (int x = 16; x > 0; x /= 2) sum += __shfl_xor_sync(kFullMask, sum, x);
-      const float old = m[r] == top ? 1.0f : exp2_of(m[r] - top);
-      m[r] = top;
-      l[r] = l[r] * old + sum;
-      o[r].x *= old, o[r].y *= old, o[r].z *= old, o[r].w *= old;
-    }
-    const int here = min(32, pieces - i0);
-#pragma unroll 4
-    for (int i = 0; i < here; i++) {
+      for (int s = 1; s < kJoinPieces; s *= 2) sum += __shfl_xor_sync(kFullMask, sum, s);
+      m = top;
+      l = l * old + sum;
 #pragma unroll
-      for (int r = 0; r < kFinishRows; r++) {
-        const float by = __shfl_sync(kFullMask, weight[r], i);
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (d < DP) x = *reinterpret_cast<const float4*>(P.ws.parts + index(i0 + i, r) * DP + d);
-        o[r].x = fmaf(by, x.x, o[r].x);
-        o[r].y = fmaf(by, x.y, o[r].y);
-        o[r].z = fmaf(by, x.z, o[r].z);
-        o[r].w = fmaf(by, x.w, o[r].w);
+      for (int r = 0; r < kJoinRows; r++) {
+        const float keep = __shfl_sync(kFullMask, old, r * kJoinPieces);
+        o[r].x *= keep, o[r].y *= keep, o[r].z *= keep, o[r].w *= keep;
+#pragma unroll
+        for (int i = 0; i < kJoinPieces; i++) {
+          const float by = __shfl_sync(kFullMask, weight, r * kJoinPieces + i);
+          o[r].x = fmaf(by, x[i][r].x, o[r].x);
+          o[r].y = fmaf(by, x[i][r].y, o[r].y);
+          o[r].z = fmaf(by, x[i][r].z, o[r].z);
+          o[r].w = fmaf(by, x[i][r].w, o[r].w);
+        }
       }
     }
-  }
-  if (d >= P.cache.head_dim) return;
+    if (kShares > 1) {
+      // the warps' shares, in their order
+      if (my_piece == 0) s_ml[warp][my_row] = make_float2(m, l);
 #pragma unroll
-  for (int r = 0; r < kFinishRows; r++) {
-    if (row0 + r >= rows) break;
-    const float inv = 1.0f / l[r];
-    const int flat = at.row_tile * kRowTile + row0 + r, node = flat / P.group, g = flat - node * P.group;
-    *reinterpret_cast<uint2*>(P.out.data + at.b * P.out.batch_stride + node * P.out.node_stride +
-                              (at.h * P.group + g) * P.out.head_stride + d) =
-        make_uint2(E::pack(o[r].x * inv, o[r].y * inv), E::pack(o[r].z * inv, o[r].w * inv));
+      for (int r = 0; r < kJoinRows; r++) s_o[warp][r][lane] = o[r];
+      __syncthreads();
+      if (share) return;  // rows are few: there is no other round
+#pragma unroll 1
+      for (int w = 1; w < kShares; w++) {
+        const float2 ml = s_ml[warp + w * kRowGroups][my_row];
+        const float top = fmaxf(m, ml.x);
+        const float old = m == top ? 1.0f : exp2_of(m - top);
+        const float weight = ml.x == top ? 1.0f : exp2_of(ml.x - top);
+        m = top;
+        l = l * old + weight * ml.y;
+#pragma unroll
+        for (int r = 0; r < kJoinRows; r++) {
+          const float keep = __shfl_sync(kFullMask, old, r * kJoinPieces);
+          const float by = __shfl_sync(kFullMask, weight, r * kJoinPieces);
+          const float4 x = s_o[warp + w * kRowGroups][r][lane];
+          o[r].x = o[r].x * keep + by * x.x;
+          o[r].y = o[r].y * keep + by * x.y;
+          o[r].z = o[r].z * keep + by * x.z;
+          o[r].w = o[r].w * keep + by * x.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kJoinRows; r++) {
+      const float inv = 1.0f / __shfl_sync(kFullMask, l, r * kJoinPieces);
+      if (row0 + r >= rows || d >= P.cache.head_dim) continue;
+      const int flat = cut.row_tile * kRowTile + row0 + r, node = flat / P.group, g = flat - node * P.group;
+      *reinterpret_cast<uint2*>(P.out.data + cut.b * P.out.batch_stride + node * P.out.node_stride +
+                                (cut.h * P.group + g) * P.out.head_stride + d) =
+          make_uint2(E::pack(o[r].x * inv, o[r].y * inv), E::pack(o[r].z * inv, o[r].w * inv));
+    }
   }
 }
 
@@ -1252,20 +1322,18 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 // The shape of the work that B, N and the heads give, whatever the lengths are.
 struct Plan {
   int mode, dim, row_tile, part_rows, dealt;
-  size_t bad, starts, stats, parts, total;  // offsets in the workspace
+  size_t stats, parts, total;  // offsets in the workspace; before them the header and the cuts
 
-  Plan(int B, int N, int group, int head_dim) {
+  Plan(int N, int group, int head_dim) {
     const int rows = N * group;
     mode = rows <= 64 ? 0 : rows <= kRows ? 1 : 2;
     dim = head_dim <= 64 ? 64 : 128;
     row_tile = mode == 0 ? 64 : mode == 1 ? kRows : 2 * kRows;
     part_rows = (rows < row_tile ? rows : row_tile) + 7 & ~7;
-    // a piece of many rows is as large as a key tile: then fewer of them
-    dealt = part_rows > 64 ? kMaxCtas : 3 * kMaxCtas;
+    // a piece of 256 rows is as large as two key tiles with their values: fewer of them
+    dealt = mode == 2 ? kMaxCtas : 3 * kMaxCtas;
     const size_t runs = kMaxCtas + dealt;
-    bad = 256;
-    starts = bad + align256(static_cast<size_t>(B) * 4);
-    stats = starts + align256(runs * sizeof(Start));
+    stats = SPECV_ATTENTION_HEADER_BYTES + align256(runs * sizeof(Cut));
     parts = stats + align256(2 * runs * part_rows * sizeof(float2));
     total = parts + align256(2 * runs * part_rows * dim * sizeof(float));
   }
@@ -1319,13 +1387,17 @@ cudaError_t run(const AttnParams& P, const CUtensorMap& k_map, const CUtensorMap
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const int groups = (P.part_rows + kFinishWarps * kFinishRows - 1) / (kFinishWarps * kFinishRows);
-  cfg.gridDim = dim3(P.B + (P.ctas + P.dealt - 1) * groups);
-  cfg.blockDim = dim3(kFinishWarps * 32);
+  // (with one CTA there is no cut: the block resets the header)
+  const int cuts = P.ctas + P.dealt - 1 > 0 ? P.ctas + P.dealt - 1 : 1;
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, finish_kernel<E, DP, S::kRowTile>, P, groups);
+  cfg.gridDim = dim3(cuts);
+  if (kMode > 0) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8>, P);
+  if (P.part_rows <= 16) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 2>, P);
+  if (P.part_rows <= 32) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 4>, P);
+  return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8>, P);
 }
 
 template <class E>
@@ -1349,7 +1421,7 @@ size_t specv_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, 
       q_heads < kv_heads || q_heads > 1024 || q_heads % kv_heads != 0 || head_dim < 8 ||
       head_dim > SPECV_MAX_HEAD_DIM || head_dim % 8 != 0)
     return 0;
-  return Plan(B, N, q_heads / kv_heads, head_dim).total;
+  return Plan(N, q_heads / kv_heads, head_dim).total;
 }
 
 specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
@@ -1366,7 +1438,7 @@ specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
     return SPECV_ERR_INVALID_ARG;
   if (q_heads > 1024) return SPECV_ERR_UNSUPPORTED;
   const int group = q_heads / cache->heads;
-  const Plan plan(B, N, group, cache->head_dim);
+  const Plan plan(N, group, cache->head_dim);
   if (workspace_bytes < plan.total) return SPECV_ERR_WORKSPACE;
   int device = 0, ctas = 0;
   if (cudaGetDevice(&device) != cudaSuccess ||
@@ -1374,8 +1446,8 @@ specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
     return SPECV_ERR_CUDA;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
   char* base = static_cast<char*>(workspace);
-  const Workspace ws{reinterpret_cast<Header*>(base), reinterpret_cast<int32_t*>(base + plan.bad),
-                     reinterpret_cast<Start*>(base + plan.starts),
+  const Workspace ws{reinterpret_cast<Header*>(base),
+                     reinterpret_cast<Cut*>(base + SPECV_ATTENTION_HEADER_BYTES),
                      reinterpret_cast<float2*>(base + plan.stats),
                      reinterpret_cast<float*>(base + plan.parts)};
   const int page = cache->page_size;

@@ -16,7 +16,7 @@ import struct
 
 import torch
 
-from ._native import SPECV_BF16, SPECV_F16, SPECV_F32, check, lib
+from ._native import ATTENTION_HEADER_BYTES, SPECV_BF16, SPECV_F16, SPECV_F32, check, lib
 
 _CACHE_DTYPES = {torch.bfloat16: SPECV_BF16, torch.float16: SPECV_F16}
 _LOGIT_DTYPES = {torch.bfloat16: SPECV_BF16, torch.float32: SPECV_F32}
@@ -184,8 +184,8 @@ def append_nodes(q, k, v, k_cache, v_cache, page_table, cache_lens, inv_freq=Non
 
 
 class AttentionWorkspace:
-    """Device workspace for tree_attention over B requests of up to N nodes,
-    zeroed once on creation (every call leaves it ready for the next).  Calls
+    """Device workspace for tree_attention over B requests of up to N nodes, its
+    header zeroed once on creation (every call leaves it ready for the next).  Calls
     that may run at the same time (on two streams, or two captured graphs that
     may be replayed together) need one each."""
 
@@ -199,7 +199,7 @@ class AttentionWorkspace:
         dev = self.tensor.device
         with torch.cuda.device(dev):
             check("specv_workspace_init", lib().specv_workspace_init(
-                self.tensor.data_ptr(), 256,  # its header
+                self.tensor.data_ptr(), ATTENTION_HEADER_BYTES,
                 _raw_stream(dev.index) if stream is None else getattr(stream, "cuda_stream", stream)))
 
 
