@@ -46,6 +46,7 @@ constexpr int kSumWarp = 14;    // issues O += P V
 constexpr int kDealWarp = 15;
 constexpr int kThreads = 512;
 constexpr int kItems = 4;  // items dealt out ahead
+constexpr int kItemCost = 1;  // what an item takes besides its key tiles, in their time
 constexpr int kNear = 3;   // key tiles before an item's end at which the next run is called for
 // Registers a thread of each warpgroup: 2 * 200 + 56 + 56 = 512 = 4 * 128, what
 // the block is launched with.  The softmax keeps a row of scores in them.
@@ -64,7 +65,7 @@ struct Header {
 // Where a run begins in the middle of an item: the item's second piece.
 struct Cut {
   int32_t b, h, row_tile, n;
-  int32_t pieces;  // of the item; 0: the run does not begin its second piece
+  int32_t pieces;  // of the item; 0: the run does not begin with an item's second piece
   int32_t pad[3];
 };
 
@@ -99,9 +100,7 @@ struct Runs {
   __device__ __forceinline__ Runs(const AttnParams& P, int64_t units)
       : total(units), dealt(1), ctas(P.ctas) {
     if (total >= 8 * ctas && P.dealt > 0) {
-      // about 3/4 and, where pieces are small and more of them cost little, 3/5
-      even = quotient(total, ctas);
-      even = P.dealt > ctas ? even / 5 * 3 : even / 4 * 3;
+      even = quotient(total, ctas) * 7 / 8;
       const int64_t rest = total - static_cast<int64_t>(even) * ctas;
       dealt = quotient(rest + P.dealt - 1, P.dealt);
       count = ctas + quotient(rest + dealt - 1, dealt);
@@ -434,14 +433,15 @@ template <int kStages> struct Tail {
   float2 stats[2][kRows];
 };
 
-// The work units (128-key tiles of a row tile of a key head) of request b.
+// The work units of request b: for each row tile of a key head (an item)
+// kItemCost and its 128-key tiles, in this order.
 template <int kRowTile>
 __device__ __forceinline__ int64_t units_of(const AttnParams& P, int b, int& tiles, int& row_tiles,
                                             int& len, int& n) {
   n = nodes_of(P, b, len);
   tiles = n ? (len + n + kKeys - 1) / kKeys : 0;
   row_tiles = (n * P.group + kRowTile - 1) / kRowTile;
-  return static_cast<int64_t>(tiles) * row_tiles * P.cache.heads;
+  return n ? static_cast<int64_t>(tiles + kItemCost) * row_tiles * P.cache.heads : 0;
 }
 
 // Bits of the 32 columns from `first` (a key's number less len): which of them
@@ -771,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t u = runs.start(run);
         const int64_t end = runs.start(run + 1);
         bool begins = true;
+        if (lane == 0) P.ws.cuts[run] = Cut{0, 0, 0, 0, 0, {0, 0, 0}};
         while (u < end && !stop) {
           // the request with unit u: 32 requests at a time
           int tiles, row_tiles, len, n;
@@ -811,17 +812,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (P.parents && i < n) parent = P.parents[static_cast<int64_t>(b) * P.N + i];
             up[k] = static_cast<uint8_t>(parent >= 0 && parent < i ? parent : 0);
           }
+          const int span = tiles + kItemCost;
           while (u < end && u < before + units) {
             const int64_t off = u - before;
-            const int64_t of = off >> 32 ? off / tiles : static_cast<uint32_t>(off) / tiles;
-            const int t0 = static_cast<int>(off - of * tiles);
+            const int64_t of = off >> 32 ? off / span : static_cast<uint32_t>(off) / span;
+            const int64_t first = u - (off - of * span) + kItemCost;  // of its tiles' units
             const int h = static_cast<int>(of) / row_tiles;  // below 1024 heads * 512 row tiles
             const int row_tile = static_cast<int>(of) - h * row_tiles;
-            const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (end - u)));
+            const int t0 = static_cast<int>(max(u - first, static_cast<int64_t>(0)));
+            const int t1 = static_cast<int>(min(end - first, static_cast<int64_t>(tiles)));
+            u = min(end, first + tiles);
+            if (t1 <= t0) continue;  // the run ends before the item's first tile
             // runs before and behind with pieces of this item
             int first_run = run, last_run = run;
-            if (t0 > 0) first_run = runs.last(0, u - t0 + 1);
-            if (t1 < tiles) last_run = runs.last(run, u - t0 + tiles);
+            if (t0 > 0) first_run = runs.last(0, first + 1);
+            if (t1 < tiles) last_run = runs.last(run, first + tiles);
             const uint32_t slot = items % kItems;
             barrier_wait(smem_of(&s.item_empty[slot]), (items / kItems & 1) ^ 1, gave_up);
             stop = __any_sync(kFullMask, *gave_up != 0);
@@ -840,16 +845,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               to.n = n;
               to.run = run;
               to.pieces = last_run - first_run + 1;
-              if (begins)
-                P.ws.cuts[run] = Cut{b, h, row_tile, n,
-                                     t0 > 0 && first_run == run - 1 ? last_run - first_run + 1 : 0,
-                                     {0, 0, 0}};
+              if (begins && t0 > 0 && first_run == run - 1)
+                P.ws.cuts[run] = Cut{b, h, row_tile, n, last_run - first_run + 1, {0, 0, 0}};
             }
             __syncwarp();
             if (lane == 0) barrier_arrive(smem_of(&s.item_full[slot]));
             items++;
             begins = false;
-            u += t1 - t0;
           }
         }
         // Not before the copies are near this run's end: a run taken early is one that
@@ -1205,11 +1207,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // share out the pieces.  A lane has four columns of each row, and the weight of
 // one row and piece.  The code is short on purpose: it runs once, and fetching
 // it was most of the time of an unrolled form (5.7 of 8 us).
-constexpr int kJoinWarps = 8, kJoinRows = 8;
+constexpr int kJoinRows = 8;
 
-template <class E, int DP, int kRowTile, int kRowGroups>
-__global__ void __launch_bounds__(kJoinWarps * 32, kRowGroups == kJoinWarps ? 2 : 1)
-    join_kernel(const AttnParams P) {
+template <class E, int DP, int kRowTile, int kJoinWarps, int kRowGroups>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P) {
   constexpr int kShares = kJoinWarps / kRowGroups;
   constexpr int kJoinPieces = kShares > 1 ? 4 : 2;
   __shared__ float4 s_o[kShares > 1 ? kJoinWarps : 1][kJoinRows][32];
@@ -1221,9 +1222,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kRowGroups == kJoinWarps ? 2 
   const Cut cut = P.ws.cuts[run];
   const int count = P.ws.header->count;
   if (blockIdx.x == 0 && threadIdx.x == 0) P.ws.header->next = 0;  // for the next call
-  if (run >= count || cut.pieces == 0) return;
+  // (A call that gave up may leave records of another: they are not followed out of bounds.)
+  if (run >= count || cut.pieces < 2 || cut.pieces > count - run + 1 || cut.b < 0 || cut.b >= P.B ||
+      cut.h < 0 || cut.h >= P.cache.heads || cut.n < 1 || cut.n > P.N || cut.row_tile < 0 ||
+      cut.row_tile * kRowTile >= cut.n * P.group)
+    return;
   const int rows = min(kRowTile, cut.n * P.group - cut.row_tile * kRowTile);
-  if (P.status[cut.b]) return;
+  const int flagged = P.status[cut.b];  // its first piece has cleared the rows
   const int d = 4 * lane, my_row = lane / kJoinPieces % kJoinRows, my_piece = lane % kJoinPieces;
 #pragma unroll 1
   for (int row0 = group * kJoinRows; row0 < (kShares > 1 ? kRowGroups * kJoinRows : rows);
@@ -1306,7 +1311,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kRowGroups == kJoinWarps ? 2 
 #pragma unroll
     for (int r = 0; r < kJoinRows; r++) {
       const float inv = 1.0f / __shfl_sync(kFullMask, l, r * kJoinPieces);
-      if (row0 + r >= rows || d >= P.cache.head_dim) continue;
+      if (row0 + r >= rows || d >= P.cache.head_dim || flagged) continue;
       const int flat = cut.row_tile * kRowTile + row0 + r, node = flat / P.group, g = flat - node * P.group;
       *reinterpret_cast<uint2*>(P.out.data + cut.b * P.out.batch_stride + node * P.out.node_stride +
                                 (cut.h * P.group + g) * P.out.head_stride + d) =
@@ -1330,8 +1335,9 @@ struct Plan {
     dim = head_dim <= 64 ? 64 : 128;
     row_tile = mode == 0 ? 64 : mode == 1 ? kRows : 2 * kRows;
     part_rows = (rows < row_tile ? rows : row_tile) + 7 & ~7;
-    // a piece of 256 rows is as large as two key tiles with their values: fewer of them
-    dealt = mode == 2 ? kMaxCtas : 3 * kMaxCtas;
+    // As many again: more even out the ends better, but each costs a piece written and
+    // read.  A piece of 256 rows costs more than the dealing gains (388 us against 395).
+    dealt = mode == 2 ? 0 : kMaxCtas;
     const size_t runs = kMaxCtas + dealt;
     stats = SPECV_ATTENTION_HEADER_BYTES + align256(runs * sizeof(Cut));
     parts = stats + align256(2 * runs * part_rows * sizeof(float2));
@@ -1389,15 +1395,15 @@ cudaError_t run(const AttnParams& P, const CUtensorMap& k_map, const CUtensorMap
   cudaLaunchConfig_t cfg = {};
   // (with one CTA there is no cut: the block resets the header)
   const int cuts = P.ctas + P.dealt - 1 > 0 ? P.ctas + P.dealt - 1 : 1;
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.gridDim = dim3(cuts);
+  cfg.blockDim = dim3(kMode > 0 ? 512 : 256);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(cuts);
-  if (kMode > 0) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8>, P);
-  if (P.part_rows <= 16) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 2>, P);
-  if (P.part_rows <= 32) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 4>, P);
-  return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8>, P);
+  if (kMode > 0) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 16, 16>, P);
+  if (P.part_rows <= 16) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8, 2>, P);
+  if (P.part_rows <= 32) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8, 4>, P);
+  return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8, 8>, P);
 }
 
 template <class E>
