@@ -49,8 +49,9 @@ template <> struct Elt<SPECV_BF16> {
   static __device__ uint16_t store(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 };
 
-constexpr int kTextThreads = 128;  // threads of a block that count the text first
-constexpr int kSegment = 1024;     // entries of a row that a warp takes at a time
+constexpr int kTokens = 512;  // tokens of the text that a warp counts at a time
+constexpr int kFound = 160;   // of them in the chunk: four from each lane may follow 31 that wait
+constexpr int kMaxRows = 8;     // rows of a block
 
 // What a block needs of one request's text, for its chunk of the vocabulary.
 template <int kChunk> struct Text {
@@ -60,6 +61,7 @@ template <int kChunk> struct Text {
   uint16_t biased[SPECV_MAX_BIAS];  // ... and their entries
   int drafted[kMaxNodes];  // entry of node i's token, -1 where it is another chunk's
   int num_biased, touched, ticket, bad;
+  uint32_t found[8][kFound];  // by warp: tokens of the text that are in this chunk
   uint16_t list[8];  // touched entries: at most kChunk, and the text's, drafts' and biases' number
 };
 
@@ -90,17 +92,18 @@ template <int DT> __device__ __forceinline__ void mask_vec(uint4& v, uint32_t ke
 }
 
 // A block takes kChunk vocabulary entries of one request, for P.rows of its
-// rows.  Nearly every element is only masked and copied, whatever the text
-// says: the warps take segments of rows off a counter and stream them, while
-// the first four count the text's tokens in this chunk in shared memory and
-// list the entries they touch; those join the streaming when they are done.
-// Then the listed entries are computed from the input, one to a thread, and
+// rows.  It counts the text's tokens in this chunk in shared memory and lists
+// the entries they touch.  Nearly every element is only masked and copied,
+// whatever the text says, so the warps take first parts of the text and then
+// segments of rows off one counter, and none waits for another.  Then the
+// listed entries are computed from the input, one to a thread for two rows, and
 // stored over the copies.
 template <int DT, int kChunk, int kThreads, Layout kLayout>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const Params P) {
   using E = Elt<DT>;
   using T = typename E::T;
   constexpr int kVec = kLayout == kSingle ? 1 : 16 / sizeof(T);
+  constexpr int kSegment = 1024;  // entries of a row that a warp copies at a time
   constexpr int kMine = kSegment / 32 / kVec;        // vectors of a segment a lane has
   constexpr int kFlight = kMine < 4 ? kMine : 4;     // ... in flight
   extern __shared__ __align__(16) char smem[];
@@ -109,114 +112,148 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
   const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
   const int c0 = blockIdx.x * kChunk, c1 = min(P.V, c0 + kChunk);
   const int given = P.n_rows ? P.n_rows[b] : P.R;
-  const int n = given < 1 || given > P.R ? P.R : given;
-  const int first_row = blockIdx.z * P.rows, last_row = min(n, first_row + P.rows);
-  if (first_row >= last_row) return;
+  const int total = P.seq_lens[b], prompt = P.prompt_lens ? P.prompt_lens[b] : 0;
   const float rho = P.repetition ? P.repetition[b] : 1.0f;
   const float freq = P.frequency ? P.frequency[b] : 0.0f;
   const float pres = P.presence ? P.presence[b] : 0.0f;
-  const int total = P.seq_lens[b], prompt = P.prompt_lens ? P.prompt_lens[b] : 0;
+  for (int e = tid; e < kChunk / 4; e += kThreads)
+    reinterpret_cast<uint4*>(s.count)[e] = make_uint4(0, 0, 0, 0);
   if (tid == 0) {
     s.num_biased = 0;
     s.touched = 0;
     s.ticket = 0;
     s.bad = 0;
   }
+  const int n = given < 1 || given > P.R ? P.R : given;
+  const int first_row = blockIdx.z * P.rows, last_row = min(n, first_row + P.rows);
+  if (first_row >= last_row) return;
   __syncthreads();
 
-  if (tid < kTextThreads) {
-    // the text's first tokens are on their way while the counts are cleared
-    constexpr int kAhead = 4;
-    const int32_t* hist = P.history + b * P.history_stride;
-    const bool fits = total >= 0 && total <= P.L;
-    const int vectors = fits && reinterpret_cast<uintptr_t>(hist) % 16 == 0 ? total / 4 : 0;
-    int4 ahead[kAhead];
+  // Whoever finds an untouched word lists its entry.  Counts are whole numbers:
+  // the order in which the threads add does not show.
+  auto touch = [&](int e, uint32_t old) {
+    if (old == 0) s.list[atomicAdd(&s.touched, 1)] = static_cast<uint16_t>(e);
+  };
+  const bool fits = total >= 0 && total <= P.L;
+  if (tid < 32) {
+    Tree t = read_tree(P.parents, P.n_rows, P.seq_lens, b, P.R, INT64_MAX, lane);
+    if (!(t.bad & SPECV_DEV_BAD_TREE)) {
+      bool bad_token = false;
 #pragma unroll
-    for (int k = 0; k < kAhead; k++)
-      if (tid + k * kTextThreads < vectors)
-        ahead[k] = reinterpret_cast<const int4*>(hist)[tid + k * kTextThreads];
-    for (int e = tid; e < kChunk / 4; e += kTextThreads)
-      reinterpret_cast<uint4*>(s.count)[e] = make_uint4(0, 0, 0, 0);
-    bool bad_token = false;
-    if (tid < 32) {
-      Tree t = read_tree(P.parents, P.n_rows, P.seq_lens, b, P.R, INT64_MAX, lane);
-      if (!(t.bad & SPECV_DEV_BAD_TREE)) {
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-          const int i = lane + 32 * k;
-          int at = -1;
-          if (i >= 1 && i < t.n) {
-            const int token = P.parents ? P.tokens[static_cast<int64_t>(b) * P.R + i]
-                                        : P.tokens[static_cast<int64_t>(b) * (P.R - 1) + i - 1];
-            bad_token |= token < 0 || token >= P.V;
-            if (token >= c0 && token < c1) at = token - c0;
-          }
-          s.drafted[i] = at;
+      for (int k = 0; k < 2; k++) {
+        const int i = lane + 32 * k;
+        int at = -1;
+        if (i >= 1 && i < t.n) {
+          const int token = P.parents ? P.tokens[static_cast<int64_t>(b) * P.R + i]
+                                      : P.tokens[static_cast<int64_t>(b) * (P.R - 1) + i - 1];
+          bad_token |= token < 0 || token >= P.V;
+          if (token >= c0 && token < c1) at = token - c0;
         }
+        s.drafted[i] = at;
+        if (at >= 0) touch(at, atomicOr(&s.count[at], kDrafted));
+      }
+      if (__any_sync(kFullMask, bad_token)) t.bad |= SPECV_DEV_BAD_TOKEN;
+      // paths matter only where a drafted token is one of this chunk's
+      if (__any_sync(kFullMask, s.drafted[lane] >= 0 || s.drafted[lane + 32] >= 0)) {
         uint64_t bits[2];
         ancestors(t, lane, bits);
         s.path[lane] = bits[0];
         s.path[lane + 32] = bits[1];
       }
-      if (total > P.L || prompt < 0 || prompt > total) t.bad |= SPECV_DEV_BAD_CACHE;
-      if (!(rho > 0.0f) || !isfinite(rho) || !isfinite(freq) || !isfinite(pres))
-        t.bad |= SPECV_DEV_BAD_PENALTY;
-      if (lane == 0) s.bad = static_cast<int>(t.bad);
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(kTextThreads) : "memory");
-    if (!s.bad) {
-      unsigned largest = 0;
-      // Counts are whole numbers: the order in which the threads add does not
-      // show.  Whoever finds an untouched word lists its entry.
-      auto touch = [&](int e, uint32_t old) {
-        if (old == 0) s.list[atomicAdd(&s.touched, 1)] = static_cast<uint16_t>(e);
-      };
-      auto count = [&](int i, int token) {
-        largest = max(largest, static_cast<unsigned>(token));
-        const int e = token - c0;
-        if (static_cast<unsigned>(e) >= static_cast<unsigned>(c1 - c0)) return;
-        touch(e, i < prompt ? atomicOr(&s.count[e], kInPrompt) : atomicAdd(&s.count[e], 1u));
-      };
-      auto count4 = [&](int i, const int4& t) {
-        count(4 * i, t.x);
-        count(4 * i + 1, t.y);
-        count(4 * i + 2, t.z);
-        count(4 * i + 3, t.w);
-      };
-#pragma unroll
-      for (int k = 0; k < kAhead; k++)
-        if (tid + k * kTextThreads < vectors) count4(tid + k * kTextThreads, ahead[k]);
-#pragma unroll 4
-      for (int i = tid + kAhead * kTextThreads; i < vectors; i += kTextThreads)
-        count4(i, reinterpret_cast<const int4*>(hist)[i]);
-      for (int i = 4 * vectors + tid; i < total; i += kTextThreads) count(i, hist[i]);
-      bad_token |= largest >= static_cast<unsigned>(P.V);
-      if (tid < n && s.drafted[tid] >= 0)
-        touch(s.drafted[tid], atomicOr(&s.count[s.drafted[tid]], kDrafted));
-      const int32_t* names = P.bias_tokens + static_cast<int64_t>(b) * P.num_bias;
-      const float* values = P.bias_values + static_cast<int64_t>(b) * P.num_bias;
-      for (int i = tid; i < P.num_bias; i += kTextThreads) {
-        const int token = names[i];
-        bad_token |= token >= P.V;
-        if (token < c0 || token >= c1) continue;
-        // the first place that names a token adds up all of them, in their order
-        float sum = 0.0f;
-        bool first = true;
-        for (int j = 0; j < P.num_bias; j++)
-          if (names[j] == token) {
-            if (j < i) first = false;
-            sum = sum + values[j];
-          }
-        if (first) {
-          const int at = atomicAdd(&s.num_biased, 1);
-          s.biased[at] = static_cast<uint16_t>(token - c0);
-          s.bias[at] = sum;
-          touch(token - c0, atomicOr(&s.count[token - c0], kBiased));
+    if (total > P.L || prompt < 0 || prompt > total) t.bad |= SPECV_DEV_BAD_CACHE;
+    if (!(rho > 0.0f) || !isfinite(rho) || !isfinite(freq) || !isfinite(pres))
+      t.bad |= SPECV_DEV_BAD_PENALTY;
+    if (lane == 0 && t.bad) atomicOr(&s.bad, static_cast<int>(t.bad));
+  }
+  bool bad_token = false;
+  {
+    const int32_t* names = P.bias_tokens + static_cast<int64_t>(b) * P.num_bias;
+    const float* values = P.bias_values + static_cast<int64_t>(b) * P.num_bias;
+    for (int i = tid; i < P.num_bias; i += kThreads) {
+      const int token = names[i];
+      bad_token |= token >= P.V;
+      if (token < c0 || token >= c1) continue;
+      // the first place that names a token adds up all of them, in their order
+      float sum = 0.0f;
+      bool first = true;
+      for (int j = 0; j < P.num_bias; j++)
+        if (names[j] == token) {
+          if (j < i) first = false;
+          sum = sum + values[j];
         }
+      if (first) {
+        const int at = atomicAdd(&s.num_biased, 1);
+        s.biased[at] = static_cast<uint16_t>(token - c0);
+        s.bias[at] = sum;
+        touch(token - c0, atomicOr(&s.count[token - c0], kBiased));
       }
     }
-    if (bad_token) atomicOr(&s.bad, SPECV_DEV_BAD_TOKEN);
   }
+  auto take = [&]() {
+    const int ticket = lane == 0 ? atomicAdd(&s.ticket, 1) : 0;
+    return __shfl_sync(kFullMask, ticket, 0);
+  };
+  int ticket = take();
+  const int parts = fits ? (total + kTokens - 1) / kTokens : 0;
+  if (ticket < parts) {
+    const int32_t* hist = P.history + b * P.history_stride;
+    const bool vectors = reinterpret_cast<uintptr_t>(hist) % 16 == 0;
+    unsigned largest = 0;
+    // Of the text's tokens a small part is in this chunk: a warp gathers those
+    // first, and counts them 32 at a time.  (Counting each where it is found took
+    // three times the instructions: nearly always one of 32 lanes has one.)
+    uint32_t* found = s.found[tid / 32];
+    int waiting = 0;  // the same on every lane
+    auto gather = [&](int i, int token) {
+      const uint32_t e = token - c0;
+      if (i < total) largest = max(largest, static_cast<unsigned>(token));
+      const bool mine = i < total && e < static_cast<uint32_t>(c1 - c0);
+      const uint32_t who = __ballot_sync(kFullMask, mine);
+      if (mine) found[waiting + __popc(who & ((1u << lane) - 1))] = e | (i < prompt ? kInPrompt : 0);
+      waiting += __popc(who);
+    };
+    auto count_found = [&](int most) {  // all but `most` at the front
+      __syncwarp();
+      while (waiting > most) {
+        const int at = waiting - 1 - lane;
+        if (at >= 0 && at >= waiting - 32) {
+          const uint32_t word = found[at], e = word & ~kInPrompt;
+          touch(e, word & kInPrompt ? atomicOr(&s.count[e], kInPrompt) : atomicAdd(&s.count[e], 1u));
+        }
+        waiting = max(waiting - 32, 0);
+      }
+      __syncwarp();
+    };
+    for (; ticket < parts; ticket = take()) {
+      int4 t[kTokens / 128];
+#pragma unroll
+      for (int k = 0; k < kTokens / 128; k++) {
+        const int i = ticket * kTokens + k * 128 + lane * 4;
+        t[k] = make_int4(0, 0, 0, 0);
+        if (vectors && i + 3 < total) {
+          t[k] = *reinterpret_cast<const int4*>(hist + i);
+        } else {
+          if (i < total) t[k].x = hist[i];
+          if (i + 1 < total) t[k].y = hist[i + 1];
+          if (i + 2 < total) t[k].z = hist[i + 2];
+          if (i + 3 < total) t[k].w = hist[i + 3];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kTokens / 128; k++) {
+        const int i = ticket * kTokens + k * 128 + lane * 4;
+        gather(i, t[k].x);
+        gather(i + 1, t[k].y);
+        gather(i + 2, t[k].z);
+        gather(i + 3, t[k].w);
+        count_found(31);
+      }
+    }
+    count_found(0);
+    bad_token |= largest >= static_cast<unsigned>(P.V);
+  }
+  if (bad_token) atomicOr(&s.bad, SPECV_DEV_BAD_TOKEN);
 
   const T* in0 = reinterpret_cast<const T*>(P.in) + b * P.batch_stride;
   T* out0 = reinterpret_cast<T*>(P.out) + b * P.out_batch_stride;
@@ -229,9 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
   struct Segment {
     int row, s0, s1;
   };
-  auto take = [&](uint32_t (&keep)[kMine]) {
-    int ticket = lane == 0 ? atomicAdd(&s.ticket, 1) : 0;
-    ticket = __shfl_sync(kFullMask, ticket, 0);
+  auto segment_of = [&](int ticket, uint32_t (&keep)[kMine]) {
+    ticket -= parts;
     Segment g{-1, 0, 0};
     if (ticket >= tickets) return g;
     g.row = first_row + ticket / kSegments;
@@ -247,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
     return g;
   };
   uint32_t keep_next[kMine];
-  Segment next = take(keep_next);
+  Segment next = segment_of(ticket, keep_next);
   while (next.row >= 0) {
     const int row = next.row, s0 = next.s0, s1 = next.s1;
     uint32_t keep[kMine];
@@ -265,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
           if (keep[u0 + u])  // where nothing is allowed there is nothing to read
             data[u] = *reinterpret_cast<const uint4*>(in + s0 + ((u0 + u) * 32 + lane) * kVec);
         if (!asked) {
-          next = take(keep_next);
+          next = segment_of(take(), keep_next);
           asked = true;
         }
 #pragma unroll
@@ -303,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
               out[at + e] = keep >> e & 1 ? in[at + e] : static_cast<T>(E::kNegInf);
         }
       }
-      next = take(keep_next);
+      next = segment_of(take(), keep_next);
     }
   }
   __syncthreads();
@@ -318,26 +354,40 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
 
   // The entries that the text, a draft or a bias touches.  (In place, the copy
   // left them as they were, or masked.)
-  const int touched = s.touched, blocks = (touched + 31) / 32;
-  for (int unit = tid / 32; unit < blocks * (last_row - first_row); unit += kThreads / 32) {
-    const int row = first_row + unit / blocks, k = unit % blocks * 32 + lane;
-    if (k >= touched) continue;
-    const int e = s.list[k], t = c0 + e;
-    if (P.allowed && !(mask_of(row)[t >> 5] >> (t & 31) & 1)) continue;
-    float z = E::load(in0[row * P.row_stride + t]);
-    const uint32_t w = s.count[e];
-    uint32_t count = w & kCount;
-    if (w & kDrafted) {
-      // the root (node 0) is the text's last token already
-      const uint64_t path = s.path[row];
-      for (int j = 1; j <= row; j++) count += s.drafted[j] == e && (path >> j & 1);
+  const int touched = s.touched, blocks = (touched + 31) / 32, pairs = (last_row - first_row + 1) / 2;
+  for (int unit = tid / 32; unit < blocks * pairs; unit += kThreads / 32) {
+    const int pair = unit / blocks, i = (unit - pair * blocks) * 32 + lane;
+    if (i >= touched) continue;
+    const int e = s.list[i], t = c0 + e, row0 = first_row + 2 * pair;
+    T z[2];
+    bool keep[2];
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+      keep[r] = row0 + r < last_row;
+      if (!keep[r]) continue;
+      z[r] = in0[(row0 + r) * P.row_stride + t];
+      if (P.allowed) keep[r] = mask_of(row0 + r)[t >> 5] >> (t & 31) & 1;
     }
-    if (count || (w & kInPrompt)) z = z > 0.0f ? z / rho : z * rho;
-    if (count) z = fmaf(-freq, static_cast<float>(count), z) - pres;
+    const uint32_t w = s.count[e];
+    float bias = 0.0f;
     if (w & kBiased)
       for (int j = 0; j < s.num_biased; j++)
-        if (s.biased[j] == e) z += s.bias[j];
-    out0[row * P.out_row_stride + t] = E::store(z);
+        if (s.biased[j] == e) bias = s.bias[j];
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+      if (!keep[r]) continue;
+      uint32_t count = w & kCount;
+      if (w & kDrafted) {
+        // the root (node 0) is the text's last token already
+        const uint64_t path = s.path[row0 + r];
+        for (int j = 1; j <= row0 + r; j++) count += s.drafted[j] == e && (path >> j & 1);
+      }
+      float x = E::load(z[r]);
+      if (count || (w & kInPrompt)) x = x > 0.0f ? x / rho : x * rho;
+      if (count) x = fmaf(-freq, static_cast<float>(count), x) - pres;
+      if (w & kBiased) x += bias;
+      out0[(row0 + r) * P.out_row_stride + t] = E::store(x);
+    }
   }
 }
 
@@ -360,7 +410,7 @@ template <int DT, Layout kLayout>
 cudaError_t launch(Params& P, int B, cudaStream_t stream) {
   // Large chunks read the text less often; small ones fill the machine where
   // requests are few.
-  P.rows = P.R < 8 ? P.R : 8;
+  P.rows = P.R < kMaxRows ? P.R : kMaxRows;
   return static_cast<int64_t>(B) * ((P.V + 8191) / 8192) >= 304 ? run<DT, 8192, 256, kLayout>(P, B, stream)
                                                                 : run<DT, 1024, 256, kLayout>(P, B, stream);
 }
