@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // copies of 16 bytes wrote through the generic proxy, the MMA reads through the other
       if (!P.box_rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     };
-    uint32_t tile = 0, jobs = 0;  // key tiles so far, copies before this item
+    uint32_t jobs = 0;            // copies before this item
     uint32_t issued[2] = {0, 0};  // scores or sums of each stream so far
     if (warp == kScoreWarp && lane == 0) {
       const int steps = (C.head_dim + 15) / 16;
@@ -705,14 +705,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         done_item();
         barrier_wait(smem_of(&s.q_full[q_buffer]), q_use & 1, gave_up);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (int i = 0; i < tiles; i++, tile++) {
+        for (int i = 0; i < tiles; i++) {
           const uint32_t job = jobs + S::key_job(i);
           kv_wait(job);
           if (kPair) {
             scores(0, base, stage_at(job));
             if (second) scores(1, base + S::kQueryBytes, stage_at(job));
           } else {
-            scores(tile & 1, base + q_buffer * S::kQueryBytes, stage_at(job));
+            scores(i & 1, base + q_buffer * S::kQueryBytes, stage_at(job));
           }
           mma_commit(smem_of(&s.kv_empty[job % kStages]));
         }
@@ -743,14 +743,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool second = kPair && w.rows(P.group, S::kRowTile) > kRows;
         const int tiles = w.t1 - w.t0;
         done_item();
-        for (int i = 0; i < tiles; i++, tile++) {
+        for (int i = 0; i < tiles; i++) {
           const uint32_t job = jobs + S::value_job(i, tiles);
           kv_wait(job);
           if (kPair) {
             sums(0, stage_at(job), i == 0);
             if (second) sums(1, stage_at(job), i == 0);
           } else {
-            sums(tile & 1, stage_at(job), i < 2);
+            sums(i & 1, stage_at(job), i < 2);
           }
           mma_commit(smem_of(&s.kv_empty[job % kStages]));
         }
@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quarter * 32 + lane;  // of the stream's tile
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const float c = P.scale_log2;
-    uint32_t tile = 0, jobs = 0, scores[2] = {0, 0};  // scores: tiles of each stream so far
+    uint32_t jobs = 0, scored = 0;  // scored: tiles of this stream so far
     while (true) {
       const uint32_t item = items;
       const Item& given = next_item();
@@ -954,17 +954,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       int taken[2] = {0, 0};  // tiles of this item that each stream took
       float m = -INFINITY, l = 0.0f;  // m: the maximum that O and l were taken with, times c
 
-      for (int t = w.t0; t < w.t1; t++, tile++) {
+      for (int t = w.t0; t < w.t1; t++) {
         if (kPair) {
           taken[0]++;
           if (second) taken[1]++;
           if (st == 1 && !second) continue;
         } else {
-          taken[tile & 1]++;
-          if ((tile & 1) != st) continue;
+          // by the item's own count, so that a row's sums do not depend on what ran before
+          taken[(t - w.t0) & 1]++;
+          if (((t - w.t0) & 1) != st) continue;
         }
+        barrier_wait(smem_of(&s.s_full[st]), scored & 1, gave_up);
         const bool mixed = (t + 1) * kKeys > w.len;  // holds keys that not every row sees
         if (mixed && (!kPair || st == 0)) {
+          // (Only now that the scores are there: a wait tells phases apart by their parity,
+          // so the copy before this one in the same stage must be known to have landed.)
           // A value that is not finite would pass through a weight of 0 into rows that do
           // not see its node: it becomes 0 here and comes back, at the end, for those that do.
           const uint32_t job = jobs + S::value_job(t - w.t0, w.t1 - w.t0), stage = job % kStages;
@@ -1000,7 +1004,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (changed || stale) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        barrier_wait(smem_of(&s.s_full[st]), scores[st] & 1, gave_up);
         __syncwarp();
         tmem_fence_after();
         const bool first = taken[st] == 1;
@@ -1033,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!first && __any_sync(kFullMask, rise)) {
             // the last update of O must be done
-            barrier_wait(smem_of(&s.o_full[st]), (scores[st] - 1) & 1, gave_up);
+            barrier_wait(smem_of(&s.o_full[st]), (scored - 1) & 1, gave_up);
             __syncwarp();
             tmem_fence_after();
             l *= by;
@@ -1079,21 +1082,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) barrier_arrive(smem_of(&s.p_full[st][1]));
-        scores[st]++;
+        scored++;
       }
 
       jobs += 2 * (w.t1 - w.t0);
 
-      // The item's end: both streams' last updates, and what they know.
-      if (!kPair) scores[st ^ 1] += taken[st ^ 1];
-      else if (st == 0) scores[1] += taken[1];
-      else scores[0] += taken[0];
-#pragma unroll
-      for (int k = 0; k < 2; k++)
-        if (taken[k]) barrier_wait(smem_of(&s.o_full[k]), (scores[k] - 1) & 1, gave_up);
-      tmem_fence_after();
+      // The item's end: this stream's last sum, and by the barrier the other's too.
+      if (taken[st]) barrier_wait(smem_of(&s.o_full[st]), (scored - 1) & 1, gave_up);
       s.stats[st][row] = make_float2(m, l);
+      tmem_fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");
+      tmem_fence_after();
       const uint64_t fix = *odd & visible;
       const float2 other = s.stats[st ^ 1][row];
       if (tid == 0) s.odd_values[(item & 1) ^ 1] = 0;

@@ -76,10 +76,10 @@ class Attn:
                 None if self.parents is None else i32(self.parents),
                 i32(self.nodes) if self.given_nodes else None)
 
-    def want(self):
+    def want(self, many=False):
         scale = self.scale if self.scale is not None else self.D ** -0.5
-        parts = ref.attention(self.q, self.k, self.v, self.table, self.lens, self.parents, self.nodes,
-                              scale)
+        parts = (ref.attention_of_many if many else ref.attention)(
+            self.q, self.k, self.v, self.table, self.lens, self.parents, self.nodes, scale)
         keys = max(self.lens) + self.N
         return parts, ref.attention_tolerance(parts, self.D, keys, self.dtype)
 
@@ -135,6 +135,40 @@ def test_attention_many_short_requests(sv):
     lens = np.random.default_rng(2).integers(0, 90, 300)
     nodes = np.random.default_rng(4).integers(1, 4, 300)
     Attn(8, 300, 3, 4, 2, 64, 16, lens, BF16, nodes=nodes).check(sv)
+
+
+@pytest.mark.parametrize("dtype,B,N,Hq,Hkv,D,page,most", [
+    (BF16, 24, 4, 32, 8, 128, 16, 3000),     # at most 64 rows
+    (F16, 40, 13, 32, 8, 64, 64, 2000),
+    (BF16, 24, 32, 32, 8, 128, 64, 2900),    # at most 128
+    (F16, 30, 16, 16, 2, 80, 128, 9000),
+    (BF16, 20, 20, 24, 6, 128, 24, 2900),    # pages that take single copies
+    (BF16, 16, 64, 32, 4, 128, 256, 4500),   # more: two row tiles on the same keys, two of them
+    (F16, 20, 40, 40, 8, 64, 32, 2300),
+    (BF16, 16, 33, 48, 6, 112, 100, 3000),
+])
+def test_attention_fills_the_machine(sv, dtype, B, N, Hq, Hkv, D, page, most):
+    """More work than eight tiles for each SM: runs are dealt out, items cut
+    anywhere, trees lie across tiles; the same bits every time."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, most, B)
+    lens[:4] = [most, 870, 127, 128 * 7 - 1]
+    a = Attn(B + N, B, N, Hq, Hkv, D, page, lens, dtype, nodes=rng.integers(1, N + 1, B))
+    tiles = sum(-(-(x + N) // 128) for x in a.lens) * Hkv * -(-N * Hq // Hkv // 256)
+    assert tiles > 8 * 152
+    parts, tol = a.want(many=True)
+    args, ws = a.args(), sv.AttentionWorkspace(B, N, Hq, Hkv, D, device="cuda")
+    first = None
+    for _ in range(4):
+        out = torch.full(a.q.shape, 7.0, dtype=dtype, device="cuda")
+        got, status = sv.tree_attention(*args, out=out, workspace=ws)
+        assert status.tolist() == [0] * B
+        for b in range(B):
+            n = int(a.nodes[b])
+            close(got[b, :n], parts[0][b, :n], tol[b, :n], f"request {b}")
+            assert (got[b, n:] == 7.0).all()
+        assert first is None or torch.equal(got, first)
+        first = got.clone()
 
 
 @pytest.mark.parametrize("sharp", [0.0, 12.0])

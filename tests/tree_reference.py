@@ -79,6 +79,33 @@ def attention(q, k, v, table, lens, parents, nodes, scale):
     return out, mass, reach, spread
 
 
+def attention_of_many(q, k, v, table, lens, parents, nodes, scale):
+    """attention() for finite caches of many keys: a request at a time."""
+    B, N, Hq, D = q.shape
+    page, G = k.shape[1], Hq // k.shape[2]
+    out = torch.full(q.shape, float("nan"), dtype=torch.float64, device=q.device)
+    mass, reach, spread = out.clone(), out.clone(), out.clone()
+    for b in range(B):
+        n, first = int(nodes[b]), int(lens[b])
+        seen = torch.zeros(n, first + n, dtype=torch.bool)
+        seen[:, :first] = True
+        for i in range(n):
+            seen[i, [first + j for j in path_of(parents, b, i)]] = True
+        seen = seen.to(q.device)
+        pg, off = slots(table, b, page, list(range(first + n)), q.device)
+        kk, vv = k[pg, off].double(), v[pg, off].double()
+        for h in range(Hq):
+            qq, kh, vh = q[b, :n, h].double(), kk[:, h // G], vv[:, h // G]
+            s = (qq @ kh.T * scale).masked_fill(~seen, float("-inf"))
+            p = torch.softmax(s, -1)
+            total = torch.exp(s - s.amax(-1, keepdim=True)).sum(-1, keepdim=True)
+            out[b, :n, h], mass[b, :n, h] = p @ vh, p @ vh.abs()
+            far = (qq.abs() @ kh.abs().T * scale).masked_fill(~seen, 0.0)
+            reach[b, :n, h] = far.amax(-1, keepdim=True)
+            spread[b, :n, h] = seen.double() @ vh.abs() / total
+    return out, mass, reach, spread
+
+
 def attention_tolerance(parts, D, keys, dtype):
     """Bound on |kernel - out|, element by element.
 
