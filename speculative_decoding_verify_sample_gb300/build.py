@@ -1,10 +1,13 @@
-"""Builds libspecverify.so in-tree with nvcc for sm_103a (GB300)."""
+"""Builds libspecverify.so in-tree with nvcc for sm_103a (GB300), and beside it
+the argument side of the drafted tree's operators, a Python extension on torch's
+tensors, with g++."""
 
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -13,6 +16,7 @@ SOURCES = [os.path.join(PKG_DIR, "csrc", name)
            for name in ("specverify.cu", "cache.cu", "attention.cu", "logits.cu")]
 HEADERS = [os.path.join(INCLUDE, "specverify.h"), os.path.join(PKG_DIR, "csrc", "cache.cuh")]
 LIB_PATH = os.path.join(PKG_DIR, "libspecverify.so")
+BINDING_SOURCE = os.path.join(PKG_DIR, "csrc", "binding.cpp")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -31,10 +35,59 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_path() -> str:
+    """The extension's file: one of another torch or Python does not load, so both
+    versions are in its name."""
+    import torch
+    return os.path.join(
+        PKG_DIR, f"_binding-{torch.__version__}-py{sysconfig.get_python_version()}.so")
+
+
+def _build_binding(force: bool, verbose: bool):
+    """Starts the extension's compiler where it is needed; returns what waits for
+    it.  Without torch there are no tensors to bind and nothing is built."""
+    try:
+        import torch
+    except ImportError:
+        return lambda: None
+    home = os.path.dirname(torch.__file__)
+    path = binding_path()
+    if not force and not _stale(path, [BINDING_SOURCE, HEADERS[0]]):
+        return lambda: None
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    include = [INCLUDE, os.path.join(home, "include"),
+               os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in include), BINDING_SOURCE, "-o", tmp, f"-L{home}/lib",
+           f"-Wl,-rpath,{home}/lib", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd))
+    compiler = subprocess.Popen(cmd)
+
+    def wait():
+        if compiler.wait() != 0:
+            raise subprocess.CalledProcessError(compiler.returncode, cmd)
+        os.replace(tmp, path)
+    return wait
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile the CUDA library if a source or header is newer than it."""
+    """Compile the CUDA library and the binding's extension where a source or
+    header is newer than them."""
+    wait = _build_binding(force, verbose)
+    try:
+        _build_library(force, verbose, extra_flags)
+    finally:
+        wait()
+    return LIB_PATH
+
+
+def _build_library(force: bool, verbose: bool, extra_flags):
     if not force and not _stale(LIB_PATH, SOURCES + HEADERS):
-        return LIB_PATH
+        return
     nvcc = nvcc_path()
     cuda_lib = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "lib64")
     tmp = LIB_PATH + f".tmp{os.getpid()}"
@@ -46,7 +99,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

@@ -4,37 +4,45 @@ masks on the logits, and the move of the accepted path's cache rows
 ("Decodificación Especulativa y EAGLE", section "Verificación de Atención en
 Árvore"; "Accelerating Sonar through speculation", section "EAGLE").
 
-As in the rest of the binding: shapes, types and devices are checked here,
-the limits and alignments in the library; every step runs in its kernels.
+Shapes, types and devices are checked in csrc/binding.cpp (these calls take a few
+microseconds on the device, so what the host spends on them counts), the limits
+and alignments in the library; every step runs in its kernels.
 """
 
 from __future__ import annotations
 
 import contextlib
-import math
-import struct
+import ctypes
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
-from ._native import ATTENTION_HEADER_BYTES, SPECV_BF16, SPECV_F16, SPECV_F32, check, lib
+from ._native import ATTENTION_HEADER_BYTES, SpecVerifyError, check, lib
+from .build import binding_path
 
-_CACHE_DTYPES = {torch.bfloat16: SPECV_BF16, torch.float16: SPECV_F16}
-_LOGIT_DTYPES = {torch.bfloat16: SPECV_BF16, torch.float32: SPECV_F32}
-_INT32, _FLOAT32 = torch.int32, torch.float32
-# specv_cache and specv_rows of the header, as bytes: these calls take a few
-# microseconds on the device, so what the host spends on them counts
-_pack_cache = struct.Struct("@4P4q8i").pack
-_pack_rows = struct.Struct("@P3q").pack
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_binding = None
 
 
-def _elsewhere(device, stream):
-    """Whether the call has to be made on another device or stream than the
-    current ones (it allocates on what it launches on)."""
-    if device.type != "cuda":
-        raise ValueError(f"the operators on a drafted tree take CUDA tensors, got {device}")
-    return stream is not None or device.index != torch.cuda.current_device()
+def _load():
+    """The extension, bound to the library.  Raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        path, handle = binding_path(), lib()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built; run "
+                               "speculative_decoding_verify_sample_gb300.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_binding", loader))
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+            handle.spec_append_nodes, handle.spec_tree_attention, handle.spec_keep_path,
+            handle.spec_process_logits, handle.specv_attention_workspace_bytes,
+            handle.specv_workspace_init)))
+        _binding = module
+    return _binding
 
 
 @contextlib.contextmanager
@@ -49,85 +57,17 @@ def _there(device, stream):
                 yield
 
 
-def _need(name, t, shape, dtype, dev):
-    """t is a contiguous tensor of this shape, type and device."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != dev \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
-                         f"on {dev}")
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _strides(t, shape):
-    """Strides in elements; those of a single entry are never used."""
-    st = t.stride()
-    return [s if n > 1 else 0 for s, n in zip(st, shape)] if 1 in shape else st
-
-
-def _rows(name, t, shape, dtype, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != dev:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {dev}")
-    b, n, h, d = _strides(t, shape)
-    if d != 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
-    return _pack_rows(t.data_ptr(), b, n, h)
-
-
-def _cache(k_cache, v_cache, page_table, cache_lens, layered=False):
-    """(the cache argument, B, heads, head_dim)."""
-    shape, dtype, dev = k_cache.shape, k_cache.dtype, k_cache.device
-    if len(shape) != 4 and not (layered and len(shape) == 5):
-        raise ValueError("k_cache must be [pages, page_size, heads, head_dim]"
-                         + (" or [layers, pages, page_size, heads, head_dim]" if layered else ""))
-    code = _CACHE_DTYPES.get(dtype)
-    if code is None:
-        raise TypeError(f"k_cache must be bfloat16 or float16, got {dtype}")
-    st = _strides(k_cache, shape)
-    if v_cache.shape != shape or v_cache.dtype != dtype or v_cache.device != dev \
-            or _strides(v_cache, shape) != st or st[-1] != 1:
-        raise ValueError("v_cache must have k_cache's shape, strides, type and device, and both a "
-                         "contiguous last dimension")
-    if page_table.dim() != 2 or page_table.dtype != _INT32 or page_table.device != dev \
-            or (page_table.stride(1) != 1 and page_table.shape[1] > 1):
-        raise ValueError(f"page_table must be an int32 tensor [B, pages of a request] on {dev} with "
-                         "contiguous rows")
-    B, max_pages = page_table.shape
-    _need("cache_lens", cache_lens, (B,), _INT32, dev)
-    pages, page_size, heads, head_dim = shape[-4:]
-    layers, layer_stride = (shape[0], st[0]) if len(shape) == 5 else (1, 0)
-    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-                       cache_lens.data_ptr(), layer_stride, st[-4], st[-3], st[-2], layers, pages,
-                       page_size, max_pages, page_table.stride(0) if B > 1 else max_pages, heads,
-                       head_dim, code), B, heads, head_dim
-
-
-def _tree(parents, n_nodes, B, N, dev):
-    if parents is not None:
-        _need("parents", parents, (B, N), _INT32, dev)
-    if n_nodes is not None:
-        _need("n_nodes", n_nodes, (B,), _INT32, dev)
-
-
-def _per_request(name, t, B, dev):
-    """An int32 output [B], made here if the caller gave none."""
-    if t is None:
-        return torch.empty(B, dtype=_INT32, device=dev)
-    _need(name, t, (B,), _INT32, dev)
-    return t
-
-
-def _new(n_nodes, shape, dtype, dev):
-    """An output that the caller did not give: zeros where rows may be left."""
-    return (torch.empty if n_nodes is None else torch.zeros)(shape, dtype=dtype, device=dev)
-
-
-def _nodes_of(q):
-    if q.dim() != 4:
-        raise ValueError("q must be [B, N, q_heads, head_dim]")
-    return q.shape
+def _call(name, fn, tensor, stream, *args):
+    """fn(*args) on tensor's device and the stream: its outputs are allocated where
+    it launches."""
+    cuda = isinstance(tensor, torch.Tensor) and tensor.is_cuda
+    out = fn(*args) if stream is None or not cuda else None
+    if out is None:
+        with _there(tensor.device, stream):
+            out = fn(*args)
+    if out.__class__ is int:
+        raise SpecVerifyError(name, out)
+    return out
 
 
 def append_nodes(q, k, v, k_cache, v_cache, page_table, cache_lens, inv_freq=None, parents=None,
@@ -148,39 +88,9 @@ def append_nodes(q, k, v, k_cache, v_cache, page_table, cache_lens, inv_freq=Non
     [B] int32 (None: all N).  Returns (q_out, status [B] int32: 0 or DEV_*
     bits); rows of q_out behind n_nodes[b] are left as they were (zeros in a
     new one).  ``q_out`` may be q.  Asynchronous."""
-    B, N, Hq, D = _nodes_of(q)
-    cache, rows, heads, head_dim = _cache(k_cache, v_cache, page_table, cache_lens)
-    dev, dtype = k_cache.device, k_cache.dtype
-    if rows != B or head_dim != D:
-        raise ValueError(f"q is for {B} requests and heads of {D}, the cache for {rows} and "
-                         f"{head_dim}")
-    q_arg = _rows("q", q, q.shape, dtype, dev)
-    k_arg = _rows("k", k, (B, N, heads, D), dtype, dev)
-    v_arg = _rows("v", v, (B, N, heads, D), dtype, dev)
-    _tree(parents, n_nodes, B, N, dev)
-    if q_weight is not None:
-        _need("q_weight", q_weight, (D,), dtype, dev)
-    if k_weight is not None:
-        _need("k_weight", k_weight, (D,), dtype, dev)
-    half = 0
-    if inv_freq is not None:
-        half = inv_freq.numel()
-        _need("inv_freq", inv_freq, (half,), _FLOAT32, dev)
-    if _elsewhere(dev, stream):
-        with _there(dev, stream):
-            return append_nodes(q, k, v, k_cache, v_cache, page_table, cache_lens, inv_freq, parents,
-                                n_nodes, q_weight=q_weight, k_weight=k_weight, eps=eps,
-                                interleaved=interleaved, rope_scale=rope_scale, q_out=q_out,
-                                status=status)
-    if q_out is None:
-        q_out = _new(n_nodes, q.shape, dtype, dev)
-    out_arg = q_arg if q_out is q else _rows("q_out", q_out, q.shape, dtype, dev)
-    status = _per_request("status", status, B, dev)
-    check("spec_append_nodes", lib().spec_append_nodes(
-        cache, q_arg, k_arg, v_arg, _ptr(parents), _ptr(n_nodes), B, N, Hq, _ptr(q_weight),
-        _ptr(k_weight), eps, _ptr(inv_freq) if half else None, 2 * half, 1 if interleaved else 0,
-        rope_scale, out_arg, status.data_ptr(), _raw_stream(dev.index)))
-    return q_out, status
+    return _call("spec_append_nodes", (_binding or _load()).append_nodes, k_cache, stream, q, k, v,
+                 k_cache, v_cache, page_table, cache_lens, inv_freq, parents, n_nodes, q_weight,
+                 k_weight, eps, interleaved, rope_scale, q_out, status)
 
 
 class AttentionWorkspace:
@@ -200,7 +110,8 @@ class AttentionWorkspace:
         with torch.cuda.device(dev):
             check("specv_workspace_init", lib().specv_workspace_init(
                 self.tensor.data_ptr(), ATTENTION_HEADER_BYTES,
-                _raw_stream(dev.index) if stream is None else getattr(stream, "cuda_stream", stream)))
+                torch.cuda.current_stream(dev).cuda_stream if stream is None
+                else getattr(stream, "cuda_stream", stream)))
 
 
 def tree_attention(q, k_cache, v_cache, page_table, cache_lens, parents=None, n_nodes=None, *,
@@ -216,31 +127,9 @@ def tree_attention(q, k_cache, v_cache, page_table, cache_lens, parents=None, n_
     scores.  Returns (out [B, N, q_heads, D], status [B] int32: 0 or DEV_*
     bits); rows of out behind n_nodes[b] are left as they were (zeros in a new
     one).  Asynchronous."""
-    B, N, Hq, D = _nodes_of(q)
-    cache, rows, heads, head_dim = _cache(k_cache, v_cache, page_table, cache_lens)
-    dev, dtype = k_cache.device, k_cache.dtype
-    if rows != B or head_dim != D or Hq % heads:
-        raise ValueError(f"q is for {B} requests and {Hq} heads of {D}, the cache for {rows} and "
-                         f"{heads} of {head_dim}")
-    q_arg = _rows("q", q, q.shape, dtype, dev)
-    _tree(parents, n_nodes, B, N, dev)
-    if _elsewhere(dev, stream):
-        with _there(dev, stream):
-            return tree_attention(q, k_cache, v_cache, page_table, cache_lens, parents, n_nodes,
-                                  scale=scale, out=out, status=status, workspace=workspace)
-    if out is None:
-        out = _new(n_nodes, q.shape, dtype, dev)
-    out_arg = _rows("out", out, q.shape, dtype, dev)
-    status = _per_request("status", status, B, dev)
-    if workspace is None:
-        workspace = AttentionWorkspace(B, N, Hq, heads, D, device=dev)
-    elif workspace.tensor.device != dev:
-        raise ValueError(f"workspace is on {workspace.tensor.device}, the cache on {dev}")
-    check("spec_tree_attention", lib().spec_tree_attention(
-        cache, q_arg, _ptr(parents), _ptr(n_nodes), B, N, Hq,
-        1.0 / math.sqrt(D) if scale is None else scale, out_arg, status.data_ptr(),
-        workspace.tensor.data_ptr(), workspace.nbytes, _raw_stream(dev.index)))
-    return out, status
+    return _call("spec_tree_attention", (_binding or _load()).tree_attention, k_cache, stream, q,
+                 k_cache, v_cache, page_table, cache_lens, parents, n_nodes, scale, out, status,
+                 None if workspace is None else workspace.tensor)
 
 
 def keep_path(path_nodes, accepted_len, k_cache, v_cache, page_table, cache_lens, *, new_lens=None,
@@ -251,23 +140,8 @@ def keep_path(path_nodes, accepted_len, k_cache, v_cache, page_table, cache_lens
     may be [layers, pages, page_size, heads, D]: every layer in one call.
     Returns (new_lens [B] = cache_lens + accepted_len + 1, status [B]) int32;
     a flagged request keeps its rows and its length.  Asynchronous."""
-    cache, B, _, _ = _cache(k_cache, v_cache, page_table, cache_lens, layered=True)
-    dev = k_cache.device
-    if path_nodes.dim() != 2:
-        raise ValueError("path_nodes must be [B, N]")
-    N = path_nodes.shape[1]
-    _need("path_nodes", path_nodes, (B, N), _INT32, dev)
-    _need("accepted_len", accepted_len, (B,), _INT32, dev)
-    if _elsewhere(dev, stream):
-        with _there(dev, stream):
-            return keep_path(path_nodes, accepted_len, k_cache, v_cache, page_table, cache_lens,
-                             new_lens=new_lens, status=status)
-    new_lens = _per_request("new_lens", new_lens, B, dev)
-    status = _per_request("status", status, B, dev)
-    check("spec_keep_path", lib().spec_keep_path(
-        cache, path_nodes.data_ptr(), accepted_len.data_ptr(), B, N, new_lens.data_ptr(),
-        status.data_ptr(), _raw_stream(dev.index)))
-    return new_lens, status
+    return _call("spec_keep_path", (_binding or _load()).keep_path, k_cache, stream, path_nodes,
+                 accepted_len, k_cache, v_cache, page_table, cache_lens, new_lens, status)
 
 
 def process_logits(logits, history, seq_lens, prompt_lens=None, *, tokens=None, parents=None,
@@ -288,64 +162,6 @@ def process_logits(logits, history, seq_lens, prompt_lens=None, *, tokens=None, 
     int32: bit t % 32 of word t // 32 set, or z becomes -inf.  Returns (out,
     status [B] int32: 0 or DEV_* bits); rows behind n_nodes[b] are left as
     they were (zeros in a new out).  ``out`` may be logits.  Asynchronous."""
-    if logits.dim() not in (2, 3):
-        raise ValueError("logits must be [B, R, V] or [B, V]")
-    if logits.dtype not in _LOGIT_DTYPES:
-        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
-    shape, dtype, dev = logits.shape, logits.dtype, logits.device
-    B, V = shape[0], shape[-1]
-    R = shape[1] if len(shape) == 3 else 1
-    if history.dim() != 2 or history.dtype != _INT32 or history.device != dev \
-            or history.shape[0] != B or (history.stride(1) != 1 and history.shape[1] > 1):
-        raise ValueError(f"history must be an int32 tensor [B, L] on {dev} with contiguous rows")
-    _need("seq_lens", seq_lens, (B,), _INT32, dev)
-    _tree(parents, n_nodes, B, R, dev)
-    if tokens is not None:
-        _need("tokens", tokens, (B, R if parents is not None else R - 1), _INT32, dev)
-    elif R > 1:
-        raise ValueError("tokens must be given for more than one row")
-    if prompt_lens is not None:
-        _need("prompt_lens", prompt_lens, (B,), _INT32, dev)
-    if repetition is not None:
-        _need("repetition", repetition, (B,), _FLOAT32, dev)
-    if frequency is not None:
-        _need("frequency", frequency, (B,), _FLOAT32, dev)
-    if presence is not None:
-        _need("presence", presence, (B,), _FLOAT32, dev)
-    if (bias_tokens is None) != (bias_values is None):
-        raise ValueError("bias_tokens and bias_values go together")
-    num_bias = 0
-    if bias_tokens is not None:
-        num_bias = bias_tokens.shape[-1]
-        _need("bias_tokens", bias_tokens, (B, num_bias), _INT32, dev)
-        _need("bias_values", bias_values, (B, num_bias), _FLOAT32, dev)
-    if allowed is not None:
-        _need("allowed", allowed, shape[:-1] + (-(-V // 32),), _INT32, dev)
-
-    def rows(name, t):
-        if t.shape != shape or t.dtype != dtype or t.device != dev:
-            raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {dev}")
-        st = _strides(t, shape)
-        if V > 1 and st[-1] != 1:
-            raise ValueError(f"{name} must have a contiguous last dimension")
-        return st[0], st[1] if R > 1 else 0
-
-    batch_stride, row_stride = rows("logits", logits)
-    if _elsewhere(dev, stream):
-        with _there(dev, stream):
-            return process_logits(logits, history, seq_lens, prompt_lens, tokens=tokens,
-                                  parents=parents, n_nodes=n_nodes, repetition=repetition,
-                                  frequency=frequency, presence=presence, bias_tokens=bias_tokens,
-                                  bias_values=bias_values, allowed=allowed, out=out, status=status)
-    if out is None:
-        out = _new(n_nodes, shape, dtype, dev)
-    out_batch_stride, out_row_stride = rows("out", out)
-    status = _per_request("status", status, B, dev)
-    check("spec_process_logits", lib().spec_process_logits(
-        logits.data_ptr(), batch_stride, row_stride, _LOGIT_DTYPES[dtype], B, R, V,
-        _ptr(tokens) if R > 1 else None, _ptr(parents), _ptr(n_nodes), history.data_ptr(),
-        history.stride(0) if B > 1 else 0, history.shape[1], seq_lens.data_ptr(), _ptr(prompt_lens),
-        _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(bias_tokens), _ptr(bias_values),
-        num_bias, _ptr(allowed), out.data_ptr(), out_batch_stride, out_row_stride, status.data_ptr(),
-        _raw_stream(dev.index)))
-    return out, status
+    return _call("spec_process_logits", (_binding or _load()).process_logits, logits, stream, logits,
+                 history, seq_lens, prompt_lens, tokens, parents, n_nodes, repetition, frequency,
+                 presence, bias_tokens, bias_values, allowed, out, status)
