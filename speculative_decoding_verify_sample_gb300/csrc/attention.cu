@@ -73,7 +73,9 @@ struct Workspace {
   Header* header;
   Cut* cuts;      // [runs]
   float2* stats;  // [2 runs][part_rows] pieces' m c and l: of an item that began before the
-  float* parts;   // [2 runs][part_rows][dim]   run, then of one that goes on behind it; their O
+                  // run, then of one that goes on behind it
+  float4* parts;  // [2 runs][dim / 4][part_rows] their O, four columns of a row together: the
+                  // softmax's lanes have a row each, and adjacent rows make whole lines
 };
 
 struct AttnParams {
@@ -1122,8 +1124,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mine = row < my_rows;
         uint16_t* out = P.out.data + w.b * P.out.batch_stride + node * P.out.node_stride +
                         (w.h * P.group + g) * P.out.head_stride;
-        const int64_t part =
-            static_cast<int64_t>(2 * run + (w.t0 == 0)) * P.part_rows + first_row + row;
+        const int64_t slot = 2 * run + (w.t0 == 0);
+        float4* part = P.ws.parts + slot * (DP / 4) * P.part_rows + first_row + row;
         constexpr int kCols = kPair ? DP : DP / 2;
         const int col0 = kPair ? 0 : st * kCols;
 #pragma unroll 1
@@ -1176,12 +1178,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (mine) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(P.ws.parts + part * DP + col0 + k + e) =
-                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              part[(col0 + k + e) / 4 * P.part_rows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
           __syncwarp();
         }
-        if (!whole && mine && (kPair || st == 0)) P.ws.stats[part] = make_float2(m, l);
+        if (!whole && mine && (kPair || st == 0)) 
+          P.ws.stats[slot * P.part_rows + first_row + row] = make_float2(m, l);
       }
       tmem_fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -1201,18 +1203,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the pieces of the items that runs cut:
 //   m = max m_i, O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i, in order.
-// A block to a cut.  A warp takes eight rows and kPieces pieces at a time, all of
-// their loads in flight, and where rows are few (then pieces are many) the warps
-// share out the pieces.  A lane has four columns of each row, and the weight of
-// one row and piece.  The code is short on purpose: it runs once, and fetching
-// it was most of the time of an unrolled form (5.7 of 8 us).
+// A block to a cut.  A warp takes eight rows and kJoinPieces pieces at a time, all
+// of their loads in flight, and where rows are few (then pieces are many) the
+// warps share out the pieces.  A lane has one row and every fourth four columns
+// of it.  The code is short on purpose: it runs once, and fetching it was most
+// of the time of an unrolled form.
 constexpr int kJoinRows = 8;
 
 template <class E, int DP, int kRowTile, int kJoinWarps, int kRowGroups>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P) {
   constexpr int kShares = kJoinWarps / kRowGroups;
   constexpr int kJoinPieces = kShares > 1 ? 4 : 2;
-  __shared__ float4 s_o[kShares > 1 ? kJoinWarps : 1][kJoinRows][32];
+  constexpr int kQuads = DP / 16;  // of a lane
+  __shared__ float4 s_o[kShares > 1 ? kJoinWarps : 1][kQuads][32];
   __shared__ float2 s_ml[kJoinWarps][kJoinRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int group = warp % kRowGroups, share = warp / kRowGroups;
@@ -1228,93 +1231,85 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     return;
   const int rows = min(kRowTile, cut.n * P.group - cut.row_tile * kRowTile);
   const int flagged = P.status[cut.b];  // its first piece has cleared the rows
-  const int d = 4 * lane, my_row = lane / kJoinPieces % kJoinRows, my_piece = lane % kJoinPieces;
+  const int row = lane % kJoinRows, quad = lane / kJoinRows;
 #pragma unroll 1
   for (int row0 = group * kJoinRows; row0 < (kShares > 1 ? kRowGroups * kJoinRows : rows);
        row0 += kRowGroups * kJoinRows) {
-    // the first piece ends a run, the others begin theirs (slots have whole eights of rows)
-    auto index = [&](int i) {
-      const int slot = 2 * (run - 1 + i) + (i == 0);
-      return static_cast<int64_t>(slot) * P.part_rows + min(row0, P.part_rows - kJoinRows);
-    };
-    float m = -INFINITY, l = 0.0f;  // of row my_row
-    float4 o[kJoinRows];
+    // (slots have whole eights of rows)
+    const int at = min(row0, P.part_rows - kJoinRows) + row;
+    float m = -INFINITY, l = 0.0f;
+    float4 o[kQuads];
 #pragma unroll
-    for (int r = 0; r < kJoinRows; r++) o[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < kQuads; j++) o[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // What is there so far keeps `old` of its weight, the other gets `by`.
+    auto add = [&](float old, float by, const float4* x, int step) {
+#pragma unroll
+      for (int j = 0; j < kQuads; j++) {
+        const float4 y = x[j * step];
+        o[j].x = fmaf(by, y.x, o[j].x * old);
+        o[j].y = fmaf(by, y.y, o[j].y * old);
+        o[j].z = fmaf(by, y.z, o[j].z * old);
+        o[j].w = fmaf(by, y.w, o[j].w * old);
+      }
+    };
 #pragma unroll 1
     for (int i0 = share * kJoinPieces; i0 < cut.pieces; i0 += kShares * kJoinPieces) {
-      float4 x[kJoinPieces][kJoinRows];
+      float4 x[kJoinPieces][kQuads];
+      float2 ml[kJoinPieces];
 #pragma unroll
       for (int i = 0; i < kJoinPieces; i++) {
-        const float4* from =
-            reinterpret_cast<const float4*>(P.ws.parts + index(i0 + i) * DP + d % DP);
+        // the first piece ends a run, the others begin theirs
+        const int piece = i0 + i;
+        const int64_t slot = 2 * (run - 1 + piece) + (piece == 0);
+        const bool real = piece < cut.pieces;
+        const float4* from = P.ws.parts + (slot * (DP / 4) + quad) * P.part_rows + at;
+        ml[i] = real ? P.ws.stats[slot * P.part_rows + at] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-        for (int r = 0; r < kJoinRows; r++)
-          x[i][r] = i0 + i < cut.pieces ? from[r * (DP / 4)] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int j = 0; j < kQuads; j++)
+          x[i][j] = real ? from[4 * j * P.part_rows] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      if (i0 + my_piece < cut.pieces) ml = P.ws.stats[index(i0 + my_piece) + my_row];
-      float top = ml.x;
+      float top = m;
 #pragma unroll
-      for (int s = 1; s < kJoinPieces; s *= 2) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, s));
-      top = fmaxf(top, m);
-      const float weight =
-          i0 + my_piece >= cut.pieces ? 0.0f : ml.x == top ? 1.0f : exp2_of(ml.x - top);
-      const float old = m == top ? 1.0f : exp2_of(m - top);
-      float sum = weight * ml.y;
-#pragma unroll
-      for (int s = 1; s < kJoinPieces; s *= 2) sum += __shfl_xor_sync(kFullMask, sum, s);
+      for (int i = 0; i < kJoinPieces; i++) top = fmaxf(top, ml[i].x);
+      float old = m == top ? 1.0f : exp2_of(m - top);
       m = top;
-      l = l * old + sum;
 #pragma unroll
-      for (int r = 0; r < kJoinRows; r++) {
-        const float keep = __shfl_sync(kFullMask, old, r * kJoinPieces);
-        o[r].x *= keep, o[r].y *= keep, o[r].z *= keep, o[r].w *= keep;
-#pragma unroll
-        for (int i = 0; i < kJoinPieces; i++) {
-          const float by = __shfl_sync(kFullMask, weight, r * kJoinPieces + i);
-          o[r].x = fmaf(by, x[i][r].x, o[r].x);
-          o[r].y = fmaf(by, x[i][r].y, o[r].y);
-          o[r].z = fmaf(by, x[i][r].z, o[r].z);
-          o[r].w = fmaf(by, x[i][r].w, o[r].w);
-        }
+      for (int i = 0; i < kJoinPieces; i++) {
+        const float by = i0 + i >= cut.pieces ? 0.0f : ml[i].x == top ? 1.0f : exp2_of(ml[i].x - top);
+        l = fmaf(by, ml[i].y, l * old);
+        add(old, by, x[i], 1);
+        old = 1.0f;
       }
     }
     if (kShares > 1) {
       // the warps' shares, in their order
-      if (my_piece == 0) s_ml[warp][my_row] = make_float2(m, l);
+      if (quad == 0) s_ml[warp][row] = make_float2(m, l);
 #pragma unroll
-      for (int r = 0; r < kJoinRows; r++) s_o[warp][r][lane] = o[r];
+      for (int j = 0; j < kQuads; j++) s_o[warp][j][lane] = o[j];
       __syncthreads();
       if (share) return;  // rows are few: there is no other round
 #pragma unroll 1
       for (int w = 1; w < kShares; w++) {
-        const float2 ml = s_ml[warp + w * kRowGroups][my_row];
+        const float2 ml = s_ml[warp + w * kRowGroups][row];
         const float top = fmaxf(m, ml.x);
         const float old = m == top ? 1.0f : exp2_of(m - top);
-        const float weight = ml.x == top ? 1.0f : exp2_of(ml.x - top);
+        const float by = ml.x == top ? 1.0f : exp2_of(ml.x - top);
         m = top;
-        l = l * old + weight * ml.y;
-#pragma unroll
-        for (int r = 0; r < kJoinRows; r++) {
-          const float keep = __shfl_sync(kFullMask, old, r * kJoinPieces);
-          const float by = __shfl_sync(kFullMask, weight, r * kJoinPieces);
-          const float4 x = s_o[warp + w * kRowGroups][r][lane];
-          o[r].x = o[r].x * keep + by * x.x;
-          o[r].y = o[r].y * keep + by * x.y;
-          o[r].z = o[r].z * keep + by * x.z;
-          o[r].w = o[r].w * keep + by * x.w;
-        }
+        l = fmaf(by, ml.y, l * old);
+        add(old, by, &s_o[warp + w * kRowGroups][0][lane], 32);
       }
     }
+    if (row0 + row >= rows || flagged) continue;
+    const float inv = 1.0f / l;
+    const int flat = cut.row_tile * kRowTile + row0 + row, node = flat / P.group, g = flat - node * P.group;
+    uint16_t* out = P.out.data + cut.b * P.out.batch_stride + node * P.out.node_stride +
+                    (cut.h * P.group + g) * P.out.head_stride;
 #pragma unroll
-    for (int r = 0; r < kJoinRows; r++) {
-      const float inv = 1.0f / __shfl_sync(kFullMask, l, r * kJoinPieces);
-      if (row0 + r >= rows || d >= P.cache.head_dim || flagged) continue;
-      const int flat = cut.row_tile * kRowTile + row0 + r, node = flat / P.group, g = flat - node * P.group;
-      *reinterpret_cast<uint2*>(P.out.data + cut.b * P.out.batch_stride + node * P.out.node_stride +
-                                (cut.h * P.group + g) * P.out.head_stride + d) =
-          make_uint2(E::pack(o[r].x * inv, o[r].y * inv), E::pack(o[r].z * inv, o[r].w * inv));
+    for (int j = 0; j < kQuads; j++) {
+      const int d = 4 * (quad + 4 * j);
+      if (d < P.cache.head_dim)
+        *reinterpret_cast<uint2*>(out + d) = make_uint2(E::pack(o[j].x * inv, o[j].y * inv),
+                                                        E::pack(o[j].z * inv, o[j].w * inv));
     }
   }
 }
@@ -1454,7 +1449,7 @@ specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
   const Workspace ws{reinterpret_cast<Header*>(base),
                      reinterpret_cast<Cut*>(base + SPECV_ATTENTION_HEADER_BYTES),
                      reinterpret_cast<float2*>(base + plan.stats),
-                     reinterpret_cast<float*>(base + plan.parts)};
+                     reinterpret_cast<float4*>(base + plan.parts)};
   const int page = cache->page_size;
   int box_rows = page % 8 == 0 && (page >= kKeys ? page % kKeys == 0 : kKeys % page == 0)
                      ? (page < kKeys ? page : kKeys)
