@@ -1330,7 +1330,8 @@ struct Plan {
     row_tile = mode == 0 ? 64 : mode == 1 ? kRows : 2 * kRows;
     part_rows = (rows < row_tile ? rows : row_tile) + 7 & ~7;
     // As many again: more even out the ends better, but each costs a piece written and
-    // read.  A piece of 256 rows costs more than the dealing gains (388 us against 395).
+    // read (twice as many: batch of trees 88 -> 94 us, long chains 148 -> 158).  A piece of
+    // 256 rows costs more than the dealing gains (64-node trees 373 us without, 393 with).
     dealt = mode == 2 ? 0 : kMaxCtas;
     const size_t runs = kMaxCtas + dealt;
     stats = SPECV_ATTENTION_HEADER_BYTES + align256(runs * sizeof(Cut));
