@@ -105,7 +105,6 @@ typedef enum specv_dtype {
 #define SPECV_MAX_NODES 64      /* nodes of a tree, rows of a request     */
 #define SPECV_MAX_HEAD_DIM 128  /* cache operators: a multiple of 8 in 8..128 */
 #define SPECV_MAX_BIAS 1024     /* biased tokens of a request             */
-#define SPECV_ATTENTION_HEADER_BYTES 256  /* of its workspace, to be zeroed once */
 
 /* Library version (major*10000 + minor*100 + patch). */
 int specv_version(void);
@@ -440,11 +439,9 @@ size_t specv_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, 
  * rounded to the cache's dtype before the product with the values.
  *   q, out    [B, N, q_heads, head_dim]; q_heads a multiple of cache->heads.
  *   scale     > 0 and finite (1/sqrt(head_dim) as a rule).
- *   workspace specv_attention_workspace_bytes bytes, 256-byte aligned, its
- *             first SPECV_ATTENTION_HEADER_BYTES zeroed once with
- *             specv_workspace_init (every call leaves them ready for the
- *             next; after SPECV_DEV_TIMEOUT zero them again).
- *             Calls that may run at the same time need one each.
+ *   workspace specv_attention_workspace_bytes bytes, 256-byte aligned,
+ *             whatever it holds.  Calls that may run at the same time need
+ *             one each.
  * Two kernels, the second as a programmatic dependent launch.
  */
 specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,

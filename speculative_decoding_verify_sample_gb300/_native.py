@@ -31,7 +31,6 @@ DEV_BAD_CACHE = 0x100
 DEV_BAD_PENALTY = 0x200
 
 MAX_NODES = 64
-ATTENTION_HEADER_BYTES = 256
 MAX_HEAD_DIM = 128
 
 # exported function -> (restype, argtypes)

@@ -13,17 +13,15 @@
 // no result shows: m is whatever both O and the sum l were taken with.
 //
 // The work is the list of (request, key head, row tile, 128-key tile), a unit
-// each, cut into runs: one for every CTA (one to an SM), and the rest in short
-// runs that the CTAs take off a counter as they finish, for equal runs do not
-// take equal time (with 80 units each, 121 to 172 us).  A row tile whose keys
-// one run has whole is written out; pieces leave (m, l, O) in the workspace for
-// join_kernel.
+// each, cut into even runs, one for every CTA (one to an SM), whatever the
+// requests' lengths are.  A row tile whose keys one run has whole is written out;
+// pieces leave (m, l, O) in the workspace for join_kernel.
 //
 // Two streams share an SM, each with its S and O in TMEM and its four softmax
 // warps: with up to 128 rows they take the key tiles in turn and are joined
 // at the end, with more they are two row tiles on the same keys
 // (kPair).  Of the other warps four copy, two threads issue the MMAs, one
-// warp deals out the work and one checks the requests' data beside it all.
+// warp lists the run's work and one checks the requests' data beside it all.
 
 #include <cuda.h>
 
@@ -37,17 +35,20 @@ namespace {
 
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kRows = 128;     // query rows of a stream
+static_assert(kKeys == kRows, "tiles of queries, keys and values are laid out alike");
 constexpr int kMaxCtas = 152;  // SMs of a GB300
 constexpr int kLoadWarps = 4;
 constexpr int kLoadWarp = 8;  // the first of them; the last makes the tensor copies
 constexpr int kCheckWarp = 12;
 constexpr int kScoreWarp = 13;  // issues S = Q K^T
 constexpr int kSumWarp = 14;    // issues O += P V
-constexpr int kDealWarp = 15;
+constexpr int kListWarp = 15;
 constexpr int kThreads = 512;
-constexpr int kItems = 4;  // items dealt out ahead
-constexpr int kItemCost = 1;  // what an item takes besides its key tiles, in their time
-constexpr int kNear = 3;   // key tiles before an item's end at which the next run is called for
+constexpr int kItems = 4;  // items listed ahead
+// What an item takes besides its key tiles, in their time: its end, and the next
+// one's first scores (a batch of 32 trees: 90.8, 78.4, 73.5, 70.3, 70.1 us with 0 .. 4;
+// 64-node trees 368.6, 365.6, 365.8, 363.8, 368.7).
+constexpr int kItemCost = 3;
 // Registers a thread of each warpgroup: 2 * 200 + 56 + 56 = 512 = 4 * 128, what
 // the block is launched with.  The softmax keeps a row of scores in them.
 #define SPECV_REGS_SOFTMAX "200"
@@ -57,11 +58,6 @@ constexpr float kRise = 8.0f;  // log2 of how far a maximum may rise before O is
 
 // ---------------------------------------------------------------- the work
 
-struct Header {
-  int32_t next;   // runs dealt out so far; 0 between calls
-  int32_t count;  // of this call's runs
-};
-
 // Where a run begins in the middle of an item: the item's second piece.
 struct Cut {
   int32_t b, h, row_tile, n;
@@ -70,7 +66,6 @@ struct Cut {
 };
 
 struct Workspace {
-  Header* header;
   Cut* cuts;      // [runs]
   float2* stats;  // [2 runs][part_rows] pieces' m c and l: of an item that began before the
                   // run, then of one that goes on behind it
@@ -86,46 +81,27 @@ struct AttnParams {
   const int32_t* n_nodes;
   int32_t* status;
   int B, N, q_heads, group;  // group: query heads to a key head
-  int ctas, dealt;           // runs: one for each CTA, and at most `dealt` more
+  int ctas;                  // and runs
   int part_rows;             // rows of a piece in the workspace
   int box_rows;              // rows that one tensor copy brings; 0: copies of 16 bytes
   float scale_log2;
 };
 
-// How the units are cut into runs.  Few units (under 8 for each CTA) are cut
-// evenly; of more, a share is cut evenly and the rest is dealt out.
+// How the units are cut into runs.  (A share dealt out to CTAs as they finish evens
+// out the ends, but costs pieces written and read: 16 requests of 4,300 keys took
+// 88 us against 69, eight of 24,000 148 against 137.)
 struct Runs {
-  int64_t total;
-  int even, dealt;  // lengths of the two kinds of runs
-  int ctas, count;
+  int64_t total, each;
 
   __device__ __forceinline__ Runs(const AttnParams& P, int64_t units)
-      : total(units), dealt(1), ctas(P.ctas) {
-    if (total >= 8 * ctas && P.dealt > 0) {
-      even = quotient(total, ctas) * 7 / 8;
-      const int64_t rest = total - static_cast<int64_t>(even) * ctas;
-      dealt = quotient(rest + P.dealt - 1, P.dealt);
-      count = ctas + quotient(rest + dealt - 1, dealt);
-    } else {
-      even = quotient(total + ctas - 1, ctas);
-      count = total ? quotient(total + even - 1, even) : 0;
-    }
-  }
-  static __device__ __forceinline__ int quotient(int64_t a, int b) {
-    return a >> 32 ? static_cast<int>(a / b)
-                   : static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+      : total(units), each(quotient(units + P.ctas - 1, P.ctas)) {}
+  static __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
   }
   // Where run `run` begins, and run - 1 ends.
-  __device__ __forceinline__ int64_t start(int run) const {
-    return min(total, run < ctas ? static_cast<int64_t>(run) * even
-                                 : static_cast<int64_t>(ctas) * even +
-                                       static_cast<int64_t>(run - ctas) * dealt);
-  }
-  // Runs that units u .. are in, from `run` on, which has the first.
-  __device__ __forceinline__ int last(int run, int64_t end) const {
-    const int64_t evens = static_cast<int64_t>(ctas) * even;
-    return end <= evens ? quotient(end - 1, even) : max(run, ctas + quotient(end - 1 - evens, dealt));
-  }
+  __device__ __forceinline__ int64_t start(int run) const { return min(total, run * each); }
+  // The run that has unit u.
+  __device__ __forceinline__ int of(int64_t u) const { return static_cast<int>(quotient(u, each)); }
 };
 
 // Nodes of request b, 0 where its count or length is out of range.
@@ -382,16 +358,12 @@ __device__ __forceinline__ float exp2_of(float x) {
 
 // --------------------------------------------------------------- attention
 
-// kMode: 0 at most 64 query rows, 1 at most 128, 2 more (kPair).
-template <int DP, int kMode> struct Shape {
-  static constexpr bool kPair = kMode == 2;
+// kPair: more than 128 query rows, two row tiles on the same keys.
+template <int DP, bool kPair> struct Shape {
   static constexpr int kTileBytes = kKeys * DP * 2;  // of keys or of values
-  // Few queries leave room for a sixth tile.  (The MMA reads 128 rows all the
-  // same: what lies behind makes scores of rows that nobody reads.)
-  static constexpr int kQueryRows = kMode == 0 ? 64 : kRows;
-  static constexpr int kQueryBytes = kQueryRows * DP * 2;
-  static constexpr int kStages = (kMode == 0 ? 6 : 5) * (128 / DP);
-  static constexpr int kRowTile = kPair ? 2 * kRows : kMode == 0 ? 64 : kRows;
+  static constexpr int kQueryBytes = kRows * DP * 2;
+  static constexpr int kStages = 5 * (128 / DP);
+  static constexpr int kRowTile = kPair ? 2 * kRows : kRows;
   // shared memory: queries (two tiles: both row tiles, or this and the next item's), stages,
   // then the barriers and what the warps tell one another
   static constexpr int kStageAt = 2 * kQueryBytes;
@@ -412,7 +384,7 @@ template <int DP, int kMode> struct Shape {
 // All key tiles t0 .. t1-1 of a row tile that one run has.
 struct Item {
   int32_t b, h, row_tile, t0, t1, tiles, len, n;  // t0 < 0: no more items
-  int32_t run, pieces;  // runs that have key tiles of it
+  int32_t pieces;       // runs that have key tiles of it
   int32_t bad;          // written by the checking warp
   uint8_t parents[kMaxNodes];                          // each below its node, whatever the input
 
@@ -429,7 +401,6 @@ template <int kStages> struct Tail {
   uint64_t odd_values[2];  // nodes whose values were not finite, by parity of the item
   unsigned long long total;
   int gave_up;
-  int ending;  // items whose copies are near their end
   uint32_t tmem;
   Item items[kItems];
   float2 stats[2][kRows];
@@ -454,12 +425,11 @@ __device__ __forceinline__ uint32_t seen_of(int first, uint64_t visible) {
   return first < 64 ? static_cast<uint32_t>(visible >> first) : 0u;
 }
 
-template <class E, int DP, int kMode>
+template <class E, int DP, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const AttnParams P, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
-  using S = Shape<DP, kMode>;
-  constexpr bool kPair = S::kPair;
+  using S = Shape<DP, kPair>;
   constexpr int kStages = S::kStages;
   // weights in f16 go below 2^-14, where its steps stop shrinking: taken 2^7 larger
   // they reach 2^15 at most (2^kRise more than the maximum's)
@@ -490,7 +460,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       barrier_init(smem_of(&s.item_checked[i]), 1);
       barrier_init(smem_of(&s.item_empty[i]), kLoadWarps + 3 + 8);
     }
-    s.ending = 0;
     barrier_init(smem_of(&s.drained), 2);
     s.gave_up = 0;
     s.total = 0;
@@ -522,7 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tS[2] = {tmem, tmem + 128};
   const uint32_t tO[2] = {tmem + 256, tmem + 256 + DP};
   volatile int* gave_up = &s.gave_up;
-  volatile int* near_end = &s.ending;
   // The next item of this thread's warp; lane 0 gives it back when it is done.
   uint32_t items = 0;
   auto next_item = [&]() -> const Item& {
@@ -549,9 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 128-byte rows, their 16-byte pieces swapped by the row's number: rows
     // kRowsAtOnce apart, and sub < kRowsAtOnce, so r and sub set bits of their own
     const uint32_t swap = (piece % 8) ^ sub;
-    auto tile_copy = [&](uint32_t to, int tile_rows, const uint16_t* from, int64_t off) {
+    auto tile_copy = [&](uint32_t to, const uint16_t* from, int64_t off) {
       // this lane's row is 32 lw + lane of the tile, at from + off (off < 0: none)
-      const uint32_t lane_at = (piece / 8) * (tile_rows * 128) + (32 * lw + sub) * 128;
+      const uint32_t lane_at = (piece / 8) * (kRows * 128) + (32 * lw + sub) * 128;
 #pragma unroll
       for (int r = 0; r < 32; r += kRowsAtOnce) {
         const int64_t o = __shfl_sync(kFullMask, off, r + sub);
@@ -575,13 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int node = at / P.group, g = at - node * P.group;
         const int64_t off = w.b * P.q.batch_stride + node * P.q.node_stride +
                             (w.h * P.group + g) * P.q.head_stride;
-        if (32 * lw < S::kQueryRows)
-          tile_copy(base + (kPair ? half : q_buffer) * S::kQueryBytes, S::kQueryRows, P.q.data,
-                    real ? off : -1);
+        tile_copy(base + (kPair ? half : q_buffer) * S::kQueryBytes, P.q.data, real ? off : -1);
       }
       copies_arrive(smem_of(&s.q_full[q_buffer]));
       const int keys = w.len + w.n, t1 = w.t1;
-      const int ending = max(w.t0, t1 - kNear);  // the tile whose copy calls for the next run
       const int32_t* table = C.page_table + static_cast<int64_t>(w.b) * C.table_stride;
       // Page numbers are read a tile ahead of their use; one out of range (its
       // request is flagged elsewhere) is no page.
@@ -617,7 +582,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           int page_before = -1;
           for (int t = w.t0; t < t1; t++) {
             const int i = t - w.t0;
-            if (t == ending && lane == 0) *near_end = items + 1;
             copy(S::key_job(i), &k_map, page, t);
             if (kPair) copy(S::value_job(i, t1 - w.t0), &v_map, page, t);
             else if (i > 0) copy(S::value_job(i - 1, t1 - w.t0), &v_map, page_before, t - 1);
@@ -634,13 +598,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto copy = [&](uint32_t job, const uint16_t* from, int64_t off) {
           const uint32_t stage = (jobs + job) % kStages, use = (jobs + job) / kStages;
           barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
-          tile_copy(base + S::kStageAt + stage * S::kTileBytes, kKeys, from, off);
+          tile_copy(base + S::kStageAt + stage * S::kTileBytes, from, off);
           copies_arrive(smem_of(&s.kv_full[stage]));
         };
         int64_t before = -1;
         for (int t = w.t0; t < t1; t++) {
           const int i = t - w.t0;
-          if (t == ending && lane == 0 && lw == kLoadWarps - 1) *near_end = items + 1;
           const int64_t off = page < 0 ? static_cast<int64_t>(-1)
                                        : page * C.page_stride +
                                              key_of(t) % C.page_size * C.row_stride +
@@ -689,9 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_ss<false>(tS[st], a, b, kIdescS);
 #pragma unroll
         for (int k = 1; k < DP / 16; k++) {
-          const uint32_t q_step = ((k / 4) * (S::kQueryRows * 128) + (k % 4) * 32) >> 4;
-          const uint32_t k_step = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
-          if (k < steps) mma_ss<true>(tS[st], a + q_step, b + k_step, kIdescS);
+          const uint32_t step = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;  // of both
+          if (k < steps) mma_ss<true>(tS[st], a + step, b + step, kIdescS);
         }
         mma_commit(smem_of(&s.s_full[st]));
         issued[st]++;
@@ -762,111 +724,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       barrier_wait_own(smem_of(&s.drained), 0);
     }
     __syncwarp();
-    // ------------------------------------------------------------ dealing
-    if (warp == kDealWarp) {
+    // ------------------------------------------------------------ listing
+    if (warp == kListWarp) {
       const Runs runs(P, static_cast<int64_t>(s.total));
-      if (blockIdx.x == 0 && lane == 0) P.ws.header->count = runs.count;
-      int b = 0;         // the request where the search is, ...
+      const int run = blockIdx.x;
+      int b = 0;           // the request where the search is, ...
       int64_t before = 0;  // ... and the units before it
-      bool stop = false;
-      for (int run = blockIdx.x; run < runs.count && !stop;) {
-        int64_t u = runs.start(run);
-        const int64_t end = runs.start(run + 1);
-        bool begins = true;
-        if (lane == 0) P.ws.cuts[run] = Cut{0, 0, 0, 0, 0, {0, 0, 0}};
-        while (u < end && !stop) {
-          // the request with unit u: 32 requests at a time
-          int tiles, row_tiles, len, n;
-          int64_t units;
-          while (true) {
-            units = b + lane < P.B ? units_of<S::kRowTile>(P, b + lane, tiles, row_tiles, len, n) : 0;
-            int64_t upto = units;
+      bool stop = false, begins = true;
+      // every run's, whatever is in it: the join follows what it finds
+      if (lane == 0) P.ws.cuts[run] = Cut{0, 0, 0, 0, 0, {0, 0, 0}};
+      int64_t u = runs.start(run);
+      const int64_t end = runs.start(run + 1);
+      while (u < end && !stop) {
+        // the request with unit u: 32 requests at a time
+        int tiles, row_tiles, len, n;
+        int64_t units;
+        while (true) {
+          units = b + lane < P.B ? units_of<S::kRowTile>(P, b + lane, tiles, row_tiles, len, n) : 0;
+          int64_t upto = units;
 #pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-              const int64_t x = __shfl_up_sync(kFullMask, upto, o);
-              if (lane >= o) upto += x;
-            }
-            const uint32_t past = __ballot_sync(kFullMask, before + upto > u);
-            const int from = past ? __ffs(past) - 1 : 31;
-            if (past) {
-              before += __shfl_sync(kFullMask, upto - units, from);
-              b += from;
-              tiles = __shfl_sync(kFullMask, tiles, from);
-              row_tiles = __shfl_sync(kFullMask, row_tiles, from);
-              len = __shfl_sync(kFullMask, len, from);
-              n = __shfl_sync(kFullMask, n, from);
-              units = __shfl_sync(kFullMask, units, from);
-              break;
-            }
-            before += __shfl_sync(kFullMask, upto, 31);
-            b += 32;
-            if (b >= P.B) {  // the lengths changed meanwhile
-              stop = true;
-              break;
-            }
+          for (int o = 1; o < 32; o *= 2) {
+            const int64_t x = __shfl_up_sync(kFullMask, upto, o);
+            if (lane >= o) upto += x;
           }
+          const uint32_t past = __ballot_sync(kFullMask, before + upto > u);
+          const int from = past ? __ffs(past) - 1 : 31;
+          if (past) {
+            before += __shfl_sync(kFullMask, upto - units, from);
+            b += from;
+            tiles = __shfl_sync(kFullMask, tiles, from);
+            row_tiles = __shfl_sync(kFullMask, row_tiles, from);
+            len = __shfl_sync(kFullMask, len, from);
+            n = __shfl_sync(kFullMask, n, from);
+            units = __shfl_sync(kFullMask, units, from);
+            break;
+          }
+          before += __shfl_sync(kFullMask, upto, 31);
+          b += 32;
+          if (b >= P.B) {  // the lengths changed meanwhile
+            stop = true;
+            break;
+          }
+        }
+        if (stop) break;
+        uint8_t up[2];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+          const int i = lane + 32 * k;
+          int parent = i - 1;
+          if (P.parents && i < n) parent = P.parents[static_cast<int64_t>(b) * P.N + i];
+          up[k] = static_cast<uint8_t>(parent >= 0 && parent < i ? parent : 0);
+        }
+        const int span = tiles + kItemCost;
+        while (u < end && u < before + units) {
+          const int64_t off = u - before;
+          const int64_t of = Runs::quotient(off, span);
+          const int64_t first = u - (off - of * span) + kItemCost;  // of its tiles' units
+          const int h = static_cast<int>(of) / row_tiles;  // below 1024 heads * 512 row tiles
+          const int row_tile = static_cast<int>(of) - h * row_tiles;
+          const int t0 = static_cast<int>(max(u - first, static_cast<int64_t>(0)));
+          const int t1 = static_cast<int>(min(end - first, static_cast<int64_t>(tiles)));
+          u = min(end, first + tiles);
+          if (t1 <= t0) continue;  // the run ends before the item's first tile
+          // runs before and behind with pieces of this item
+          int first_run = run, last_run = run;
+          if (t0 > 0) first_run = runs.of(first);
+          if (t1 < tiles) last_run = runs.of(first + tiles - 1);
+          const uint32_t slot = items % kItems;
+          barrier_wait(smem_of(&s.item_empty[slot]), (items / kItems & 1) ^ 1, gave_up);
+          stop = __any_sync(kFullMask, *gave_up != 0);
           if (stop) break;
-          uint8_t up[2];
-#pragma unroll
-          for (int k = 0; k < 2; k++) {
-            const int i = lane + 32 * k;
-            int parent = i - 1;
-            if (P.parents && i < n) parent = P.parents[static_cast<int64_t>(b) * P.N + i];
-            up[k] = static_cast<uint8_t>(parent >= 0 && parent < i ? parent : 0);
+          Item& to = s.items[slot];
+          to.parents[lane] = up[0];
+          to.parents[lane + 32] = up[1];
+          if (lane == 0) {
+            to.b = b;
+            to.h = h;
+            to.row_tile = row_tile;
+            to.t0 = t0;
+            to.t1 = t1;
+            to.tiles = tiles;
+            to.len = len;
+            to.n = n;
+            to.pieces = last_run - first_run + 1;
+            if (begins && t0 > 0 && first_run == run - 1)
+              P.ws.cuts[run] = Cut{b, h, row_tile, n, last_run - first_run + 1, {0, 0, 0}};
           }
-          const int span = tiles + kItemCost;
-          while (u < end && u < before + units) {
-            const int64_t off = u - before;
-            const int64_t of = off >> 32 ? off / span : static_cast<uint32_t>(off) / span;
-            const int64_t first = u - (off - of * span) + kItemCost;  // of its tiles' units
-            const int h = static_cast<int>(of) / row_tiles;  // below 1024 heads * 512 row tiles
-            const int row_tile = static_cast<int>(of) - h * row_tiles;
-            const int t0 = static_cast<int>(max(u - first, static_cast<int64_t>(0)));
-            const int t1 = static_cast<int>(min(end - first, static_cast<int64_t>(tiles)));
-            u = min(end, first + tiles);
-            if (t1 <= t0) continue;  // the run ends before the item's first tile
-            // runs before and behind with pieces of this item
-            int first_run = run, last_run = run;
-            if (t0 > 0) first_run = runs.last(0, first + 1);
-            if (t1 < tiles) last_run = runs.last(run, first + tiles);
-            const uint32_t slot = items % kItems;
-            barrier_wait(smem_of(&s.item_empty[slot]), (items / kItems & 1) ^ 1, gave_up);
-            stop = __any_sync(kFullMask, *gave_up != 0);
-            if (stop) break;
-            Item& to = s.items[slot];
-            to.parents[lane] = up[0];
-            to.parents[lane + 32] = up[1];
-            if (lane == 0) {
-              to.b = b;
-              to.h = h;
-              to.row_tile = row_tile;
-              to.t0 = t0;
-              to.t1 = t1;
-              to.tiles = tiles;
-              to.len = len;
-              to.n = n;
-              to.run = run;
-              to.pieces = last_run - first_run + 1;
-              if (begins && t0 > 0 && first_run == run - 1)
-                P.ws.cuts[run] = Cut{b, h, row_tile, n, last_run - first_run + 1, {0, 0, 0}};
-            }
-            __syncwarp();
-            if (lane == 0) barrier_arrive(smem_of(&s.item_full[slot]));
-            items++;
-            begins = false;
-          }
+          __syncwarp();
+          if (lane == 0) barrier_arrive(smem_of(&s.item_full[slot]));
+          items++;
+          begins = false;
         }
-        // Not before the copies are near this run's end: a run taken early is one that
-        // an idle CTA does not find.
-        for (const uint64_t since = now_ns(); *near_end < static_cast<int>(items) && !*gave_up;) {
-          __nanosleep(100);
-          if (now_ns() - since > 2000000000ull) *gave_up = 1;
-        }
-        __syncwarp();
-        const int dealt =
-            __shfl_sync(kFullMask, lane == 0 ? atomicAdd(&P.ws.header->next, 1) : 0, 0);
-        if (dealt < 0) break;  // a workspace that was not zeroed
-        run = dealt < INT_MAX - P.ctas ? P.ctas + dealt : INT_MAX;
       }
       {
         const uint32_t slot = items % kItems;
@@ -1101,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid == 0 && *gave_up) atomicOr(P.status + w.b, SPECV_DEV_TIMEOUT);
       barrier_wait(smem_of(&s.item_checked[items % kItems]), items / kItems & 1, gave_up);
       const bool bad = given.bad != 0;
-      const int run = given.run, pieces = given.pieces;
+      const int pieces = given.pieces;
       __syncwarp();
       done_item();
       // kPair: this stream's rows, all columns; else half of the columns of both streams' sum
@@ -1124,7 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mine = row < my_rows;
         uint16_t* out = P.out.data + w.b * P.out.batch_stride + node * P.out.node_stride +
                         (w.h * P.group + g) * P.out.head_stride;
-        const int64_t slot = 2 * run + (w.t0 == 0);
+        const int64_t slot = 2 * static_cast<int>(blockIdx.x) + (w.t0 == 0);
         float4* part = P.ws.parts + slot * (DP / 4) * P.part_rows + first_row + row;
         constexpr int kCols = kPair ? DP : DP / 2;
         const int col0 = kPair ? 0 : st * kCols;
@@ -1222,10 +1170,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
   const int run = 1 + blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = P.ws.cuts[run];
-  const int count = P.ws.header->count;
-  if (blockIdx.x == 0 && threadIdx.x == 0) P.ws.header->next = 0;  // for the next call
   // (A call that gave up may leave records of another: they are not followed out of bounds.)
-  if (run >= count || cut.pieces < 2 || cut.pieces > count - run + 1 || cut.b < 0 || cut.b >= P.B ||
+  if (cut.pieces < 2 || cut.pieces > P.ctas - run + 1 || cut.b < 0 || cut.b >= P.B ||
       cut.h < 0 || cut.h >= P.cache.heads || cut.n < 1 || cut.n > P.N || cut.row_tile < 0 ||
       cut.row_tile * kRowTile >= cut.n * P.group)
     return;
@@ -1320,23 +1266,19 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // The shape of the work that B, N and the heads give, whatever the lengths are.
 struct Plan {
-  int mode, dim, row_tile, part_rows, dealt;
-  size_t stats, parts, total;  // offsets in the workspace; before them the header and the cuts
+  bool pair;
+  int dim, row_tile, part_rows;
+  size_t stats, parts, total;  // offsets in the workspace; before them the cuts
 
   Plan(int N, int group, int head_dim) {
     const int rows = N * group;
-    mode = rows <= 64 ? 0 : rows <= kRows ? 1 : 2;
+    pair = rows > kRows;
     dim = head_dim <= 64 ? 64 : 128;
-    row_tile = mode == 0 ? 64 : mode == 1 ? kRows : 2 * kRows;
+    row_tile = pair ? 2 * kRows : kRows;
     part_rows = (rows < row_tile ? rows : row_tile) + 7 & ~7;
-    // As many again: more even out the ends better, but each costs a piece written and
-    // read (twice as many: batch of trees 88 -> 94 us, long chains 148 -> 158).  A piece of
-    // 256 rows costs more than the dealing gains (64-node trees 373 us without, 393 with).
-    dealt = mode == 2 ? 0 : kMaxCtas;
-    const size_t runs = kMaxCtas + dealt;
-    stats = SPECV_ATTENTION_HEADER_BYTES + align256(runs * sizeof(Cut));
-    parts = stats + align256(2 * runs * part_rows * sizeof(float2));
-    total = parts + align256(2 * runs * part_rows * dim * sizeof(float));
+    stats = align256(kMaxCtas * sizeof(Cut));
+    parts = stats + align256(2 * kMaxCtas * part_rows * sizeof(float2));
+    total = parts + align256(2 * kMaxCtas * part_rows * dim * sizeof(float));
   }
 };
 
@@ -1372,45 +1314,38 @@ bool tensor_map(CUtensorMap* map, const specv_cache* c, void* data, int box_rows
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class E, int DP, int kMode>
+template <class E, int DP, bool kPair>
 cudaError_t run(const AttnParams& P, const CUtensorMap& k_map, const CUtensorMap& v_map,
                 cudaStream_t stream) {
-  using S = Shape<DP, kMode>;
+  using S = Shape<DP, kPair>;
   constexpr int kSmem = S::kTailAt + static_cast<int>(sizeof(Tail<S::kStages>));
   static_assert(kSmem <= 232448, "one CTA's shared memory");
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<E, DP, kMode>,
+  cudaError_t e = cudaFuncSetAttribute(attention_kernel<E, DP, kPair>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  attention_kernel<E, DP, kMode><<<P.ctas, kThreads, kSmem, stream>>>(P, k_map, v_map);
+  attention_kernel<E, DP, kPair><<<P.ctas, kThreads, kSmem, stream>>>(P, k_map, v_map);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // (with one CTA there is no cut: the block resets the header)
-  const int cuts = P.ctas + P.dealt - 1 > 0 ? P.ctas + P.dealt - 1 : 1;
-  cfg.gridDim = dim3(cuts);
-  cfg.blockDim = dim3(kMode > 0 ? 512 : 256);
+  if (P.ctas == 1) return cudaSuccess;  // nothing is cut
+  cfg.gridDim = dim3(P.ctas - 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (kMode > 0) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 16, 16>, P);
+  cfg.blockDim = dim3(P.part_rows <= 32 ? 256 : 512);
   if (P.part_rows <= 16) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8, 2>, P);
   if (P.part_rows <= 32) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8, 4>, P);
-  return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8, 8>, P);
+  return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 16, 16>, P);
 }
 
 template <class E>
 cudaError_t run_any(const AttnParams& P, const Plan& plan, const CUtensorMap& k, const CUtensorMap& v,
                     cudaStream_t stream) {
-  if (plan.dim == 64)
-    return plan.mode == 0   ? run<E, 64, 0>(P, k, v, stream)
-           : plan.mode == 1 ? run<E, 64, 1>(P, k, v, stream)
-                            : run<E, 64, 2>(P, k, v, stream);
-  return plan.mode == 0   ? run<E, 128, 0>(P, k, v, stream)
-         : plan.mode == 1 ? run<E, 128, 1>(P, k, v, stream)
-                          : run<E, 128, 2>(P, k, v, stream);
+  if (plan.dim == 64) return plan.pair ? run<E, 64, true>(P, k, v, stream) : run<E, 64, false>(P, k, v, stream);
+  return plan.pair ? run<E, 128, true>(P, k, v, stream) : run<E, 128, false>(P, k, v, stream);
 }
 
 }  // namespace
@@ -1447,8 +1382,7 @@ specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
     return SPECV_ERR_CUDA;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
   char* base = static_cast<char*>(workspace);
-  const Workspace ws{reinterpret_cast<Header*>(base),
-                     reinterpret_cast<Cut*>(base + SPECV_ATTENTION_HEADER_BYTES),
+  const Workspace ws{reinterpret_cast<Cut*>(base),
                      reinterpret_cast<float2*>(base + plan.stats),
                      reinterpret_cast<float4*>(base + plan.parts)};
   const int page = cache->page_size;
@@ -1459,10 +1393,6 @@ specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
   if (box_rows && (!tensor_map(&k_map, cache, cache->k, box_rows) ||
                    !tensor_map(&v_map, cache, cache->v, box_rows)))
     box_rows = 0;
-  // Where no length can give eight units to a CTA, no run is dealt out.
-  const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * page + kKeys - 1) / kKeys;
-  const int row_tiles = (N * group + plan.row_tile - 1) / plan.row_tile;
-  const bool deals = static_cast<int64_t>(B) * cache->heads * row_tiles * tiles >= 8 * ctas;
   const AttnParams P{to_cache(cache),
                      to_rows(q),
                      to_rows(out),
@@ -1475,7 +1405,6 @@ specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
                      q_heads,
                      group,
                      ctas,
-                     deals ? plan.dealt : 0,
                      plan.part_rows,
                      box_rows,
                      scale * 1.4426950408889634f};

@@ -27,7 +27,6 @@ decltype(&spec_tree_attention) attention_fn;
 decltype(&spec_keep_path) keep_fn;
 decltype(&spec_process_logits) process_fn;
 decltype(&specv_attention_workspace_bytes) workspace_bytes_fn;
-decltype(&specv_workspace_init) workspace_init_fn;
 
 // Other threads of Python run while one allocates or launches.
 struct Released {
@@ -260,11 +259,7 @@ at::Tensor new_workspace(int32_t B, int32_t N, int32_t heads, const CacheOf& c) 
            " q_heads=" + std::to_string(heads) + " kv_heads=" + std::to_string(c.arg.heads) +
            " head_dim=" + std::to_string(c.arg.head_dim));
   const Released released;
-  const at::Tensor t = at::empty({static_cast<int64_t>(bytes)},
-                                 at::TensorOptions().dtype(at::kByte).device(c.dev));
-  TORCH_CHECK(workspace_init_fn(t.data_ptr(), SPECV_ATTENTION_HEADER_BYTES, stream_of(c.dev)) == SPECV_OK,
-              "specv_workspace_init failed");
-  return t;
+  return at::empty({static_cast<int64_t>(bytes)}, at::TensorOptions().dtype(at::kByte).device(c.dev));
 }
 
 PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -373,13 +368,13 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// The addresses of the C ABI's functions: the four operators, then the two on
-// the attention's workspace.
+// The addresses of the C ABI's functions: the four operators, then the size
+// of the attention's workspace.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  count(n, 6);
-  void* at[6];
-  for (int i = 0; i < 6; i++) {
+  count(n, 5);
+  void* at[5];
+  for (int i = 0; i < 5; i++) {
     at[i] = PyLong_AsVoidPtr(a[i]);
     if (!at[i]) throw python_error();
   }
@@ -388,7 +383,6 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   keep_fn = reinterpret_cast<decltype(keep_fn)>(at[2]);
   process_fn = reinterpret_cast<decltype(process_fn)>(at[3]);
   workspace_bytes_fn = reinterpret_cast<decltype(workspace_bytes_fn)>(at[4]);
-  workspace_init_fn = reinterpret_cast<decltype(workspace_init_fn)>(at[5]);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

@@ -19,7 +19,7 @@ import os
 
 import torch
 
-from ._native import ATTENTION_HEADER_BYTES, SpecVerifyError, check, lib
+from ._native import SpecVerifyError, lib
 from .build import binding_path
 
 _binding = None
@@ -39,8 +39,7 @@ def _load():
         loader.exec_module(module)
         module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
             handle.spec_append_nodes, handle.spec_tree_attention, handle.spec_keep_path,
-            handle.spec_process_logits, handle.specv_attention_workspace_bytes,
-            handle.specv_workspace_init)))
+            handle.spec_process_logits, handle.specv_attention_workspace_bytes)))
         _binding = module
     return _binding
 
@@ -94,24 +93,16 @@ def append_nodes(q, k, v, k_cache, v_cache, page_table, cache_lens, inv_freq=Non
 
 
 class AttentionWorkspace:
-    """Device workspace for tree_attention over B requests of up to N nodes, its
-    header zeroed once on creation (every call leaves it ready for the next).  Calls
+    """Device workspace for tree_attention over B requests of up to N nodes.  Calls
     that may run at the same time (on two streams, or two captured graphs that
     may be replayed together) need one each."""
 
-    def __init__(self, B: int, N: int, q_heads: int, kv_heads: int, head_dim: int, device=None,
-                 stream=None):
+    def __init__(self, B: int, N: int, q_heads: int, kv_heads: int, head_dim: int, device=None):
         self.nbytes = int(lib().specv_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim))
         if self.nbytes == 0:
             raise ValueError(f"unsupported attention shape B={B} N={N} q_heads={q_heads} "
                              f"kv_heads={kv_heads} head_dim={head_dim}")
         self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
-        dev = self.tensor.device
-        with torch.cuda.device(dev):
-            check("specv_workspace_init", lib().specv_workspace_init(
-                self.tensor.data_ptr(), ATTENTION_HEADER_BYTES,
-                torch.cuda.current_stream(dev).cuda_stream if stream is None
-                else getattr(stream, "cuda_stream", stream)))
 
 
 def tree_attention(q, k_cache, v_cache, page_table, cache_lens, parents=None, n_nodes=None, *,
