@@ -49,10 +49,10 @@ constexpr int kItems = 4;  // items listed ahead
 // one's first scores (a batch of 32 trees: 90.8, 78.4, 73.5, 70.3, 70.1 us with 0 .. 4;
 // 64-node trees 368.6, 365.6, 365.8, 363.8, 368.7).
 constexpr int kItemCost = 3;
-// Registers a thread of each warpgroup: 2 * 200 + 56 + 56 = 512 = 4 * 128, what
+// Registers a thread of each warpgroup: 2 * 192 + 72 + 56 = 512 = 4 * 128, what
 // the block is launched with.  The softmax keeps a row of scores in them.
-#define SPECV_REGS_SOFTMAX "200"
-#define SPECV_REGS_LOAD "56"
+#define SPECV_REGS_SOFTMAX "192"
+#define SPECV_REGS_LOAD "72"
 #define SPECV_REGS_OTHER "56"
 constexpr float kRise = 8.0f;  // log2 of how far a maximum may rise before O is rescaled
 
