@@ -43,6 +43,12 @@ __device__ __forceinline__ float2 turn(int pos, float freq, uint64_t steps, floa
   return make_float2(cs * scale, sn * scale);
 }
 
+// x <- x / sqrt(mean x^2 + eps) * weight, then the pairs' rotation, in 32 bits.
+// Bytes bound it, each row read and written once: 256 trees of 17 to 32 nodes, 64
+// query and 8 + 8 key and value heads of 128, 57 us (257 MB, 4.5 TB/s; three blocks
+// of 80 registers to an SM keep 96 KB of copies in flight); 32 trees 10 to 12 us and
+// one chain 6 to 8, most of it the chain of loads from a request's length to its slot.
+//
 // A warp has a node and goes through its heads, 32 / kLanes rows at a time.  A
 // lane has two 16-byte pieces of a row, the two that a rotation in halves
 // joins, and their cosines and sines stay in its registers for all heads.
@@ -260,7 +266,9 @@ void run_append(const AppendParams& P, cudaStream_t stream) {
   const int rows_at_once = narrow ? 8 : 4;
   const int passes = (P.q_heads + rows_at_once - 1) / rows_at_once +
                      2 * ((P.cache.heads + rows_at_once - 1) / rows_at_once);
-  // Few nodes: their heads are shared out over several warps, 16 to an SM.
+  // Few nodes: their heads are shared out over several warps, 16 to an SM (48 trees,
+  // 1,536 nodes, 12.4 us with two warps a node and 14.4 with one; 64 trees, 2,048 nodes,
+  // 15.0 and 16.0; for 32 to an SM 32 trees took 13.8 us against 11.6, 64 trees 18.2).
   const int tokens = P.B * P.N;
   const int splits = tokens >= 2432 ? 1 : (2432 + tokens - 1) / tokens;
   const dim3 grid((tokens + kAppendWarps - 1) / kAppendWarps, splits < passes ? splits : passes);
@@ -279,6 +287,11 @@ void run_append(const AppendParams& P, cudaStream_t stream) {
 constexpr int kKeepThreads = 256;
 constexpr int kBatch = 8;  // rows a thread has in flight
 
+// The kept rows' bytes, read and written, bound it: 128 requests, 16 layers, 8 + 8
+// heads of 128, up to 6 rows of each move in 16.4 us (50 MB, 3.1 TB/s), one layer of
+// one request in 5.  (Several layers to a block, so that length and pages are read
+// less often, took 15.9 to 16.5 us; more warps to an SM, of fewer registers, 23 to 30.)
+//
 // One block per request and layer; a thread owns 16 bytes of a row of K or V
 // and moves them for every kept node in order.  A path's nodes increase, so
 // path[j] >= j: no row is a destination before it was read, also between the
