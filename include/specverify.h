@@ -377,11 +377,13 @@ specv_status spec_insert_accepted(const int32_t* accepted_len, const int32_t* ou
  * page_table[b, s / page_size].  Element (layer, page, row, head, d) of k is
  * at k + layer*layer_stride + page*page_stride + row*row_stride +
  * head*head_stride + d; v has the same strides.  Strides count elements, are
- * multiples of 8 and may pass 32 bits; k and v are 16-byte aligned. */
+ * multiples of 8, 0 or more, and may pass 32 bits; k and v are 16-byte
+ * aligned. */
 typedef struct specv_cache {
   void* k;
   void* v;
-  const int32_t* page_table; /* [B, max_pages], rows table_stride apart */
+  const int32_t* page_table; /* [B, max_pages], rows table_stride apart,
+                                max_pages or more */
   const int32_t* lens;       /* [B]: verified tokens, 0 <= lens[b], and
                                 lens[b] + n_nodes[b] <= max_pages*page_size */
   int64_t layer_stride, page_stride, row_stride, head_stride;
@@ -395,7 +397,7 @@ typedef struct specv_cache {
 
 /* Rows [B, N, heads, head_dim] of the cache's dtype: element (b, i, h, d) is
  * at data + b*batch_stride + i*node_stride + h*head_stride + d.  data is
- * 16-byte aligned, strides are multiples of 8 elements. */
+ * 16-byte aligned, strides are multiples of 8 elements, 0 or more. */
 typedef struct specv_rows {
   void* data;
   int64_t batch_stride, node_stride, head_stride;

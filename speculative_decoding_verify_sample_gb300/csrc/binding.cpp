@@ -177,6 +177,9 @@ at::Tensor output(const char* name, PyObject* o, at::IntArrayRef shape, at::Scal
   const at::Tensor* t = given(name, o);
   if (t) {
     need_like(name, *t, shape, dtype, dev);
+    for (int i = 0; i < t->dim(); i++)
+      if (t->size(i) > 1 && t->stride(i) == 0)
+        refuse(std::string(name) + " must have a place for every element");
     return *t;
   }
   const auto options = at::TensorOptions().dtype(dtype).device(dev);

@@ -148,8 +148,8 @@ def test_attention_many_short_requests(sv):
     (BF16, 16, 33, 48, 6, 112, 100, 3000),
 ])
 def test_attention_fills_the_machine(sv, dtype, B, N, Hq, Hkv, D, page, most):
-    """More work than eight tiles for each SM: runs are dealt out, items cut
-    anywhere, trees lie across tiles; the same bits every time."""
+    """More work than eight tiles for each SM: items cut anywhere, trees that lie
+    across tiles; the same bits every time."""
     rng = np.random.default_rng(B)
     lens = rng.integers(0, most, B)
     lens[:4] = [most, 870, 127, 128 * 7 - 1]
@@ -341,6 +341,68 @@ def test_attention_requests_that_share_pages(sv):
     a = Attn(45, 2, 3, 4, 2, 64, 16, [64, 64], BF16)
     a.table[1, :4] = a.table[0, :4]
     a.check(sv)
+
+
+def test_attention_whatever_the_workspace_holds(sv):
+    a = Attn(47, 5, 20, 8, 2, 128, 64, [3000, 10, 777, 2048, 0], BF16)
+    args, ws = a.args(), sv.AttentionWorkspace(5, 20, 8, 2, 128, device="cuda")
+    want, _ = sv.tree_attention(*args)
+    for fill in (0, 0xff, 0x7f, 1):
+        ws.tensor.fill_(fill)
+        got, status = sv.tree_attention(*args, workspace=ws)
+        assert torch.equal(got, want) and status.tolist() == [0] * 5
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_attention_two_calls_at_once(sv, given):
+    """On two streams, from two threads: a workspace each, given or made by the call."""
+    import threading
+
+    cases = [Attn(51, 6, 9, 8, 2, 128, 64, [900, 3000, 4, 77, 1500, 2], BF16),
+             Attn(52, 3, 40, 16, 2, 64, 32, [2500, 1, 4000], F16)]
+    wants = [sv.tree_attention(*a.args())[0] for a in cases]
+    args = [a.args() for a in cases]
+    spaces = [sv.AttentionWorkspace(a.B, a.N, a.q.shape[2], a.k.shape[2], a.D, device="cuda")
+              if given else None for a in cases]
+    torch.cuda.synchronize()
+    outs, failures = [[], []], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(30):
+                outs[i].append(sv.tree_attention(*args[i], workspace=spaces[i], stream=stream)[0])
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failures.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failures
+    for i in range(2):
+        assert len(outs[i]) == 30 and all(torch.equal(o, wants[i]) for o in outs[i])
+
+
+def test_attention_expanded_queries(sv):
+    """Requests that share their queries (stride 0) and pages, with lengths of their own; an
+    expanded page table, and an output without a place for every element, are refused."""
+    a = Attn(53, 1, 4, 8, 2, 64, 32, [200], BF16)
+    lens = i32([200, 131, 0])
+    table, parents = a.table.repeat(3, 1), i32(np.repeat(a.parents, 3, 0))
+    q = a.q.expand(3, -1, -1, -1)
+    got, status = sv.tree_attention(q, a.k, a.v, table, lens, parents)
+    assert status.tolist() == [0, 0, 0]
+    parts = ref.attention(q, a.k, a.v, table, lens.tolist(), np.repeat(a.parents, 3, 0), [4] * 3, 64 ** -0.5)
+    tol = ref.attention_tolerance(parts, 64, 204, BF16)
+    for b in range(3):
+        close(got[b], parts[0][b], tol[b], f"request {b}")
+    with pytest.raises(sv.SpecVerifyError):
+        sv.tree_attention(q, a.k, a.v, a.table.expand(3, -1), lens, parents)
+    with pytest.raises(ValueError, match="place"):
+        sv.tree_attention(q, a.k, a.v, table, lens, parents, out=torch.zeros_like(a.q).expand(3, -1, -1, -1))
 
 
 # --------------------------------------------------------------------- append
@@ -611,6 +673,37 @@ def test_logits(sv, dtype, B, R, V, chain, kw):
     for b in range(B):
         n = int(d["nodes"][b])
         assert torch.equal(same[b, :n], out[b, :n]) and torch.equal(same[b, n:], d["z"][b, n:])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,R,V,chain,kw", [
+    (76, 2, 777, True, dict(L=40, nbias=3, mask=True)),
+    (80, 3, 8192, False, dict(L=100)),
+    (30, 5, 20001, False, dict(L=300, nbias=9, mask=True)),   # rows of every alignment
+    (10, 17, 65536, True, dict(L=3000, nbias=40, mask=True)),
+    (8, 9, 100000, False, dict(L=700, penalties=False, mask=True)),
+])
+def test_logits_many_requests(sv, dtype, B, R, V, chain, kw):
+    """Enough of them that blocks take large parts of the vocabulary."""
+    d = _logits_case(V + B, B, R, V, dtype, chain=chain, **kw)
+    out = torch.full_like(d["z"], 7.0)
+    got, status = _logits_call(sv, d, out=out)
+    assert got is out and status.tolist() == [0] * B
+    _logits_check(d, out)
+    for b in range(B):
+        assert (out[b, int(d["nodes"][b]):] == 7.0).all()
+
+
+def test_logits_expanded_inputs(sv):
+    """Requests that share logits and a text (stride 0), each with penalties of its own."""
+    d = _logits_case(12, 3, 4, 5001, BF16, chain=True, ragged=False)
+    d["z"], d["history"] = d["z"][:1].repeat(3, 1, 1), np.repeat(d["history"][:1], 3, 0)
+    want, _ = _logits_call(sv, d)
+    text = i32(d["history"][:1]).expand(3, -1)
+    got, status = sv.process_logits(
+        d["z"][:1].expand(3, -1, -1), text, i32(d["seq"]), i32(d["prompt"]), tokens=i32(d["tokens"]),
+        repetition=f32(d["rho"]), frequency=f32(d["freq"]), presence=f32(d["pres"]))
+    assert status.tolist() == [0, 0, 0] and torch.equal(got, want)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])

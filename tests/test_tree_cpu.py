@@ -138,6 +138,18 @@ def test_process_refusals(L, over, status):
     assert process(L, **over) == status
 
 
+@pytest.mark.parametrize("over", [dict(b=-64 * 32), dict(n=-64 * 8), dict(h=-64)])
+def test_strides_below_zero_are_refused(L, over):
+    for name in ("q", "k", "v", "out"):
+        assert append(L, **{name: rows(**over)}) == INVALID
+    for name in ("q", "out"):
+        assert attend(L, **{name: rows(**over)}) == INVALID
+    for call in (append, attend, keep):
+        assert call(L, cache(page_stride=-16 * 2 * 64)) == INVALID
+        assert call(L, cache(row_stride=-128)) == INVALID
+        assert call(L, cache(head_stride=-64)) == INVALID
+
+
 def test_attention_workspace_sizes(L):
     size = L.specv_attention_workspace_bytes
     assert size(1, 1, 1, 1, 8) > 0
