@@ -480,8 +480,9 @@ specv_status spec_keep_path(const specv_cache* cache, const int32_t* path_nodes,
  *   z <- -inf  if the token's bit of the mask is 0
  * in 32 bits, rounded once.  A row whose mask allows nothing becomes -inf.
  *   logits, out [B, R, V] of `dtype` (SPECV_F32 or SPECV_BF16), element (b, i, t)
- *             at b*batch_stride + i*row_stride + t; out may be logits itself
- *             (with its strides), else they do not overlap.
+ *             at b*batch_stride + i*row_stride + t (strides 0 or more); out
+ *             may be logits itself (with its strides), else they do not
+ *             overlap.
  *   tokens    parents != NULL: [B, R], node i's token (tokens[b,0] unused);
  *             parents == NULL (a chain): [B, R-1], the drafted tokens of
  *             spec_verify_sample.  NULL only where R = 1.

@@ -16,7 +16,6 @@ constexpr int kMaxNodes = SPECV_MAX_NODES;
 constexpr unsigned kFullMask = 0xffffffffu;
 
 struct Bf16 {
-  using T = __nv_bfloat16;
   static __device__ __forceinline__ float2 unpack(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
@@ -27,7 +26,6 @@ struct Bf16 {
 };
 
 struct F16 {
-  using T = __half;
   static __device__ __forceinline__ float2 unpack(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
   }
@@ -192,7 +190,7 @@ inline specv_status check_cache(const specv_cache* c, int B, int N) {
       c->head_dim > SPECV_MAX_HEAD_DIM || c->head_dim % 8 != 0)
     return SPECV_ERR_UNSUPPORTED;
   if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16) || !aligned_to(c->page_table, 4) ||
-      !aligned_to(c->lens, 4) || c->layer_stride % 8 != 0 ||
+      !aligned_to(c->lens, 4) || !strides_ok(c->layer_stride, 0, 0) ||
       !strides_ok(c->page_stride, c->row_stride, c->head_stride))
     return SPECV_ERR_INVALID_ARG;
   return SPECV_OK;

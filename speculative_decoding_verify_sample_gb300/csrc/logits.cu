@@ -461,6 +461,8 @@ specv_status spec_process_logits(const void* logits, int64_t batch_stride, int64
                          frequency, presence,    bias_tokens, bias_values, allowed, status};
   for (const void* p : words)
     if (!aligned_to(p, 4)) return SPECV_ERR_INVALID_ARG;
+  if (batch_stride < 0 || row_stride < 0 || out_batch_stride < 0 || out_row_stride < 0 || history_stride < 0)
+    return SPECV_ERR_INVALID_ARG;
   if (logits == out && (batch_stride != out_batch_stride || row_stride != out_row_stride))
     return SPECV_ERR_INVALID_ARG;
   if (B > SPECV_MAX_BATCH || R > SPECV_MAX_NODES || V > specv_max_vocab(dtype) ||

@@ -148,6 +148,9 @@ def test_strides_below_zero_are_refused(L, over):
         assert call(L, cache(page_stride=-16 * 2 * 64)) == INVALID
         assert call(L, cache(row_stride=-128)) == INVALID
         assert call(L, cache(head_stride=-64)) == INVALID
+        assert call(L, cache(layer_stride=-8)) == INVALID
+    for name in ("bs", "rs", "obs", "ors", "hs"):
+        assert process(L, **{name: -1000}) == INVALID
 
 
 def test_attention_workspace_sizes(L):
