@@ -1159,9 +1159,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the pieces of the items that runs cut:
 //   m = max m_i, O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i, in order.
-// A block to a cut.  A warp takes eight rows and kJoinPieces pieces at a time, all
-// of their loads in flight, and where rows are few (then pieces are many) the
-// warps share out the pieces.  A lane has one row and every fourth four columns
+// A block to a cut, or to 16 of its rows.  A warp takes eight rows and kJoinPieces
+// pieces at a time, all of their loads in flight; with kShares > 1 the warps share
+// out the pieces.  A lane has one row and every fourth four columns
 // of it.  The code is short on purpose: it runs once, and fetching it was most
 // of the time of an unrolled form.
 constexpr int kJoinRows = 8;
@@ -1186,9 +1186,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
   const int rows = min(kRowTile, cut.n * P.group - cut.row_tile * kRowTile);
   const int flagged = P.status[cut.b];  // its first piece has cleared the rows
   const int row = lane % kJoinRows, quad = lane / kJoinRows;
+  const int first = blockIdx.y * (kRowGroups * kJoinRows);
 #pragma unroll 1
-  for (int row0 = group * kJoinRows; row0 < (kShares > 1 ? kRowGroups * kJoinRows : rows);
-       row0 += kRowGroups * kJoinRows) {
+  for (int row0 = first + group * kJoinRows;
+       kShares > 1 ? first < rows : row0 < rows; row0 += kRowGroups * kJoinRows) {
     // (slots have whole eights of rows)
     const int at = min(row0, P.part_rows - kJoinRows) + row;
     float m = -INFINITY, l = 0.0f;
@@ -1241,7 +1242,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
 #pragma unroll
       for (int j = 0; j < kQuads; j++) s_o[warp][j][lane] = o[j];
       __syncthreads();
-      if (share) return;  // rows are few: there is no other round
+      if (share) return;
 #pragma unroll 1
       for (int w = 1; w < kShares; w++) {
         const float2 ml = s_ml[warp + w * kRowGroups][row];
@@ -1253,7 +1254,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
         add(old, by, &s_o[warp + w * kRowGroups][0][lane], 32);
       }
     }
-    if (row0 + row >= rows || flagged) continue;
+    // (shared pieces: this is the only round, whatever rows there are)
+    if (row0 + row >= rows || flagged) {
+      if (kShares > 1) return;
+      continue;
+    }
     const float inv = 1.0f / l;
     const int flat = cut.row_tile * kRowTile + row0 + row, node = flat / P.group, g = flat - node * P.group;
     uint16_t* out = P.out.data + cut.b * P.out.batch_stride + node * P.out.node_stride +
@@ -1265,6 +1270,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
         *reinterpret_cast<uint2*>(out + d) = make_uint2(E::pack(o[j].x * inv, o[j].y * inv),
                                                         E::pack(o[j].z * inv, o[j].w * inv));
     }
+    if (kShares > 1) return;
   }
 }
 
@@ -1339,13 +1345,18 @@ cudaError_t run(const AttnParams& P, const CUtensorMap& k_map, const CUtensorMap
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   if (P.ctas == 1) return cudaSuccess;  // nothing is cut
-  cfg.gridDim = dim3(P.ctas - 1);
+  // Few rows, or few items (then pieces are many): blocks of 16 rows whose warps share
+  // out the pieces (64 nodes over 30,000 keys of one head 44 us, 205 with the last form;
+  // 24 items 45 us and 48, 64 items 58 and 47, 64-node trees 388 and 359).
+  const int64_t items = static_cast<int64_t>(P.B) * P.cache.heads *
+                        ((P.N * P.group + S::kRowTile - 1) / S::kRowTile);
+  const bool shared = P.part_rows <= 16 || items < 38;
+  cfg.gridDim = dim3(P.ctas - 1, shared ? (P.part_rows + 15) / 16 : 1);
+  cfg.blockDim = dim3(shared || P.part_rows <= 32 ? 256 : 512);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.blockDim = dim3(P.part_rows <= 32 ? 256 : 512);
-  // Few rows: the warps share out the pieces (one token 18.7 us, 25.4 with the last form).
-  if (P.part_rows <= 16) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8, 2>, P);
+  if (shared) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8, 2>, P);
   if (P.part_rows <= 32) return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 8, 4>, P);
   return cudaLaunchKernelEx(&cfg, join_kernel<E, DP, S::kRowTile, 16, 16>, P);
 }

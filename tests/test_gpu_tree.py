@@ -353,6 +353,33 @@ def test_attention_whatever_the_workspace_holds(sv):
         assert torch.equal(got, want) and status.tolist() == [0] * 5
 
 
+@pytest.mark.parametrize("N,Hq,Hkv,lens", [
+    (4, 4, 1, [30000]), (12, 8, 2, [9000]), (64, 4, 1, [20000]), (40, 16, 2, [7000, 12]),
+])
+def test_attention_few_items_of_many_pieces(sv, N, Hq, Hkv, lens):
+    """One or a few items cut over all CTAs; on another stream and in a graph, over a workspace
+    and an output that hold something else before each."""
+    a = Attn(61, len(lens), N, Hq, Hkv, 128, 64, lens, BF16)
+    args, ws = a.args(), sv.AttentionWorkspace(len(lens), N, Hq, Hkv, 128, device="cuda")
+    parts, tol = a.want(many=True)
+    out, side = torch.zeros_like(a.q), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sv.tree_attention(*args, out=out, workspace=ws)
+    first = None
+    for run in (lambda: sv.tree_attention(*args, out=out, workspace=ws),
+                lambda: sv.tree_attention(*args, out=out, workspace=ws, stream=side), g.replay):
+        ws.tensor.fill_(0xff)
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        run()
+        torch.cuda.synchronize()
+        for b in range(len(lens)):
+            close(out[b], parts[0][b], tol[b], f"request {b}")
+        assert first is None or torch.equal(out, first)
+        first = out.clone()
+
+
 @pytest.mark.parametrize("given", [True, False])
 def test_attention_two_calls_at_once(sv, given):
     """On two streams, from two threads: a workspace each, given or made by the call."""
