@@ -574,7 +574,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto page_of = [&](int t) {
             return t < t1 && lane < boxes ? page_at(t * kKeys + at) : -1;
           };
-          const int in_page = C.page_size > kKeys ? C.page_size : kKeys;
           int page = page_of(w.t0), page_next = page_of(w.t0 + 1);
           auto copy = [&](uint32_t job, const CUtensorMap* map, int page, int t) {
             const uint32_t stage = (jobs + job) % kStages, use = (jobs + job) / kStages;
@@ -585,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (page >= 0)
               tensor_copy(base + S::kStageAt + stage * S::kTileBytes + half * (kKeys * 128) + at * 128,
-                          map, half * 64, t * kKeys % in_page, w.h, page, bar);
+                          map, half * 64, (t * kKeys + at) % C.page_size, w.h, page, bar);
           };
           int page_before = -1;
           for (int t = w.t0; t < t1; t++) {
@@ -1297,8 +1296,7 @@ struct Plan {
 };
 
 // The tensor map of a cache: [page, head, row, d], boxes of 64 columns and
-// box_rows rows of a page.  Swizzled groups are eight rows, so pages of a
-// multiple of eight that divide a tile or are divided by it go this way.
+// box_rows rows of a page, a multiple of eight as the swizzled groups are.
 bool tensor_map(CUtensorMap* map, const specv_cache* c, void* data, int box_rows) {
   using Encode = decltype(&cuTensorMapEncodeTiled);
   static const Encode encode = [] {
@@ -1406,10 +1404,12 @@ specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,
                      reinterpret_cast<float2*>(base + plan.stats),
                      reinterpret_cast<float4*>(base + plan.parts)};
   const int page = cache->page_size;
-  // Tensor copies where pages allow (eight chains 137 us, 196 in pieces of 16 bytes).
-  int box_rows = page % 8 == 0 && (page >= kKeys ? page % kKeys == 0 : kKeys % page == 0)
-                     ? (page < kKeys ? page : kKeys)
-                     : 0;
+  // Tensor copies, the largest that fit pages and tiles alike, from 32 rows on, of pairs
+  // of row tiles from 16; smaller ones take longer than pieces of 16 bytes (eight chains:
+  // of 32 rows 135 us and 139 in pieces, of 16 157 and 145, of 8 238 and 150; 64-node
+  // trees: 360 and 404, 388 and 405, 522 and 404).
+  const int fit = page & -page;
+  int box_rows = fit < (plan.pair ? 16 : 32) ? 0 : fit < kKeys ? fit : kKeys;
   CUtensorMap k_map = {}, v_map = {};
   if (box_rows && (!tensor_map(&k_map, cache, cache->k, box_rows) ||
                    !tensor_map(&v_map, cache, cache->v, box_rows)))

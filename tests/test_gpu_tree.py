@@ -125,6 +125,13 @@ def test_attention_cache_layouts(sv, layout, dtype):
     Attn(5, 2, 6, 8, 2, 64, 16, [200, 37], dtype, layout=layout).check(sv)
 
 
+@pytest.mark.parametrize("page", [2, 4, 8, 12, 40, 48, 96, 136, 192, 384, 1000])
+@pytest.mark.parametrize("layout", ["rows", "heads"])
+def test_attention_page_sizes(sv, page, layout):
+    """Pages that tiles are made of, or that end inside one."""
+    Attn(page, 3, 5, 8, 2, 128, page, [700, 127, 2 * page + 1], BF16, layout=layout).check(sv)
+
+
 @pytest.mark.parametrize("lens,N", [([5000], 1), ([4097, 3, 2999], 4), ([2500, 2501], 40)])
 def test_attention_long_contexts(sv, lens, N):
     """Enough keys that a request's are shared out over the machine."""
@@ -142,7 +149,7 @@ def test_attention_many_short_requests(sv):
     (F16, 40, 13, 32, 8, 64, 64, 2000),
     (BF16, 24, 32, 32, 8, 128, 64, 2900),    # at most 128
     (F16, 30, 16, 16, 2, 80, 128, 9000),
-    (BF16, 20, 20, 24, 6, 128, 24, 2900),    # pages that take single copies
+    (BF16, 20, 20, 24, 6, 128, 24, 2900),    # pages that end inside a tile
     (BF16, 16, 64, 32, 4, 128, 256, 4500),   # more: two row tiles on the same keys, two of them
     (F16, 20, 40, 40, 8, 64, 32, 2300),
     (BF16, 16, 33, 48, 6, 112, 100, 3000),
