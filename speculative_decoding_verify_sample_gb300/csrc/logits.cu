@@ -9,8 +9,8 @@
 // Bytes bound it: each row is read and written once (not read where the mask
 // leaves nothing of 16 bytes), and what the text says is laid over the copy.
 // Measured: 512 requests, two rows of 129,280 bf16 and texts of up to 4,001 tokens
-// 98 us (4.2 TB/s of rows; mask and copy alone 64), 32 trees of up to 32 nodes
-// over 128,256 entries 79 us (4.4 TB/s), one chain of five rows 6.6 us.  The rest is
+// 94 us (4.4 TB/s of rows; mask and copy alone 64), 32 trees of up to 32 nodes
+// over 128,256 entries 74 us (4.7 TB/s), one chain of five rows 6.6 us.  The rest is
 // the text, which every chunk's block reads in whole before it can patch.
 
 #include "cache.cuh"
@@ -63,17 +63,17 @@ template <> struct Elt<SPECV_BF16> {
 
 constexpr int kTokens = 512;  // tokens of the text that a warp counts at a time
 constexpr int kFound = 160;   // of them in the chunk: four from each lane may follow 31 that wait
-constexpr int kMaxRows = 8;     // rows of a block (32 nodes: 79 us; four 86, sixteen 84)
+constexpr int kMaxRows = 8;     // rows of a block (32 nodes, 256 threads: 79 us; four 86, sixteen 84)
 
 // What a block needs of one request's text, for its chunk of the vocabulary.
-template <int kChunk> struct Text {
+template <int kChunk, int kWarps> struct Text {
   uint32_t count[kChunk];
   uint64_t path[kMaxNodes];
   float bias[SPECV_MAX_BIAS];       // sums of the biases in this chunk ...
   uint16_t biased[SPECV_MAX_BIAS];  // ... and their entries
   int drafted[kMaxNodes];  // entry of node i's token, -1 where it is another chunk's
   int num_biased, touched, ticket, bad;
-  uint32_t found[8][kFound];  // by warp: tokens of the text that are in this chunk
+  uint32_t found[kWarps][kFound];  // by warp: tokens of the text that are in this chunk
   uint16_t list[8];  // touched entries: at most kChunk, and the text's, drafts' and biases' number
 };
 
@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
   constexpr int kMine = kSegment / 32 / kVec;        // vectors of a segment a lane has
   constexpr int kFlight = kMine < 4 ? kMine : 4;     // ... in flight
   extern __shared__ __align__(16) char smem[];
-  Text<kChunk>& s = *reinterpret_cast<Text<kChunk>*>(smem);
+  using S = Text<kChunk, kThreads / 32>;
+  S& s = *reinterpret_cast<S*>(smem);
 
   const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
   const int c0 = blockIdx.x * kChunk, c1 = min(P.V, c0 + kChunk);
@@ -403,10 +404,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_kernel(const
   }
 }
 
+template <int kChunk, int kThreads> int smem_of(const Params& P) {
+  const int most = P.L + P.R + P.num_bias;
+  return static_cast<int>(sizeof(Text<kChunk, kThreads / 32>)) + 2 * (most < kChunk ? most : kChunk);
+}
+
 template <int DT, int kChunk, int kThreads, Layout kLayout>
 cudaError_t run(const Params& P, int B, cudaStream_t stream) {
-  const int most = P.L + P.R + P.num_bias;
-  const int smem = static_cast<int>(sizeof(Text<kChunk>)) + 2 * (most < kChunk ? most : kChunk);
+  const int smem = smem_of<kChunk, kThreads>(P);
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(logits_kernel<DT, kChunk, kThreads, kLayout>,
@@ -420,13 +425,19 @@ cudaError_t run(const Params& P, int B, cudaStream_t stream) {
 
 template <int DT, Layout kLayout>
 cudaError_t launch(Params& P, int B, cudaStream_t stream) {
-  // Large chunks read the text less often; small ones fill the machine where
-  // requests are few: large ones from half as many as SMs on (two rows of bf16:
-  // 4 requests, 64 chunks, 7.6 us with small and 8.3 with large ones, 6 requests, 96
-  // chunks, 10.3 and 8.3; 32 nodes: 4 requests 20.0 and 19.1, 8 requests 37.3 and 27.8).
   P.rows = P.R < kMaxRows ? P.R : kMaxRows;
-  return static_cast<int64_t>(B) * ((P.V + 8191) / 8192) >= 76 ? run<DT, 8192, 256, kLayout>(P, B, stream)
-                                                                : run<DT, 1024, 256, kLayout>(P, B, stream);
+  // Large chunks read the text less often; small ones fill the machine where
+  // requests are few: from half as many chunks of 8192 as SMs on, those (32 nodes: 4
+  // requests 20.0 us with 1024 and 19.7 with 8192 entries, 8 requests 37.3 and 27.5;
+  // two rows: 4 requests 7.6 and 8.3, 6 requests 10.3 and 6.3).
+  const int64_t chunks = static_cast<int64_t>(B) * ((P.V + 8191) / 8192);
+  if (chunks < 76) return run<DT, 1024, 256, kLayout>(P, B, stream);
+  // With few rows a block's text outweighs them, and chunks of twice the size halve it
+  // (512 requests of two rows 94 us, 132 with 8192; 64 chains of five 41.5 and 43.9; but
+  // 16 requests of five 20.6 and 19.0, 32 nodes 78 and 74), where two blocks fit an SM.
+  if (chunks >= 456 && P.rows < 7 && smem_of<16384, 512>(P) <= 113 * 1024)
+    return run<DT, 16384, 512, kLayout>(P, B, stream);
+  return run<DT, 8192, 512, kLayout>(P, B, stream);
 }
 
 template <int DT> cudaError_t launch(Params& P, int B, Layout layout, cudaStream_t stream) {

@@ -716,6 +716,9 @@ def test_logits(sv, dtype, B, R, V, chain, kw):
     (30, 5, 20001, False, dict(L=300, nbias=9, mask=True)),   # rows of every alignment
     (10, 17, 65536, True, dict(L=3000, nbias=40, mask=True)),
     (8, 9, 100000, False, dict(L=700, penalties=False, mask=True)),
+    (30, 2, 129280, True, dict(L=500, nbias=20, mask=True)),
+    (58, 5, 65001, False, dict(L=600, nbias=7, mask=True)),
+    (460, 1, 5000, True, dict(L=30000)),                      # a text that fills the lists
 ])
 def test_logits_many_requests(sv, dtype, B, R, V, chain, kw):
     """Enough of them that blocks take large parts of the vocabulary."""
