@@ -1050,12 +1050,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");
       tmem_fence_after();
-      const uint64_t fix = *odd & visible;
+      const uint64_t odd_rows = *odd & visible;
       const float2 other = s.stats[st ^ 1][row];
       if (tid == 0) s.odd_values[(item & 1) ^ 1] = 0;
       if (tid == 0 && *gave_up) atomicOr(P.status + w.b, SPECV_DEV_TIMEOUT);
       barrier_wait(smem_of(&s.item_checked[items % kItems]), items / kItems & 1, gave_up);
-      const bool bad = given.bad != 0;
+      const bool bad = __any_sync(kFullMask, given.bad != 0 || *gave_up);  // unchecked is bad
+      // Only a checked request's pages are followed.  (Of a flagged one a box may not have
+      // been copied, and what its place in the ring held before may look like such values.)
+      const uint64_t fix = bad ? 0 : odd_rows;
       const int pieces = given.pieces;
       __syncwarp();
       done_item();

@@ -307,6 +307,37 @@ def test_attention_flags_bad_requests(sv):
     _bad_requests(sv, call, a.table.cpu().numpy())
 
 
+@pytest.mark.parametrize("page,N,Hq", [(32, 4, 4), (64, 4, 4), (128, 4, 4), (16, 64, 8), (32, 64, 8),
+                                       (128, 64, 8)])
+@pytest.mark.parametrize("bad_page", [-1, 10 ** 6, 2 ** 31 - 1])
+def test_attention_flags_bad_pages_of_tensor_copies(sv, page, N, Hq, bad_page):
+    """Pages out of range where tensor copies bring them (with more than 128 rows to a key head
+    from 16 on), at a request's nodes and before them.  Nothing is copied there and nothing may be
+    read, whatever the tiles held before: every place that is not a key's is NaN."""
+    B, Hkv = 6, 2
+    lens = [5 * page + 3, 4 * page - 2, 3 * page, 4 * page - 1, 700, 2 * page + 1]
+    a = Attn(page + N, B, N, Hq, Hkv, 64, page, lens, BF16)
+    q, k, v, _, lens_t, parents, _ = a.args()
+    table = a.table.cpu().numpy()
+
+    def call(pages):
+        out = torch.full(q.shape, 7.0, dtype=BF16, device="cuda")
+        return sv.tree_attention(q, k, v, i32(pages), lens_t, parents, out=out)
+
+    clean, status = call(table)
+    assert status.tolist() == [0] * B
+    (want, *_), tol = a.want()
+    close(clean, want, tol)
+    for at in (0, lens[1] // page, (lens[1] + N - 1) // page):  # the first page, the nodes' first and last
+        pages = table.copy()
+        pages[1, at] = bad_page
+        rows, status = call(pages)
+        assert status.tolist() == [0, sv.DEV_BAD_CACHE] + [0] * (B - 2)
+        assert (rows[1] == 0).all()
+        for b in (0, 2, 3, 4, 5):
+            assert torch.equal(rows[b], clean[b])
+
+
 def test_attention_on_another_stream_and_in_a_graph(sv):
     a = Attn(41, 3, 6, 8, 2, 128, 32, [700, 12, 1500], BF16)
     want, _ = sv.tree_attention(*a.args())
