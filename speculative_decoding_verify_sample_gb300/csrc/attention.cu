@@ -62,6 +62,13 @@ constexpr int kItemCost = 3;
 #define SPECV_REGS_SOFTMAX "192"
 #define SPECV_REGS_LOAD "72"
 #define SPECV_REGS_OTHER "56"
+// How long a wait lasts before it gives up.  (A build with less than a millisecond polls:
+// try_wait itself may last longer.  With 0 it gives up wherever it would wait.)
+#ifndef SPECV_ATTENTION_WAIT_NS
+#define SPECV_ATTENTION_WAIT_NS 2000000000ull
+#endif
+constexpr uint64_t kWaitNs = SPECV_ATTENTION_WAIT_NS;
+constexpr bool kPolls = kWaitNs < 1000000;
 constexpr float kRise = 8.0f;  // log2 of how far a maximum may rise before O is rescaled
 
 // ---------------------------------------------------------------- the work
@@ -167,22 +174,23 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
-// Waits for a phase, two seconds at most: then, and from then on in the whole
-// CTA, nothing waits any more.  The roles run their loops out (every address
-// they form is in bounds whatever the data), and the request is flagged.
-__device__ __forceinline__ void barrier_wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+// Waits for a phase, two seconds at most: then, and from then on in the whole CTA,
+// no wait lasts any more.  False if the phase is not over: who waited for it leaves its
+// loop and arrives nowhere, so that no other takes a copy or an MMA for done that is not.
+__device__ __forceinline__ bool barrier_wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   const uint64_t start = now_ns();
-  while (!barrier_try(bar, parity)) {
-    if (*gave_up) return;
-    if (now_ns() - start > 2000000000ull) {
+  while (!(kPolls ? barrier_test(bar, parity) : barrier_try(bar, parity))) {
+    if (*gave_up) return false;
+    if (now_ns() - start >= kWaitNs) {
       *gave_up = 1;
-      return;
+      return false;
     }
   }
+  return true;
 }
 
-__device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  if (!barrier_try(bar, parity)) barrier_wait_slow(bar, parity, gave_up);
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  return (!kPolls && barrier_try(bar, parity)) || barrier_wait_slow(bar, parity, gave_up);
 }
 
 // Waits for this thread's own work in flight, a second at most, whatever gave up.
@@ -522,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lw = warp - kLoadWarp, piece = lane % kPieces, sub = lane / kPieces;
     const bool inside = piece * 8 < C.head_dim;
     uint32_t jobs = 0;  // before this item
+    uint32_t sent = 0;  // ... and by tensor copies so far
     // 128-byte rows, their 16-byte pieces swapped by the row's number: rows
     // kRowsAtOnce apart, and sub < kRowsAtOnce, so r and sub set bits of their own
     const uint32_t swap = (piece % 8) ^ sub;
@@ -542,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int q_buffer = kPair ? 0 : item & 1;
       const uint32_t q_use = kPair ? item : item / 2;
       const int rows = w.rows(P.group, S::kRowTile);
-      barrier_wait(smem_of(&s.q_empty[q_buffer]), (q_use & 1) ^ 1, gave_up);
+      if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.q_empty[q_buffer]), (q_use & 1) ^ 1, gave_up)))
+        break;
 #pragma unroll
       for (int half = 0; half < (kPair ? 2 : 1); half++) {
         const int row = half * kRows + 32 * lw + lane;
@@ -563,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (key < keys) page = table[key / C.page_size];
         return page < C.pages ? page : -1;
       };
+      bool going = true;  // the same on every lane
       if (P.box_rows) {
         // Tensor copies: lane l < boxes brings box l % per_half of 64-column half
         // l / per_half.  A page's rows behind the last key come along; the
@@ -579,24 +590,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t stage = (jobs + job) % kStages, use = (jobs + job) / kStages;
             const uint32_t bar = smem_of(&s.kv_full[stage]);
             const int count = __popc(__ballot_sync(kFullMask, page >= 0));
-            barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
+            if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up)))
+              return false;
+            sent = jobs + job + 1;
             if (lane == 0) barrier_expect(bar, count * P.box_rows * 128);
             __syncwarp();
             if (page >= 0)
               tensor_copy(base + S::kStageAt + stage * S::kTileBytes + half * (kKeys * 128) + at * 128,
                           map, half * 64, (t * kKeys + at) % C.page_size, w.h, page, bar);
+            return true;
           };
           int page_before = -1;
-          for (int t = w.t0; t < t1; t++) {
+          for (int t = w.t0; t < t1 && going; t++) {
             const int i = t - w.t0;
-            copy(S::key_job(i), &k_map, page, t);
-            if (kPair) copy(S::value_job(i, t1 - w.t0), &v_map, page, t);
-            else if (i > 0) copy(S::value_job(i - 1, t1 - w.t0), &v_map, page_before, t - 1);
+            going = copy(S::key_job(i), &k_map, page, t);
+            if (going && kPair) going = copy(S::value_job(i, t1 - w.t0), &v_map, page, t);
+            else if (going && i > 0) going = copy(S::value_job(i - 1, t1 - w.t0), &v_map, page_before, t - 1);
             page_before = page;
             page = page_next;
             page_next = page_of(t + 2);
           }
-          if (!kPair) copy(S::value_job(t1 - 1 - w.t0, t1 - w.t0), &v_map, page_before, t1 - 1);
+          if (going && !kPair)
+            going = copy(S::value_job(t1 - 1 - w.t0, t1 - w.t0), &v_map, page_before, t1 - 1);
         }
       } else {
         auto key_of = [&](int t) { return t * kKeys + 32 * lw + lane; };
@@ -604,12 +619,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         int page = page_of(w.t0), page_next = page_of(w.t0 + 1);
         auto copy = [&](uint32_t job, const uint16_t* from, int64_t off) {
           const uint32_t stage = (jobs + job) % kStages, use = (jobs + job) / kStages;
-          barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up);
+          if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up)))
+            return false;
           tile_copy(base + S::kStageAt + stage * S::kTileBytes, from, off);
           copies_arrive(smem_of(&s.kv_full[stage]));
+          return true;
         };
         int64_t before = -1;
-        for (int t = w.t0; t < t1; t++) {
+        for (int t = w.t0; t < t1 && going; t++) {
           const int i = t - w.t0;
           const int64_t off = page < 0 ? static_cast<int64_t>(-1)
                                        : page * C.page_stride +
@@ -617,22 +634,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              w.h * C.head_stride;
           page = page_next;
           page_next = page_of(t + 2);
-          copy(S::key_job(i), C.k, off);
-          if (kPair) copy(S::value_job(i, t1 - w.t0), C.v, off);
-          else if (i > 0) copy(S::value_job(i - 1, t1 - w.t0), C.v, before);
+          going = copy(S::key_job(i), C.k, off);
+          if (going && kPair) going = copy(S::value_job(i, t1 - w.t0), C.v, off);
+          else if (going && i > 0) going = copy(S::value_job(i - 1, t1 - w.t0), C.v, before);
           before = off;
         }
-        if (!kPair) copy(S::value_job(t1 - 1 - w.t0, t1 - w.t0), C.v, before);
+        if (going && !kPair) going = copy(S::value_job(t1 - 1 - w.t0, t1 - w.t0), C.v, before);
       }
+      if (!going) break;
       jobs += 2 * (t1 - w.t0);
       __syncwarp();
       done_item();
     }
-    // Copies still in flight must find this CTA's shared memory.
+    // Copies still in flight, and the arrivals that follow them, must find this CTA's
+    // shared memory.  (Where all went well, who reads them waits for them.)
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (P.box_rows && *gave_up)
-      for (uint32_t k = jobs < kStages ? 0 : jobs - kStages; k < jobs; k++)
-        barrier_wait_own(smem_of(&s.kv_full[k % kStages]), k / kStages & 1);
+    for (uint32_t k = sent < kStages ? 0 : sent - kStages; k < sent; k++)
+      barrier_wait_own(smem_of(&s.kv_full[k % kStages]), k / kStages & 1);
+    if (*gave_up) {
+      const uint64_t start = now_ns();
+      while (now_ns() - start < 100000) {
+      }
+    }
   } else if (warp >= kCheckWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_REGS_OTHER ";");
     // --------------------------------------------------------------- MMAs
@@ -644,16 +667,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // when its stream's last sum has left S, sums when the weights are there.
     auto stage_at = [&](uint32_t job) { return base + S::kStageAt + job % kStages * S::kTileBytes; };
     auto kv_wait = [&](uint32_t job) {
-      barrier_wait(smem_of(&s.kv_full[job % kStages]), job / kStages & 1, gave_up);
+      const bool there = barrier_wait(smem_of(&s.kv_full[job % kStages]), job / kStages & 1, gave_up);
       // copies of 16 bytes wrote through the generic proxy, the MMA reads through the other
       if (!P.box_rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      return there;
     };
     uint32_t jobs = 0;            // copies before this item
     uint32_t issued[2] = {0, 0};  // scores or sums of each stream so far
     if (warp == kScoreWarp && lane == 0) {
       const int steps = (C.head_dim + 15) / 16;
       auto scores = [&](int st, uint32_t q_at, uint32_t k_at) {
-        if (issued[st]) barrier_wait(smem_of(&s.o_full[st]), (issued[st] - 1) & 1, gave_up);
+        if (issued[st] && !barrier_wait(smem_of(&s.o_full[st]), (issued[st] - 1) & 1, gave_up)) return false;
         tmem_fence_after();
         const uint32_t a = operand_low(q_at, 16), b = operand_low(k_at, 16);
         mma_ss<false>(tS[st], a, b, kIdescS);
@@ -664,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mma_commit(smem_of(&s.s_full[st]));
         issued[st]++;
+        return true;
       };
       while (true) {
         const uint32_t item = items;
@@ -674,19 +699,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool second = kPair && w.rows(P.group, S::kRowTile) > kRows;
         const int tiles = w.t1 - w.t0;
         done_item();
-        barrier_wait(smem_of(&s.q_full[q_buffer]), q_use & 1, gave_up);
+        bool going = barrier_wait(smem_of(&s.q_full[q_buffer]), q_use & 1, gave_up);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (int i = 0; i < tiles; i++) {
+        for (int i = 0; i < tiles && going; i++) {
           const uint32_t job = jobs + S::key_job(i);
-          kv_wait(job);
+          going = kv_wait(job);
           if (kPair) {
-            scores(0, base, stage_at(job));
-            if (second) scores(1, base + S::kQueryBytes, stage_at(job));
+            going = going && scores(0, base, stage_at(job));
+            if (second) going = going && scores(1, base + S::kQueryBytes, stage_at(job));
           } else {
-            scores(i & 1, base + q_buffer * S::kQueryBytes, stage_at(job));
+            going = going && scores(i & 1, base + q_buffer * S::kQueryBytes, stage_at(job));
           }
-          mma_commit(smem_of(&s.kv_empty[job % kStages]));
+          if (going) mma_commit(smem_of(&s.kv_empty[job % kStages]));
         }
+        if (!going) break;
         jobs += 2 * tiles;
         mma_commit(smem_of(&s.q_empty[q_buffer]));
       }
@@ -699,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b = operand_low(v_at, kKeys * 128);
 #pragma unroll
         for (int half = 0; half < 2; half++) {
-          barrier_wait(smem_of(&s.p_full[st][half]), issued[st] & 1, gave_up);
+          if (!barrier_wait(smem_of(&s.p_full[st][half]), issued[st] & 1, gave_up)) return false;
           tmem_fence_after();
 #pragma unroll
           for (int k = half * kKeys / 32; k < (half + 1) * kKeys / 32; k++)
@@ -707,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mma_commit(smem_of(&s.o_full[st]));
         issued[st]++;
+        return true;
       };
       while (true) {
         const Item& w = next_item();
@@ -714,17 +741,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool second = kPair && w.rows(P.group, S::kRowTile) > kRows;
         const int tiles = w.t1 - w.t0;
         done_item();
-        for (int i = 0; i < tiles; i++) {
+        bool going = true;
+        for (int i = 0; i < tiles && going; i++) {
           const uint32_t job = jobs + S::value_job(i, tiles);
-          kv_wait(job);
+          going = kv_wait(job);
           if (kPair) {
-            sums(0, stage_at(job), i == 0);
-            if (second) sums(1, stage_at(job), i == 0);
+            going = going && sums(0, stage_at(job), i == 0);
+            if (second) going = going && sums(1, stage_at(job), i == 0);
           } else {
-            sums(i & 1, stage_at(job), i < 2);
+            going = going && sums(i & 1, stage_at(job), i < 2);
           }
-          mma_commit(smem_of(&s.kv_empty[job % kStages]));
+          if (going) mma_commit(smem_of(&s.kv_empty[job % kStages]));
         }
+        if (!going) break;
         jobs += 2 * tiles;
       }
       mma_commit(smem_of(&s.drained));
@@ -921,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           taken[(t - w.t0) & 1]++;
           if (((t - w.t0) & 1) != st) continue;
         }
-        barrier_wait(smem_of(&s.s_full[st]), scored & 1, gave_up);
+        if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.s_full[st]), scored & 1, gave_up))) break;
         const bool mixed = (t + 1) * kKeys > w.len;  // holds keys that not every row sees
         if (mixed && (!kPair || st == 0)) {
           // (Only now that the scores are there: a wait tells phases apart by their parity,
@@ -929,7 +958,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // A value that is not finite would pass through a weight of 0 into rows that do
           // not see its node: it becomes 0 here and comes back, at the end, for those that do.
           const uint32_t job = jobs + S::value_job(t - w.t0, w.t1 - w.t0), stage = job % kStages;
-          barrier_wait(smem_of(&s.kv_full[stage]), job / kStages & 1, gave_up);
+          if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.kv_full[stage]), job / kStages & 1, gave_up)))
+            break;
           char* v = smem + S::kStageAt + stage * S::kTileBytes;
           const int from = max(w.len - t * kKeys, 0), to = min(keys - t * kKeys, kKeys);
           // (and a tensor copy's rows behind the last key hold whatever the page has)
@@ -993,8 +1023,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!first && __any_sync(kFullMask, rise)) {
             // the last update of O must be done
-            barrier_wait(smem_of(&s.o_full[st]), (scored - 1) & 1, gave_up);
-            __syncwarp();
+            if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.o_full[st]), (scored - 1) & 1, gave_up)))
+              break;
             tmem_fence_after();
             l *= by;
 #pragma unroll 1

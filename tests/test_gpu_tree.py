@@ -338,6 +338,74 @@ def test_attention_flags_bad_pages_of_tensor_copies(sv, page, N, Hq, bad_page):
             assert torch.equal(rows[b], clean[b])
 
 
+WAITS = (0, 2000, 6000, 12000, 25000)  # ns
+
+
+@pytest.fixture(scope="module")
+def impatient(sv, tmp_path_factory):
+    """The attention with waits so short that they run out, by their length: functions like
+    tree_attention of a case and an output, that return the status."""
+    import ctypes
+    import importlib
+    import struct
+    import subprocess
+
+    from speculative_decoding_verify_sample_gb300 import _native
+
+    how = importlib.import_module("speculative_decoding_verify_sample_gb300.build")
+    where = tmp_path_factory.mktemp("impatient")
+    source = next(x for x in how.SOURCES if x.endswith("attention.cu"))
+    builds = [subprocess.Popen([how.nvcc_path(), *how.ARCH_FLAGS, "-O3", "-std=c++17", "-I", how.INCLUDE,
+                                "-shared", "-Xcompiler", "-fPIC", "-cudart", "shared",
+                                f"-DSPECV_ATTENTION_WAIT_NS={ns}ull", "-o", str(where / f"{ns}.so"), source])
+              for ns in WAITS]
+    assert [b.wait() for b in builds] == [0] * len(WAITS)
+
+    def bind(ns):
+        fn = ctypes.CDLL(str(where / f"{ns}.so")).spec_tree_attention
+        fn.restype, fn.argtypes = _native.SIGNATURES["spec_tree_attention"]
+
+        def call(a, args, out, ws):
+            q, k, v, table, lens, parents, nodes = args
+            status = i32([-1] * a.B)  # whatever was there
+            cache = struct.pack("@4P4q8i", k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), 0,
+                                *k.stride()[:3], 1, k.shape[0], k.shape[1], table.shape[1], table.stride(0),
+                                k.shape[2], a.D, 1 if a.dtype == BF16 else 2)
+            rows = [struct.pack("@P3q", t.data_ptr(), *t.stride()[:3]) for t in (q, out)]
+            ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+            assert fn(cache, rows[0], ptr(parents), ptr(nodes), a.B, a.N, a.Hq, a.D ** -0.5, rows[1],
+                      status.data_ptr(), ws.tensor.data_ptr(), ws.nbytes,
+                      torch.cuda.current_stream().cuda_stream) == 0
+            torch.cuda.synchronize()
+            return status.tolist()
+
+        return call
+
+    return {ns: bind(ns) for ns in WAITS}
+
+
+GIVE_UP = [  # B, N, Hq, Hkv, D, page, lens
+    (3, 5, 8, 2, 128, 64, [3000, 12, 700]),           # tensor copies
+    (3, 5, 8, 2, 128, 8, [3000, 12, 700]),            # copies of 16 bytes
+    (2, 64, 16, 2, 128, 64, [2000, 900]),             # two row tiles
+    (2, 64, 16, 2, 64, 12, [2000, 900]),
+    (40, 3, 8, 2, 64, 32, [100 * (i % 7) for i in range(40)]),  # many items to a run
+]
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,page,lens", GIVE_UP)
+def test_attention_gives_up_and_leaves_the_device_usable(sv, impatient, B, N, Hq, Hkv, D, page, lens):
+    """Wherever its waits run out the call ends, and those behind it are right."""
+    a = Attn(71, B, N, Hq, Hkv, D, page, lens, BF16)
+    args, ws = a.args(), sv.AttentionWorkspace(B, N, Hq, Hkv, D, device="cuda")
+    want, _ = sv.tree_attention(*args)
+    for ns in WAITS:
+        for _ in range(3):
+            impatient[ns](a, args, torch.zeros_like(a.q), ws)
+            got, status = sv.tree_attention(*args, workspace=ws)
+            assert torch.equal(got, want) and status.tolist() == [0] * B
+
+
 def test_attention_on_another_stream_and_in_a_graph(sv):
     a = Attn(41, 3, 6, 8, 2, 128, 32, [700, 12, 1500], BF16)
     want, _ = sv.tree_attention(*a.args())
