@@ -444,6 +444,8 @@ size_t specv_attention_workspace_bytes(int B, int N, int q_heads, int kv_heads, 
  *   workspace specv_attention_workspace_bytes bytes, 256-byte aligned,
  *             whatever it holds.  Calls that may run at the same time need
  *             one each.
+ * A wait inside the kernel that lasts two seconds gives up: then every request
+ * of the call has SPECV_DEV_TIMEOUT in its status, and the rows hold anything.
  * Two kernels, the second as a programmatic dependent launch.
  */
 specv_status spec_tree_attention(const specv_cache* cache, const specv_rows* q,

@@ -73,11 +73,13 @@ constexpr float kRise = 8.0f;  // log2 of how far a maximum may rise before O is
 
 // ---------------------------------------------------------------- the work
 
-// Where a run begins in the middle of an item: the item's second piece.
+// Where a run begins in the middle of an item: the item's second piece.  And
+// whether one of the run's waits gave up, so that it may have left items undone.
 struct Cut {
   int32_t b, h, row_tile, n;
   int32_t pieces;  // of the item; 0: the run does not begin with an item's second piece
-  int32_t pad[3];
+  int32_t gave_up;
+  int32_t pad[2];
 };
 
 struct Workspace {
@@ -768,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t before = 0;  // ... and the units before it
       bool stop = false, begins = true;
       // every run's, whatever is in it: the join follows what it finds
-      if (lane == 0) P.ws.cuts[run] = Cut{0, 0, 0, 0, 0, {0, 0, 0}};
+      if (lane == 0) P.ws.cuts[run] = Cut{0, 0, 0, 0, 0, 0, {0, 0}};
       int64_t u = runs.start(run);
       const int64_t end = runs.start(run + 1);
       while (u < end && !stop) {
@@ -844,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             to.n = n;
             to.pieces = last_run - first_run + 1;
             if (begins && t0 > 0 && first_run == run - 1)
-              P.ws.cuts[run] = Cut{b, h, row_tile, n, last_run - first_run + 1, {0, 0, 0}};
+              P.ws.cuts[run] = Cut{b, h, row_tile, n, last_run - first_run + 1, 0, {0, 0}};
           }
           __syncwarp();
           if (lane == 0) barrier_arrive(smem_of(&s.item_full[slot]));
@@ -900,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item& w = s.items[slot];
         barrier_wait(smem_of(&s.item_full[slot]), items / kItems & 1, gave_up);
         if (__any_sync(kFullMask, over(w))) {
-          while (next < P.B && !__any_sync(kFullMask, *gave_up != 0)) report();
+          while (next < P.B) report();
           break;
         }
         if (w.b != last) last_bad = static_cast<int>(check(w.b, n));
@@ -1083,7 +1085,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t odd_rows = *odd & visible;
       const float2 other = s.stats[st ^ 1][row];
       if (tid == 0) s.odd_values[(item & 1) ^ 1] = 0;
-      if (tid == 0 && *gave_up) atomicOr(P.status + w.b, SPECV_DEV_TIMEOUT);
       barrier_wait(smem_of(&s.item_checked[items % kItems]), items / kItems & 1, gave_up);
       const bool bad = __any_sync(kFullMask, given.bad != 0 || *gave_up);  // unchecked is bad
       // Only a checked request's pages are followed.  (Of a flagged one a box may not have
@@ -1181,6 +1182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tmem_fence_before();
   __syncthreads();
+  if (tid == 0 && s.gave_up) P.ws.cuts[blockIdx.x].gave_up = 1;
   if (warp == kScoreWarp) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -1191,7 +1193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the pieces of the items that runs cut:
 //   m = max m_i, O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i, in order.
-// A block to a cut, or to 16 of its rows.  A warp takes eight rows and kJoinPieces
+// A block to a run's cut, or to 16 of its rows; that of a run that gave up flags the
+// whole call (whose statuses are all written by now).  A warp takes eight rows and kJoinPieces
 // pieces at a time, all of their loads in flight; with kShares > 1 the warps share
 // out the pieces.  A lane has one row and every fourth four columns
 // of it.  The code is short on purpose: it runs once, and fetching it was most
@@ -1207,9 +1210,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
   __shared__ float2 s_ml[kJoinWarps][kJoinRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int group = warp % kRowGroups, share = warp / kRowGroups;
-  const int run = 1 + blockIdx.x;
+  const int run = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Cut cut = P.ws.cuts[run];
+  if (cut.gave_up && blockIdx.y == 0)
+    for (int b = threadIdx.x; b < P.B; b += kJoinWarps * 32) atomicOr(P.status + b, SPECV_DEV_TIMEOUT);
   // (A call that gave up may leave records of another: they are not followed out of bounds.)
   if (cut.pieces < 2 || cut.pieces > P.ctas - run + 1 || cut.b < 0 || cut.b >= P.B ||
       cut.h < 0 || cut.h >= P.cache.heads || cut.n < 1 || cut.n > P.N || cut.row_tile < 0 ||
@@ -1375,14 +1380,13 @@ cudaError_t run(const AttnParams& P, const CUtensorMap& k_map, const CUtensorMap
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  if (P.ctas == 1) return cudaSuccess;  // nothing is cut
   // Few rows, or few items (then pieces are many): blocks of 16 rows whose warps share
   // out the pieces (64 nodes over 30,000 keys of one head 44 us, 205 with the last form;
   // 24 items 45 us and 48, 64 items 58 and 47, 64-node trees 388 and 359).
   const int64_t items = static_cast<int64_t>(P.B) * P.cache.heads *
                         ((P.N * P.group + S::kRowTile - 1) / S::kRowTile);
   const bool shared = P.part_rows <= 16 || items < 38;
-  cfg.gridDim = dim3(P.ctas - 1, shared ? (P.part_rows + 15) / 16 : 1);
+  cfg.gridDim = dim3(P.ctas, shared ? (P.part_rows + 15) / 16 : 1);
   cfg.blockDim = dim3(shared || P.part_rows <= 32 ? 256 : 512);
   cfg.stream = stream;
   cfg.attrs = attr;

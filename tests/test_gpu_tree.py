@@ -406,6 +406,26 @@ def test_attention_gives_up_and_leaves_the_device_usable(sv, impatient, B, N, Hq
             assert torch.equal(got, want) and status.tolist() == [0] * B
 
 
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,page,lens", GIVE_UP)
+def test_attention_that_gives_up_flags_the_call(sv, impatient, B, N, Hq, Hkv, D, page, lens):
+    """Every status is written.  If a wait ran out anywhere, all of them say so, beside what is
+    wrong with a request itself; if none did, the rows are right."""
+    a = Attn(73, B, N, Hq, Hkv, D, page, lens, BF16)
+    args, ws = list(a.args()), sv.AttentionWorkspace(B, N, Hq, Hkv, D, device="cuda")
+    args[4] = i32([-1] + lens[1:])
+    own = [sv.DEV_BAD_CACHE] + [0] * (B - 1)
+    want, status = sv.tree_attention(*args)
+    assert status.tolist() == own
+    for ns in WAITS:
+        for _ in range(5):
+            out = torch.full_like(a.q, 7.0)
+            status = impatient[ns](a, args, out, ws)
+            if ns == 0 or status != own:
+                assert status == [x | sv.DEV_TIMEOUT for x in own], ns
+            else:
+                assert torch.equal(out, want), ns
+
+
 def test_attention_on_another_stream_and_in_a_graph(sv):
     a = Attn(41, 3, 6, 8, 2, 128, 32, [700, 12, 1500], BF16)
     want, _ = sv.tree_attention(*a.args())
