@@ -412,10 +412,13 @@ template <int kChunk, int kThreads> int smem_of(const Params& P) {
 template <int DT, int kChunk, int kThreads, Layout kLayout>
 cudaError_t run(const Params& P, int B, cudaStream_t stream) {
   const int smem = smem_of<kChunk, kThreads>(P);
-  if (smem > 48 * 1024) {
+  // The most that any call takes, not this one's: the limit is the function's, and another
+  // thread may launch it between these two calls.
+  constexpr int kMost = static_cast<int>(sizeof(Text<kChunk, kThreads / 32>)) + 2 * kChunk;
+  if (kMost > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(logits_kernel<DT, kChunk, kThreads, kLayout>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   const dim3 grid((P.V + kChunk - 1) / kChunk, B, (P.R + P.rows - 1) / P.rows);

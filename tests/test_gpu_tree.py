@@ -975,6 +975,41 @@ def test_logits_on_another_stream_and_in_a_graph(sv):
     assert torch.equal(out, want) and status.tolist() == [0, 0, 0]
 
 
+def test_logits_two_calls_at_once(sv):
+    """On two streams, from two threads, with texts whose lists take very different shared memory."""
+    import threading
+
+    cases = [_logits_case(81, 10, 2, 65536, BF16, chain=True, L=4, ragged=False),
+             _logits_case(82, 10, 2, 65536, BF16, chain=True, L=9000, ragged=False)]
+    wants, calls, failures = [], [], []
+    for d in cases:
+        want, _ = _logits_call(sv, d)
+        wants.append(want)
+        args = [d["z"], i32(d["history"]), i32(d["seq"]), i32(d["prompt"])]
+        kw = dict(tokens=i32(d["tokens"]), repetition=f32(d["rho"]), frequency=f32(d["freq"]),
+                  presence=f32(d["pres"]), out=torch.zeros_like(want), status=i32([9] * 10),
+                  stream=torch.cuda.Stream())
+        calls.append((args, kw))
+    torch.cuda.synchronize()
+
+    def work(args, kw):
+        try:
+            for _ in range(3000):
+                sv.process_logits(*args, **kw)
+            kw["stream"].synchronize()
+        except Exception as e:  # noqa: BLE001
+            failures.append(e)
+
+    threads = [threading.Thread(target=work, args=c) for c in calls]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failures
+    for (_, kw), want in zip(calls, wants):
+        assert torch.equal(kw["out"], want) and kw["status"].tolist() == [0] * 10
+
+
 # ------------------------------------------------------------------- together
 
 

@@ -4,6 +4,7 @@ before they touch the device, and the plain forms the GPU tests compare with."""
 import os
 import struct
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -151,6 +152,46 @@ def test_strides_below_zero_are_refused(L, over):
         assert call(L, cache(layer_stride=-8)) == INVALID
     for name in ("bs", "rs", "obs", "ors", "hs"):
         assert process(L, **{name: -1000}) == INVALID
+
+
+FAKE_ATTRIBUTE = r"""
+#include <stdio.h>
+int cudaFuncSetAttribute(const void* f, int attribute, int value) {
+  fprintf(stderr, "limit %p %d %d\n", f, attribute, value);
+  return 1;  // refused: the call ends here, before any launch
+}
+"""
+
+CALLS = """
+import sys
+sys.path[:0] = {paths!r}
+import speculative_decoding_verify_sample_gb300 as sv, test_tree_cpu as t
+L = sv.lib()
+for dtype in (0, 1):
+    for B, R, V in ((10, 2, 65536), (60, 4, 65536), (8, 33, 100000)):
+        for length, biases in ((1, 0), (300, 7), (9000, 1024)):
+            assert t.process(L, dtype=dtype, B=B, R=R, V=V, len=length, hs=length, nb=biases,
+                             bs=R * V, obs=R * V, rs=V, ors=V) == 4  # SPECV_ERR_CUDA
+"""
+
+
+def test_logits_shared_memory_limit_is_the_same_for_every_call(L, tmp_path):
+    """The limit belongs to the kernel, not to a call: if calls set limits of their own, one in
+    another thread could lower it between this call's setting and its launch."""
+    fake, lib = tmp_path / "fake.c", str(tmp_path / "fake.so")
+    fake.write_text(FAKE_ATTRIBUTE)
+    subprocess.run(["gcc", "-shared", "-fPIC", str(fake), "-o", lib], check=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    run = subprocess.run([sys.executable, "-c", CALLS.format(paths=[here, os.path.dirname(here)])],
+                         env=dict(os.environ, LD_PRELOAD=lib), capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr
+    limits = {}
+    for line in run.stderr.splitlines():
+        if line.startswith("limit "):
+            _, kernel, attribute, value = line.split()
+            limits.setdefault((kernel, attribute), []).append(int(value))
+    assert len(limits) == 4 and all(len(v) >= 3 for v in limits.values())  # two sizes, two types
+    assert all(len(set(v)) == 1 for v in limits.values()), limits
 
 
 def test_attention_workspace_sizes(L):
