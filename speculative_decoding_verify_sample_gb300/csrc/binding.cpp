@@ -161,7 +161,8 @@ CacheOf cache_of(PyObject* k_cache, PyObject* v_cache, PyObject* page_table, PyO
   return CacheOf{c, k.scalar_type(), dev, B};
 }
 
-// Whether the call is made on the current device.
+// (Sizes are narrowed before this: behind it, where Python's lock is given up, nothing may
+// raise.)  Whether the call is made on the current device.
 bool here(const at::Device& dev) {
   if (!dev.is_cuda())
     refuse("the operators on a drafted tree take CUDA tensors, got " + dev.str());
@@ -193,6 +194,7 @@ at::Tensor per_request(const char* name, PyObject* o, int64_t B, const at::Devic
   return t;
 }
 
+// The call, with Python's lock given up: it may not raise.
 template <class Call>
 PyObject* answer(Call call, const at::Tensor& first, const at::Tensor& second) {
   const specv_status status = [&] {
@@ -241,13 +243,15 @@ PyObject* append_nodes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float eps = number("eps", a[12]), scale = number("rope_scale", a[14]);
   const int interleaved = PyObject_IsTrue(a[13]);
   if (interleaved < 0) throw python_error();
+  const int32_t requests = small("B", B), most = small("N", N), q_heads = small("q_heads", heads);
+  const int32_t rot_dim = small("inv_freq", 2 * half);
   if (!here(c.dev)) Py_RETURN_NONE;
   const at::Tensor out = output("q_out", a[15], q.sizes(), c.dtype, c.dev, nodes != nullptr);
   const specv_rows out_rows = rows_of("q_out", out, q.sizes(), c.dtype, c.dev);
   const at::Tensor status = per_request("status", a[16], B, c.dev);
-  return answer([&] { return append_fn(&c.arg, &q_rows, &k_rows, &v_rows, parents, nodes, small("B", B),
-                          small("N", N), small("q_heads", heads), q_weight, k_weight, eps,
-                          half ? inv_freq : nullptr, small("inv_freq", 2 * half), interleaved, scale,
+  return answer([&] { return append_fn(&c.arg, &q_rows, &k_rows, &v_rows, parents, nodes, requests, most,
+                          q_heads, q_weight, k_weight, eps, half ? inv_freq : nullptr, rot_dim,
+                          interleaved, scale,
                           &out_rows, static_cast<int32_t*>(status.data_ptr()), stream_of(c.dev)); },
                 out, status);
   END_HANDLE_TH_ERRORS
@@ -281,17 +285,18 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* nodes = need<int32_t>("n_nodes", a[6], {B}, at::kInt, c.dev);
   const float scale =
       a[7] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D))) : number("scale", a[7]);
+  const int32_t requests = small("B", B), most = small("N", N), q_heads = small("q_heads", heads);
   if (!here(c.dev)) Py_RETURN_NONE;
   const at::Tensor* lent = given("workspace", a[10]);
   if (lent && (lent->device() != c.dev || lent->scalar_type() != at::kByte || !lent->is_contiguous()))
     refuse("workspace is on " + lent->device().str() + ", the cache on " + c.dev.str());
   const at::Tensor workspace =
-      lent ? *lent : new_workspace(small("B", B), small("N", N), small("q_heads", heads), c);
+      lent ? *lent : new_workspace(requests, most, q_heads, c);
   const at::Tensor out = output("out", a[8], q.sizes(), c.dtype, c.dev, nodes != nullptr);
   const specv_rows out_rows = rows_of("out", out, q.sizes(), c.dtype, c.dev);
   const at::Tensor status = per_request("status", a[9], B, c.dev);
-  return answer([&] { return attention_fn(&c.arg, &q_rows, parents, nodes, small("B", B), small("N", N),
-                             small("q_heads", heads), scale, &out_rows,
+  return answer([&] { return attention_fn(&c.arg, &q_rows, parents, nodes, requests, most, q_heads, scale,
+                             &out_rows,
                              static_cast<int32_t*>(status.data_ptr()), workspace.data_ptr(),
                              static_cast<size_t>(workspace.numel()), stream_of(c.dev)); },
                 out, status);
@@ -307,10 +312,11 @@ PyObject* keep_path(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t B = c.B, N = path.size(1);
   const auto* nodes = must<int32_t>("path_nodes", a[0], {B, N}, at::kInt, c.dev);
   const auto* accepted = must<int32_t>("accepted_len", a[1], {B}, at::kInt, c.dev);
+  const int32_t requests = small("B", B), most = small("N", N);
   if (!here(c.dev)) Py_RETURN_NONE;
   const at::Tensor lens = per_request("new_lens", a[6], B, c.dev);
   const at::Tensor status = per_request("status", a[7], B, c.dev);
-  return answer([&] { return keep_fn(&c.arg, nodes, accepted, small("B", B), small("N", N),
+  return answer([&] { return keep_fn(&c.arg, nodes, accepted, requests, most,
                         static_cast<int32_t*>(lens.data_ptr()),
                         static_cast<int32_t*>(status.data_ptr()), stream_of(c.dev)); },
                 lens, status);
@@ -354,17 +360,19 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse(std::string(name) + " must have a contiguous last dimension");
   };
   last_is_contiguous("logits", z);
+  const int32_t requests = small("B", B), rows = small("R", R), vocab = small("V", V);
+  const int32_t longest = small("L", history.size(1)), num_bias = small("biases", biases);
   if (!here(dev)) Py_RETURN_NONE;
   const at::Tensor out = output("out", a[13], z.sizes(), dtype, dev, nodes != nullptr);
   last_is_contiguous("out", out);
   const at::Tensor status = per_request("status", a[14], B, dev);
   return answer(
       [&] { return process_fn(z.data_ptr(), stride(z, 0), three ? stride(z, 1) : 0,
-                 dtype == at::kFloat ? SPECV_F32 : SPECV_BF16, small("B", B), small("R", R),
-                 small("V", V), R > 1 ? tokens : nullptr, parents, nodes,
+                 dtype == at::kFloat ? SPECV_F32 : SPECV_BF16, requests, rows, vocab,
+                 R > 1 ? tokens : nullptr, parents, nodes,
                  static_cast<const int32_t*>(history.data_ptr()), stride(history, 0),
-                 small("L", history.size(1)), seq_lens, prompt_lens, repetition, frequency, presence,
-                 bias_tokens, bias_values, small("biases", biases), allowed, out.data_ptr(),
+                 longest, seq_lens, prompt_lens, repetition, frequency, presence,
+                 bias_tokens, bias_values, num_bias, allowed, out.data_ptr(),
                  stride(out, 0), three ? stride(out, 1) : 0, static_cast<int32_t*>(status.data_ptr()),
                  stream_of(dev)); },
       out, status);

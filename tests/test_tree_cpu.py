@@ -281,6 +281,35 @@ def test_binding_refuses_wrong_tensors():
         sv.process_logits(z[:, 0], hist.float(), lens)
 
 
+def test_binding_refuses_sizes_past_32_bits():
+    """Each with a ValueError that names it: not behind the point where Python's lock is given up."""
+    big = 2 ** 31 + 7
+
+    def t(*shape, dtype=torch.int32):
+        return torch.empty(shape, dtype=dtype, device="meta")  # takes no memory
+
+    bf16, c = torch.bfloat16, t(9, 16, 1, 8, dtype=torch.bfloat16)
+    one = t(1, 1, 1, 8, dtype=bf16)
+    for name, call in [
+        ("V", lambda: sv.process_logits(t(1, big, dtype=bf16), t(1, 5), t(1))),
+        ("L", lambda: sv.process_logits(t(1, 9, dtype=bf16), t(1, big), t(1))),
+        ("B", lambda: sv.process_logits(t(big, 9, dtype=bf16), t(big, 5), t(big))),
+        ("R", lambda: sv.process_logits(t(1, big, 9, dtype=bf16), t(1, 5), t(1), tokens=t(1, big - 1))),
+        ("biases", lambda: sv.process_logits(t(1, 9, dtype=bf16), t(1, 5), t(1), bias_tokens=t(1, big),
+                                             bias_values=t(1, big, dtype=torch.float32))),
+        ("B", lambda: sv.tree_attention(t(big, 1, 1, 8, dtype=bf16), c, c, t(big, 3), t(big))),
+        ("N", lambda: sv.tree_attention(t(1, big, 1, 8, dtype=bf16), c, c, t(1, 3), t(1))),
+        ("q_heads", lambda: sv.tree_attention(t(1, 1, big, 8, dtype=bf16), c, c, t(1, 3), t(1))),
+        ("q_heads", lambda: sv.append_nodes(t(1, 1, big, 8, dtype=bf16), one, one, c, c, t(1, 3), t(1))),
+        ("inv_freq", lambda: sv.append_nodes(one, one, one, c, c, t(1, 3), t(1),
+                                             t(2 ** 30, dtype=torch.float32))),
+        ("B", lambda: sv.keep_path(t(big, 2), t(big), c, c, t(big, 3), t(big))),
+        ("N", lambda: sv.keep_path(t(1, big), t(1), c, c, t(1, 3), t(1))),
+    ]:
+        with pytest.raises(ValueError, match=f"^{name} is too large"):
+            call()
+
+
 # ---------------------------------------------------- the plain forms themselves
 
 
