@@ -44,7 +44,7 @@ namespace {
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kRows = 128;     // query rows of a stream
 static_assert(kKeys == kRows, "tiles of queries, keys and values are laid out alike");
-constexpr int kMaxCtas = 152;  // SMs of a GB300
+constexpr int kMaxCtas = kSms;
 constexpr int kLoadWarps = 4;
 constexpr int kLoadWarp = 8;  // the first of them; the last makes the tensor copies
 constexpr int kCheckWarp = 12;
@@ -1385,7 +1385,7 @@ cudaError_t run(const AttnParams& P, const CUtensorMap& k_map, const CUtensorMap
   // 24 items 45 us and 48, 64 items 58 and 47, 64-node trees 388 and 359).
   const int64_t items = static_cast<int64_t>(P.B) * P.cache.heads *
                         ((P.N * P.group + S::kRowTile - 1) / S::kRowTile);
-  const bool shared = P.part_rows <= 16 || items < 38;
+  const bool shared = P.part_rows <= 16 || items < kSms / 4;
   cfg.gridDim = dim3(P.ctas, shared ? (P.part_rows + 15) / 16 : 1);
   cfg.blockDim = dim3(shared || P.part_rows <= 32 ? 256 : 512);
   cfg.stream = stream;

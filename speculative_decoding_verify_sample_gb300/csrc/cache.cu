@@ -270,7 +270,7 @@ void run_append(const AppendParams& P, cudaStream_t stream) {
   // 1,536 nodes, 12.4 us with two warps a node and 14.4 with one; 64 trees, 2,048 nodes,
   // 15.0 and 16.0; for 32 to an SM 32 trees took 13.8 us against 11.6, 64 trees 18.2).
   const int tokens = P.B * P.N;
-  const int splits = tokens >= 2432 ? 1 : (2432 + tokens - 1) / tokens;
+  const int splits = tokens >= 16 * kSms ? 1 : (16 * kSms + tokens - 1) / tokens;
   const dim3 grid((tokens + kAppendWarps - 1) / kAppendWarps, splits < passes ? splits : passes);
   constexpr int kThreads = kAppendWarps * 32;
   if (narrow) {

@@ -13,6 +13,7 @@
 namespace specv_cache_ops {
 
 constexpr int kMaxNodes = SPECV_MAX_NODES;
+constexpr int kSms = 152;  // of a GB300: what the rules for splits and variants were measured on
 constexpr unsigned kFullMask = 0xffffffffu;
 
 struct Bf16 {

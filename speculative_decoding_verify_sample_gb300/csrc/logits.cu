@@ -434,11 +434,12 @@ cudaError_t launch(Params& P, int B, cudaStream_t stream) {
   // requests 20.0 us with 1024 and 19.7 with 8192 entries, 8 requests 37.3 and 27.5;
   // two rows: 4 requests 7.6 and 8.3, 6 requests 10.3 and 6.3).
   const int64_t chunks = static_cast<int64_t>(B) * ((P.V + 8191) / 8192);
-  if (chunks < 76) return run<DT, 1024, 256, kLayout>(P, B, stream);
+  if (chunks < kSms / 2) return run<DT, 1024, 256, kLayout>(P, B, stream);
   // With few rows a block's text outweighs them, and chunks of twice the size halve it
   // (512 requests of two rows 94 us, 132 with 8192; 64 chains of five 41.5 and 43.9; but
-  // 16 requests of five 20.6 and 19.0, 32 nodes 78 and 74), where two blocks fit an SM.
-  if (chunks >= 456 && P.rows < 7 && smem_of<16384, 512>(P) <= 113 * 1024)
+  // 16 requests of five 20.6 and 19.0, 32 nodes 78 and 74).
+  static_assert(sizeof(Text<16384, 16>) + 2 * 16384 <= 113 * 1024, "two blocks to an SM");
+  if (chunks >= 3 * kSms && P.rows < 7)
     return run<DT, 16384, 512, kLayout>(P, B, stream);
   return run<DT, 8192, 512, kLayout>(P, B, stream);
 }
