@@ -14,6 +14,7 @@ from ._native import (DEV_BAD_CACHE, DEV_BAD_DRAFT_LEN, DEV_BAD_PENALTY, DEV_BAD
                       DEV_BAD_TEMPERATURE, DEV_BAD_TOKEN, DEV_BAD_TREE, DEV_BAD_UNIFORM,
                       DEV_NO_DRAFT, DEV_TIMEOUT, SPECV_BF16, SPECV_F32, SpecVerifyError, check, lib)
 from .build import build
+from .tree import AttentionWorkspace, append_nodes, keep_path, process_logits, tree_attention
 
 __all__ = [
     "build", "lib", "Workspace", "HostStaging", "spec_verify_sample", "spec_verify_sample_debug",
@@ -24,18 +25,6 @@ __all__ = [
     "DEV_BAD_ROW", "DEV_NO_DRAFT", "DEV_TIMEOUT", "DEV_BAD_CACHE", "DEV_BAD_PENALTY",
     "AttentionWorkspace", "append_nodes", "tree_attention", "process_logits", "keep_path",
 ]
-
-
-_TREE = ("AttentionWorkspace", "append_nodes", "tree_attention", "process_logits", "keep_path")
-
-
-def __getattr__(name):
-    # the binding of a drafted tree's operators needs torch, this module does not
-    if name in _TREE:
-        from . import tree
-        globals().update({n: getattr(tree, n) for n in _TREE})
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _torch():

@@ -17,8 +17,6 @@ import importlib.machinery
 import importlib.util
 import os
 
-import torch
-
 from ._native import SpecVerifyError, lib
 from .build import binding_path
 
@@ -46,6 +44,7 @@ def _load():
 
 @contextlib.contextmanager
 def _there(device, stream):
+    import torch
     with torch.cuda.device(device):
         if stream is None:
             yield
@@ -59,7 +58,7 @@ def _there(device, stream):
 def _call(name, fn, tensor, stream, *args):
     """fn(*args) on tensor's device and the stream: its outputs are allocated where
     it launches."""
-    cuda = isinstance(tensor, torch.Tensor) and tensor.is_cuda
+    cuda = getattr(tensor, "is_cuda", False)
     out = fn(*args) if stream is None or not cuda else None
     if out is None:
         with _there(tensor.device, stream):
@@ -98,6 +97,7 @@ class AttentionWorkspace:
     may be replayed together) need one each."""
 
     def __init__(self, B: int, N: int, q_heads: int, kv_heads: int, head_dim: int, device=None):
+        import torch
         self.nbytes = int(lib().specv_attention_workspace_bytes(B, N, q_heads, kv_heads, head_dim))
         if self.nbytes == 0:
             raise ValueError(f"unsupported attention shape B={B} N={N} q_heads={q_heads} "

@@ -281,6 +281,16 @@ def test_binding_refuses_wrong_tensors():
         sv.process_logits(z[:, 0], hist.float(), lens)
 
 
+def test_star_import_needs_no_torch():
+    """Everything the package names can be imported where torch cannot."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", "import sys; sys.modules['torch'] = None\n"
+                    "from speculative_decoding_verify_sample_gb300 import *\n"
+                    "import speculative_decoding_verify_sample_gb300 as sv\n"
+                    "assert all(callable(globals()[n]) or n.startswith('DEV_') for n in sv.__all__)\n"
+                    "assert tree_attention is sv.tree_attention"], cwd=root, check=True)
+
+
 def test_binding_refuses_sizes_past_32_bits():
     """Each with a ValueError that names it: not behind the point where Python's lock is given up."""
     big = 2 ** 31 + 7
