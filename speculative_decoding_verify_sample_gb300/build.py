@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -43,9 +44,27 @@ def binding_path() -> str:
         PKG_DIR, f"_binding-{torch.__version__}-py{sysconfig.get_python_version()}.so")
 
 
+_binding_failure = None
+
+
+def binding_failure():
+    """Why this process's build() left the extension unbuilt, or None."""
+    return _binding_failure
+
+
+def _keep_failure(why: str):
+    global _binding_failure
+    _binding_failure = why
+    if os.path.exists(binding_path()):  # of an older source: not to be loaded for this one
+        os.remove(binding_path())
+    warnings.warn(f"the library is built without the drafted tree's operators in Python: {why}")
+
+
 def _build_binding(force: bool, verbose: bool):
     """Starts the extension's compiler where it is needed; returns what waits for
-    it.  Without torch there are no tensors to bind and nothing is built."""
+    it.  Without torch there are no tensors to bind and nothing is built; where it cannot
+    be built, the reason is kept for the calls that need it."""
+    global _binding_failure
     try:
         import torch
     except ImportError:
@@ -53,7 +72,10 @@ def _build_binding(force: bool, verbose: bool):
     home = os.path.dirname(torch.__file__)
     path = binding_path()
     if not force and not _stale(path, [BINDING_SOURCE, HEADERS[0]]):
+        _binding_failure = None
         return lambda: None
+    if torch.version.cuda is None:
+        return lambda: _keep_failure("this torch has no CUDA")
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     include = [INCLUDE, os.path.join(home, "include"),
                os.path.join(home, "include", "torch", "csrc", "api", "include"),
@@ -65,18 +87,27 @@ def _build_binding(force: bool, verbose: bool):
            f"-Wl,-rpath,{home}/lib", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd))
-    compiler = subprocess.Popen(cmd)
+    try:
+        compiler = subprocess.Popen(cmd, stderr=subprocess.PIPE, text=True)
+    except OSError as e:
+        why = str(e)
+        return lambda: _keep_failure(why)
 
     def wait():
-        if compiler.wait() != 0:
-            raise subprocess.CalledProcessError(compiler.returncode, cmd)
+        global _binding_failure
+        said = compiler.communicate()[1]
+        if compiler.returncode != 0:
+            _keep_failure(f"{cmd[0]} failed: {said[-4000:]}")
+            return
         os.replace(tmp, path)
+        _binding_failure = None
     return wait
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile the CUDA library and the binding's extension where a source or
-    header is newer than them."""
+    header is newer than them.  An extension that cannot be built is a warning: the
+    library stands without it."""
     wait = _build_binding(force, verbose)
     try:
         _build_library(force, verbose, extra_flags)

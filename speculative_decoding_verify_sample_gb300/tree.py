@@ -18,19 +18,19 @@ import importlib.util
 import os
 
 from ._native import SpecVerifyError, lib
-from .build import binding_path
+from .build import binding_failure, binding_path
 
 _binding = None
 
 
-def _load():
-    """The extension, bound to the library.  Raises if it has not been built."""
+def load():
+    """The extension, bound to the library.  Raises if it is not built."""
     global _binding
     if _binding is None:
         path, handle = binding_path(), lib()
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is not built; run "
-                               "speculative_decoding_verify_sample_gb300.build()")
+            raise RuntimeError(f"{path} is not built: " + (
+                binding_failure() or "run speculative_decoding_verify_sample_gb300.build()"))
         loader = importlib.machinery.ExtensionFileLoader("_binding", path)
         module = importlib.util.module_from_spec(
             importlib.util.spec_from_loader("_binding", loader))
@@ -86,7 +86,7 @@ def append_nodes(q, k, v, k_cache, v_cache, page_table, cache_lens, inv_freq=Non
     [B] int32 (None: all N).  Returns (q_out, status [B] int32: 0 or DEV_*
     bits); rows of q_out behind n_nodes[b] are left as they were (zeros in a
     new one).  ``q_out`` may be q.  Asynchronous."""
-    return _call("spec_append_nodes", (_binding or _load()).append_nodes, k_cache, stream, q, k, v,
+    return _call("spec_append_nodes", (_binding or load()).append_nodes, k_cache, stream, q, k, v,
                  k_cache, v_cache, page_table, cache_lens, inv_freq, parents, n_nodes, q_weight,
                  k_weight, eps, interleaved, rope_scale, q_out, status)
 
@@ -118,7 +118,7 @@ def tree_attention(q, k_cache, v_cache, page_table, cache_lens, parents=None, n_
     scores.  Returns (out [B, N, q_heads, D], status [B] int32: 0 or DEV_*
     bits); rows of out behind n_nodes[b] are left as they were (zeros in a new
     one).  Asynchronous."""
-    return _call("spec_tree_attention", (_binding or _load()).tree_attention, k_cache, stream, q,
+    return _call("spec_tree_attention", (_binding or load()).tree_attention, k_cache, stream, q,
                  k_cache, v_cache, page_table, cache_lens, parents, n_nodes, scale, out, status,
                  None if workspace is None else workspace.tensor)
 
@@ -131,7 +131,7 @@ def keep_path(path_nodes, accepted_len, k_cache, v_cache, page_table, cache_lens
     may be [layers, pages, page_size, heads, D]: every layer in one call.
     Returns (new_lens [B] = cache_lens + accepted_len + 1, status [B]) int32;
     a flagged request keeps its rows and its length.  Asynchronous."""
-    return _call("spec_keep_path", (_binding or _load()).keep_path, k_cache, stream, path_nodes,
+    return _call("spec_keep_path", (_binding or load()).keep_path, k_cache, stream, path_nodes,
                  accepted_len, k_cache, v_cache, page_table, cache_lens, new_lens, status)
 
 
@@ -153,6 +153,6 @@ def process_logits(logits, history, seq_lens, prompt_lens=None, *, tokens=None, 
     int32: bit t % 32 of word t // 32 set, or z becomes -inf.  Returns (out,
     status [B] int32: 0 or DEV_* bits); rows behind n_nodes[b] are left as
     they were (zeros in a new out).  ``out`` may be logits.  Asynchronous."""
-    return _call("spec_process_logits", (_binding or _load()).process_logits, logits, stream, logits,
+    return _call("spec_process_logits", (_binding or load()).process_logits, logits, stream, logits,
                  history, seq_lens, prompt_lens, tokens, parents, n_nodes, repetition, frequency,
                  presence, bias_tokens, bias_values, allowed, out, status)

@@ -291,6 +291,34 @@ def test_star_import_needs_no_torch():
                     "assert tree_attention is sv.tree_attention"], cwd=root, check=True)
 
 
+@pytest.mark.parametrize("why", ["no compiler", "failed", "no CUDA"])
+def test_build_without_the_extension_leaves_the_library(monkeypatch, tmp_path, why):
+    """build() warns and returns, a stale extension is gone, and a call that needs it says why."""
+    import importlib
+
+    how = importlib.import_module("speculative_decoding_verify_sample_gb300.build")
+    tree = importlib.import_module("speculative_decoding_verify_sample_gb300.tree")
+    built, path = [], tmp_path / "extension.so"
+    path.write_text("of an older source")
+    os.utime(path, (1, 1))
+    for module in (how, tree):
+        monkeypatch.setattr(module, "binding_path", lambda: str(path))
+    monkeypatch.setattr(how, "_build_library", lambda *a: built.append(a))
+    monkeypatch.setattr(how, "_binding_failure", None)
+    monkeypatch.setattr(tree, "_binding", None)
+    if why == "no CUDA":
+        monkeypatch.setattr(torch.version, "cuda", None)
+    else:
+        monkeypatch.setenv("CXX", str(tmp_path / "none") if why == "no compiler" else "false")
+    with pytest.warns(UserWarning, match="without the drafted tree's operators"):
+        assert how.build() == how.LIB_PATH
+    assert built and not path.exists()
+    reason = {"no compiler": "No such file", "failed": "false failed", "no CUDA": "no CUDA"}[why]
+    t = _tensors()
+    with pytest.raises(RuntimeError, match=reason):
+        sv.tree_attention(t["q"], t["cache"], t["cache"], t["table"], t["lens"])
+
+
 def test_binding_refuses_sizes_past_32_bits():
     """Each with a ValueError that names it: not behind the point where Python's lock is given up."""
     big = 2 ** 31 + 7
