@@ -63,6 +63,8 @@ def _call(name, fn, tensor, stream, *args):
     if out is None:
         with _there(tensor.device, stream):
             out = fn(*args)
+        if out is None:  # the stream took the call to its own device
+            raise ValueError(f"stream is of another device than the tensors, on {tensor.device}")
     if out.__class__ is int:
         raise SpecVerifyError(name, out)
     return out

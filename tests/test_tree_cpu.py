@@ -319,6 +319,21 @@ def test_build_without_the_extension_leaves_the_library(monkeypatch, tmp_path, w
         sv.tree_attention(t["q"], t["cache"], t["cache"], t["table"], t["lens"])
 
 
+def test_binding_refuses_a_stream_of_another_device(monkeypatch):
+    """The extension answers None where the tensors are not on the current device: with such a
+    stream it does so twice."""
+    import contextlib
+    import types
+
+    tree = sv.tree
+    monkeypatch.setattr(tree, "_there", lambda device, stream: contextlib.nullcontext())
+    tensor = types.SimpleNamespace(is_cuda=True, device="cuda:1")
+    with pytest.raises(ValueError, match="stream is of another device than the tensors, on cuda:1"):
+        tree._call("spec_keep_path", lambda: None, tensor, object())
+    answers = iter([None, ("out", "status")])  # tensors of another device than the current one
+    assert tree._call("spec_keep_path", lambda: next(answers), tensor, None) == ("out", "status")
+
+
 def test_binding_refuses_sizes_past_32_bits():
     """Each with a ValueError that names it: not behind the point where Python's lock is given up."""
     big = 2 ** 31 + 7
