@@ -416,7 +416,7 @@ typedef struct specv_rows {
  *   q, k, v   [B, N, q_heads | heads | heads, head_dim] (specv_rows, of one
  *             projection or of three); q_out may be q itself, but no two of
  *             the buffers may overlap otherwise.
- *   q_weight, k_weight  [head_dim] of the cache's dtype, or NULL.
+ *   q_weight, k_weight  [head_dim] of the cache's dtype, 16-byte aligned, or NULL.
  *   inv_freq  [rot_dim / 2] float32 (a long-context scaling is in it), or
  *             NULL with rot_dim = 0: no rotation.  rot_dim even, <= head_dim.
  * Two requests that share a page must not both write the same slot.

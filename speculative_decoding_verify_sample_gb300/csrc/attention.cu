@@ -9,8 +9,9 @@
 //   P = exp2(S c - m c), c = scale log2 e, m the running row maximum,
 //   O = O + P V (tcgen05, P from TMEM where S was, V in shared memory),
 //
-// and O is rescaled only when the maximum has risen by more than 2^8, which
-// no result shows: m is whatever both O and the sum l were taken with.
+// and O is rescaled only when the maximum has risen by more than 2^8 (a known
+// form of the running softmax), which no result shows: m is whatever both O and the
+// sum l were taken with.
 //
 // The work is the list of (request, key head, row tile, 128-key tile), a unit
 // each, cut into even runs, one for every CTA (one to an SM), whatever the
@@ -25,11 +26,13 @@
 //
 // Up to 128 rows the cache's bytes bound it: a tile of keys and one of values, 64 KB,
 // take an SM 1.5 us and their MMAs 0.7.  Measured: eight chains over 16,111 to
-// 32,749 keys 136 us (801 MB, 5.9 TB/s), 32 trees over 97 to 4,093 keys 70 us (288 MB,
-// 4.1 TB/s: about 8 us until the first scores and 8 for the join are fixed), one
-// token over 1,999 keys 18.7 us, nearly all of it such latencies.  More rows are
-// bound by the MMAs, and those of S by shared memory, which both operands are read
-// from: 64 nodes of 64 heads over 4,001 to 8,111 keys 360 us (1,130 TFLOP/s).
+// 32,749 keys 134 us (801 MB, 6.0 TB/s), 32 trees over 97 to 4,093 keys 68 us (288 MB,
+// 4.2 TB/s: about 8 us until the first scores and 8 for the join are fixed), one
+// token over 1,999 keys 16.4 us, nearly all of it such latencies.  With more rows no
+// unit is full: 64 nodes of 64 heads over 4,001 to 8,111 keys take 395 to 408 us (1,010
+// TFLOP/s; under the profiler tensor pipe 51 % active, tensor memory 53, shared memory's
+// banks 19, issue 35, DRAM 60).  What is left is the chain of scores, softmax and
+// sum in each stream, of which TMEM holds two.
 
 #include <cuda.h>
 
@@ -1051,7 +1054,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float a = exp2_of(y.x), b = exp2_of(y.y);
               sums[e / 2 % 2] =
                   add2(sums[e / 2 % 2], pair_of(__float_as_uint(a), __float_as_uint(b)));
-              // the weights' one rounding, to the type of the values they meet
+              // the weights' one rounding, to the type of the values they meet: the MMA takes
+              // both operands in one 16-bit type.  (The sum has them as they are.  Against 64 bits
+              // the output is off by 2.2e-3 of its size in bf16, 2.9e-4 in f16; by 1.6e-3 and
+              // 2.1e-4 with weights in 32 bits, the output's own rounding.)
               p[e / 2] = E::pack(a, b);
             }
             tmem_store16(tS[st] + lanes + k / 2, p);  // over scores of this row, all read

@@ -44,10 +44,12 @@ __device__ __forceinline__ float2 turn(int pos, float freq, uint64_t steps, floa
 }
 
 // x <- x / sqrt(mean x^2 + eps) * weight, then the pairs' rotation, in 32 bits.
-// Bytes bound it, each row read and written once: 256 trees of 17 to 32 nodes, 64
-// query and 8 + 8 key and value heads of 128, 57 us (257 MB, 4.5 TB/s; three blocks
-// of 80 registers to an SM keep 96 KB of copies in flight); 32 trees 10 to 12 us and
-// one chain 6 to 8, most of it the chain of loads from a request's length to its slot.
+// Each row is read and written once: 256 trees of 17 to 32 nodes, 64 query and 8 + 8
+// key and value heads of 128, 57 us (257 MB, 4.5 TB/s).  Three blocks of 80 registers fit an
+// SM, 456 the machine, and a wave that is not full costs nearly a whole one (of 32 nodes:
+// 114 trees, one wave, 31.5 us, 128 43.2; 228 56.5, 256 65.9); under the profiler 71 % of the
+// issue slots are taken.  32 trees 10 to 12 us and one chain 6 to 8, most of it
+// the chain of loads from a request's length to its slot.
 //
 // A warp has a node and goes through its heads, 32 / kLanes rows at a time.  A
 // lane has two 16-byte pieces of a row, the two that a rotation in halves
@@ -287,9 +289,9 @@ void run_append(const AppendParams& P, cudaStream_t stream) {
 constexpr int kKeepThreads = 256;
 constexpr int kBatch = 8;  // rows a thread has in flight
 
-// The kept rows' bytes, read and written, bound it: 128 requests, 16 layers, 8 + 8
-// heads of 128, up to 6 rows of each move in 16.4 us (50 MB, 3.1 TB/s), one layer of
-// one request in 5.  (Several layers to a block, so that length and pages are read
+// A block's chain of loads (count, path, pages, rows) bounds it, three blocks of 66
+// registers to an SM at a time: 128 requests, 16 layers, 8 + 8 heads of 128, up to 6 rows of
+// each move in 16.4 us (50 MB, 3.1 TB/s), one layer of one request in 4.  (Several layers to a block, so that length and pages are read
 // less often, took 15.9 to 16.5 us; more warps to an SM, of fewer registers, 23 to 30.)
 //
 // One block per request and layer; a thread owns 16 bytes of a row of K or V

@@ -10,7 +10,7 @@
 // leaves nothing of 16 bytes), and what the text says is laid over the copy.
 // Measured: 512 requests, two rows of 129,280 bf16 and texts of up to 4,001 tokens
 // 94 us (4.4 TB/s of rows; mask and copy alone 64), 32 trees of up to 32 nodes
-// over 128,256 entries 74 us (4.7 TB/s), one chain of five rows 6.6 us.  The rest is
+// over 128,256 entries 72 us (4.8 TB/s), one chain of five rows 6.1 us.  The rest is
 // the text, which every chunk's block reads in whole before it can patch.
 
 #include "cache.cuh"

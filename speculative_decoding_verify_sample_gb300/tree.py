@@ -79,7 +79,7 @@ def append_nodes(q, k, v, k_cache, v_cache, page_table, cache_lens, inv_freq=Non
     projection will do); k_cache, v_cache [pages, page_size, heads, D];
     page_table [B, P] and cache_lens [B] int32.  Each head of q and k is
     divided by the root of its mean square plus ``eps`` and multiplied by
-    ``q_weight`` / ``k_weight`` [D] (None: no norm), then its first
+    ``q_weight`` / ``k_weight`` [D] (16-byte aligned; None: no norm), then its first
     2 * len(inv_freq) elements are rotated by (cache_lens[b] + depth of the
     node) * ``inv_freq`` (f32; None: no rotation), in pairs (2j, 2j + 1) if
     ``interleaved`` and (j, j + len(inv_freq)) if not, and scaled by
