@@ -98,6 +98,9 @@ typedef enum specv_dtype {
 #define SPECV_DEV_BAD_CACHE       0x100 /* a cache length or page number out of range */
 #define SPECV_DEV_BAD_PENALTY     0x200 /* a penalty that is not finite, or a
                                            repetition penalty not above 0         */
+#define SPECV_DEV_BAD_POSITION    0x400 /* an axis number outside 0..axes-1       */
+#define SPECV_DEV_BAD_BEAM        0x800 /* a beam number outside -1..W-1, or a
+                                           beam's score that is NaN or +inf       */
 
 /* Limits. */
 #define SPECV_MAX_DRAFT 16      /* K <= 16                               */
@@ -105,6 +108,9 @@ typedef enum specv_dtype {
 #define SPECV_MAX_NODES 64      /* nodes of a tree, rows of a request     */
 #define SPECV_MAX_HEAD_DIM 128  /* cache operators: a multiple of 8 in 8..128 */
 #define SPECV_MAX_BIAS 1024     /* biased tokens of a request             */
+#define SPECV_MAX_BEAMS 64      /* beams of a request, before and after   */
+#define SPECV_MAX_STATES 32     /* states of a reordering                 */
+#define SPECV_MAX_CHUNK_REQUESTS 16384  /* requests of a chunk attention     */
 
 /* Library version (major*10000 + minor*100 + patch). */
 int specv_version(void);
@@ -507,6 +513,143 @@ specv_status spec_process_logits(const void* logits, int64_t batch_stride, int64
                                  const float* bias_values, int num_bias, const int32_t* allowed,
                                  void* out, int64_t out_batch_stride, int64_t out_row_stride,
                                  int32_t* status, specv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Before the verification: the prompt's own pass over the paged cache, in
+ * chunks of any length beside single tokens, and the drafting of a tree.
+ *
+ *   spec_append_chunk     norms, rotates and writes the tokens' keys and values
+ *   spec_chunk_attention  attends from the tokens to the cache
+ *   spec_select_beams     a tree's next level, or a beam search's next step
+ *   spec_reorder_beams    moves the beams' states along
+ *
+ * Tokens.  The new tokens of all requests are packed: rows cu_tokens[b] ..
+ * cu_tokens[b+1]-1 of T are request b's, none at all too.  Token i of request
+ * b lives in cache slot lens[b] + i, which is also its position unless the
+ * call is given others.  (specv_rows of packed rows: [T, heads, head_dim],
+ * node_stride from token to token, batch_stride 0.)
+ *
+ * Errors in the data: as with the operators on a drafted tree, by request,
+ * in status[b].  SPECV_DEV_BAD_DRAFT_LEN: cu_tokens falls or leaves 0..T (then
+ * the request has no rows), or counts more than `longest` tokens;
+ * SPECV_DEV_BAD_CACHE: lens[b] or a page out of range.  Rows of no request
+ * are left as they were.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Norms, rotation and append of the tokens' projections, one kernel: as
+ * spec_append_nodes, for packed tokens, with
+ *   t = positions[axis_of[j], i] * inv_freq[j]   (NULL positions: lens[b] + i's slot)
+ * for pair j of the token in packed row i.
+ *   q, k, v, q_out  [T, q_heads | heads | heads, head_dim]; q_out may be q
+ *             itself, but no two of the buffers may overlap otherwise.
+ *   cu_tokens [B+1] int32; no two requests' ranges may overlap.
+ *   positions [axes, T] int32 of any sign, rows position_stride apart, or NULL
+ *             (axes 0 or 1): a request's slots are its positions.
+ *   axis_of   [rot_dim / 2] int32: the axis (time, height, width ...) by which a
+ *             pair turns, 0 <= axis_of[j] < axes (else every request has
+ *             SPECV_DEV_BAD_POSITION); NULL: axis 0, with axes = 1.
+ * The other arguments as spec_append_nodes has them.  Two requests that share a
+ * page must not both write the same slot.
+ */
+specv_status spec_append_chunk(const specv_cache* cache, const specv_rows* q, const specv_rows* k,
+                               const specv_rows* v, const int32_t* cu_tokens, int B, int T,
+                               int q_heads, const int32_t* positions, int64_t position_stride,
+                               int axes, const int32_t* axis_of, const void* q_weight,
+                               const void* k_weight, float eps, const float* inv_freq, int rot_dim,
+                               int interleaved, float rope_scale, const specv_rows* q_out,
+                               int32_t* status, specv_stream_t stream);
+
+/* Bytes of workspace spec_chunk_attention needs (0 for sizes out of range). */
+size_t specv_chunk_workspace_bytes(int longest, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * Attention of the tokens over the cache.  The token at p = lens[b] + i sees
+ * slot s of its request, below lens[b] + its number of tokens, iff
+ *   s < prefix_lens[b]  or  p - window < s <= p,
+ *   out[i,h] = sum_s softmax_s(y) v[s, h'],  h' = h / (q_heads/heads),
+ *   y = cap tanh(scale q[i,h] . k[s,h'] / cap) - slopes[h] |p - s|.
+ * No other slot counts, whatever it holds, and pages of which no token of the
+ * call sees a slot need not exist.  Scores, maxima and sums in 32 bits; the
+ * weights are rounded to the cache's dtype before the product with the values.
+ *   q, out    [T, q_heads, head_dim]; q_heads a multiple of cache->heads.
+ *   cu_tokens [B+1] int32; the tokens' own rows are in the cache already
+ *             (spec_append_chunk).  B <= SPECV_MAX_CHUNK_REQUESTS.
+ *   longest   no request has more tokens (T will do; the work is laid out
+ *             for it); longest * q_heads / heads < 2^29.
+ *   scale     > 0 (1/sqrt(head_dim) as a rule).
+ *   cap       > 0, or 0: scores are not capped.
+ *   window    >= 1, or 0: no limit.
+ *   prefix_lens [B] int32 >= 0 (else SPECV_DEV_BAD_CACHE), or NULL: 0.  The
+ *             part of it that lens[b] and the tokens do not reach is not there.
+ *   slopes    [q_heads] float32, or NULL: 0.
+ *   workspace specv_chunk_workspace_bytes bytes, 256-byte aligned, whatever
+ *             it holds.  Calls that may run at the same time need one each.
+ * A wait inside the kernel that lasts two seconds gives up: then every request
+ * of the call has SPECV_DEV_TIMEOUT in its status, and the rows hold anything.
+ * Two kernels, the second as a programmatic dependent launch.
+ */
+specv_status spec_chunk_attention(const specv_cache* cache, const specv_rows* q,
+                                  const int32_t* cu_tokens, int B, int T, int longest, int q_heads,
+                                  float scale, float cap, int window, const int32_t* prefix_lens,
+                                  const float* slopes, const specv_rows* out, int32_t* status,
+                                  void* workspace, size_t workspace_bytes, specv_stream_t stream);
+
+/* Bytes of workspace spec_select_beams needs (0 for sizes out of range). */
+size_t specv_beam_workspace_bytes(int B, int W, int K, int V);
+
+/*
+ * The best next tokens of a request's W beams: of all (w, v)
+ *   score(w, v) = scores[b,w] + logits[b,w,v] - log sum_u exp logits[b,w,u]
+ * the K largest, falling, ties to the lower beam and then the lower token.  The
+ * nodes of a drafted tree's next level (the beams are the last level's, scores
+ * their summed log probabilities), or a beam search's step.
+ *   logits    [B, W, V] of `dtype` (SPECV_F32 or SPECV_BF16), element (b, w, v)
+ *             at b*batch_stride + w*row_stride + v (strides 0 or more).
+ *   scores    [B, W] float32; -inf: the beam is not in play and its row not read.
+ *   ended     [B, W] int32 or NULL: a beam whose text has ended (not 0) is one
+ *             candidate, with the score and end_token as it is; its row is not read.
+ *   out_scores [B, K] float32, tokens, beams [B, K] int32: behind the last
+ *             candidate above -inf: -inf, -1, -1.
+ *   status    [B]: SPECV_DEV_BAD_ROW (a row has a NaN or +inf), or
+ *             SPECV_DEV_BAD_BEAM (a score is one); such a request has no candidates.
+ *             A row of -inf alone has none either, and is no error.
+ *   W, K      1..SPECV_MAX_BEAMS.
+ *   workspace specv_beam_workspace_bytes bytes, 256-byte aligned, whatever it
+ *             holds.  Calls that may run at the same time need one each.
+ * The rows' sums are held in 64 bits (of exponentials in 32), scores are compared
+ * in 64 bits and rounded once.  Two kernels, the second as a programmatic dependent
+ * launch.
+ */
+specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t row_stride,
+                               specv_dtype dtype, int B, int W, int V, int K, const float* scores,
+                               const int32_t* ended, int end_token, float* out_scores,
+                               int32_t* tokens, int32_t* beams, int32_t* status, void* workspace,
+                               size_t workspace_bytes, specv_stream_t stream);
+
+/* One state of every beam: `bytes` contiguous bytes at in + b*in_batch_stride +
+ * w*in_beam_stride, for w < W, and at out + b*out_batch_stride +
+ * k*out_beam_stride, for k < K.  Strides count bytes, are 0 or more, those of out
+ * so that no two of its places overlap. */
+typedef struct specv_state {
+  const void* in;
+  void* out;
+  int64_t in_batch_stride, in_beam_stride, out_batch_stride, out_beam_stride, bytes;
+} specv_state;
+
+/*
+ * Beam k goes on from beam beams[b,k]: out[b,k] = in[b, beams[b,k]], for each of
+ * num_states states, all in one call (hidden states, texts, rows of a page
+ * table).  beams[b,k] = -1: an empty place, out[b,k] stays as it was.
+ *   beams     [B, K] int32 in -1..W-1 (else SPECV_DEV_BAD_BEAM, and the request's
+ *             states stay as they were).
+ *   states    1..SPECV_MAX_STATES of them, on the host.  out may be in itself, with
+ *             its strides (then every old state is read before it is overwritten);
+ *             otherwise no out may overlap an in or another out.
+ * One kernel; no workspace.
+ */
+specv_status spec_reorder_beams(const int32_t* beams, int B, int W, int K, const specv_state* states,
+                                int num_states, int32_t* status, specv_stream_t stream);
 
 /*
  * The sampler without any allocation, for callers that cannot allocate

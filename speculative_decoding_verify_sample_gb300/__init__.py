@@ -10,10 +10,13 @@ status codes into exceptions.  Nothing here computes any step of the rule.
 
 from __future__ import annotations
 
-from ._native import (DEV_BAD_CACHE, DEV_BAD_DRAFT_LEN, DEV_BAD_PENALTY, DEV_BAD_ROW,
-                      DEV_BAD_TEMPERATURE, DEV_BAD_TOKEN, DEV_BAD_TREE, DEV_BAD_UNIFORM,
-                      DEV_NO_DRAFT, DEV_TIMEOUT, SPECV_BF16, SPECV_F32, SpecVerifyError, check, lib)
+from ._native import (DEV_BAD_BEAM, DEV_BAD_CACHE, DEV_BAD_DRAFT_LEN, DEV_BAD_PENALTY,
+                      DEV_BAD_POSITION, DEV_BAD_ROW, DEV_BAD_TEMPERATURE, DEV_BAD_TOKEN, DEV_BAD_TREE,
+                      DEV_BAD_UNIFORM, DEV_NO_DRAFT, DEV_TIMEOUT, SPECV_BF16, SPECV_F32,
+                      SpecVerifyError, check, lib)
+from .beams import BeamWorkspace, reorder_beams, select_beams
 from .build import build
+from .prompt import ChunkWorkspace, append_chunk, chunk_attention
 from .tree import AttentionWorkspace, append_nodes, keep_path, process_logits, tree_attention
 
 __all__ = [
@@ -24,6 +27,8 @@ __all__ = [
     "DEV_BAD_DRAFT_LEN", "DEV_BAD_TOKEN", "DEV_BAD_TEMPERATURE", "DEV_BAD_UNIFORM",
     "DEV_BAD_ROW", "DEV_NO_DRAFT", "DEV_TIMEOUT", "DEV_BAD_CACHE", "DEV_BAD_PENALTY",
     "AttentionWorkspace", "append_nodes", "tree_attention", "process_logits", "keep_path",
+    "DEV_BAD_POSITION", "DEV_BAD_BEAM", "ChunkWorkspace", "append_chunk", "chunk_attention",
+    "BeamWorkspace", "select_beams", "reorder_beams",
 ]
 
 

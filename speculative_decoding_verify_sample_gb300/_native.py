@@ -29,6 +29,8 @@ DEV_TIMEOUT = 0x40
 DEV_BAD_TREE = 0x80
 DEV_BAD_CACHE = 0x100
 DEV_BAD_PENALTY = 0x200
+DEV_BAD_POSITION = 0x400
+DEV_BAD_BEAM = 0x800
 
 MAX_NODES = 64
 MAX_HEAD_DIM = 128
@@ -73,6 +75,15 @@ SIGNATURES = {
     "spec_keep_path": (_i, [_bytes, _vp, _vp, _i, _i, _vp, _vp, _vp]),
     "spec_process_logits": (_i, [_vp, _i64, _i64, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i64, _i, _vp,
                                  _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i64, _i64, _vp, _vp]),
+    "spec_append_chunk": (_i, [_bytes, _bytes, _bytes, _bytes, _vp, _i, _i, _i, _vp, _i64, _i, _vp,
+                               _vp, _vp, _f, _vp, _i, _i, _f, _bytes, _vp, _vp]),
+    "specv_chunk_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "spec_chunk_attention": (_i, [_bytes, _bytes, _vp, _i, _i, _i, _i, _f, _f, _i, _vp, _vp, _bytes,
+                                  _vp, _vp, _sz, _vp]),
+    "specv_beam_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "spec_select_beams": (_i, [_vp, _i64, _i64, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp,
+                               _vp, _sz, _vp]),
+    "spec_reorder_beams": (_i, [_vp, _i, _i, _i, _bytes, _i, _vp, _vp]),
 }
 
 NOALLOC_SCRATCH_BYTES = 4 << 20

@@ -14,8 +14,10 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = [os.path.join(PKG_DIR, "csrc", name)
-           for name in ("specverify.cu", "cache.cu", "attention.cu", "logits.cu")]
-HEADERS = [os.path.join(INCLUDE, "specverify.h"), os.path.join(PKG_DIR, "csrc", "cache.cuh")]
+           for name in ("specverify.cu", "cache.cu", "attention.cu", "logits.cu", "beams.cu",
+                        "chunk.cu", "chunk_bf16.cu", "chunk_f16.cu")]
+HEADERS = [os.path.join(INCLUDE, "specverify.h"),
+           *(os.path.join(PKG_DIR, "csrc", name) for name in ("cache.cuh", "tensor.cuh", "chunk.cuh"))]
 LIB_PATH = os.path.join(PKG_DIR, "libspecverify.so")
 BINDING_SOURCE = os.path.join(PKG_DIR, "csrc", "binding.cpp")
 

@@ -37,7 +37,10 @@ def load():
         loader.exec_module(module)
         module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
             handle.spec_append_nodes, handle.spec_tree_attention, handle.spec_keep_path,
-            handle.spec_process_logits, handle.specv_attention_workspace_bytes)))
+            handle.spec_process_logits, handle.specv_attention_workspace_bytes,
+            handle.spec_append_chunk, handle.spec_chunk_attention,
+            handle.specv_chunk_workspace_bytes, handle.spec_select_beams,
+            handle.specv_beam_workspace_bytes, handle.spec_reorder_beams)))
         _binding = module
     return _binding
 
