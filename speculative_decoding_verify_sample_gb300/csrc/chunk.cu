@@ -1,5 +1,7 @@
 // The prompt's pass over the paged cache, host side of its attention.
 
+#include <cmath>
+
 #include "chunk.cuh"
 
 using namespace specv_chunk;
@@ -82,6 +84,21 @@ specv_status spec_chunk_attention(const specv_cache* cache, const specv_rows* q,
   if (box_rows && (!tensor_map(&k_map, cache, cache->k, box_rows) ||
                    !tensor_map(&v_map, cache, cache->v, box_rows)))
     box_rows = 0;
+  // cap tanh(z) in units of log 2 as score * poly(score^2), for |z| <= 0.6 (chunk.cuh)
+  static const double kTanh[5] = {0.9999999268676429, -0.33332309962801215, 0.13310173497792807,
+                                  -0.05210147302447307, 0.015475417666045245};
+  float poly[5] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, small = -1.0f;
+  if (cap > 0.0f) {
+    const double z = static_cast<double>(scale) / cap;
+    double power = 1.4426950408889634 * cap * z;
+    bool fits = true;
+    for (int i = 0; i < 5; i++, power *= z * z) {
+      poly[i] = static_cast<float>(kTanh[i] * power);
+      fits = fits && std::fabs(poly[i]) > 1e-35 && std::fabs(poly[i]) < 1e35;
+    }
+    // (a square of a score up to here is a number, too)
+    if (fits && 0.6 / z < 1e18) small = static_cast<float>(0.6 / z);
+  }
   const Params P{to_cache(cache),
                  to_rows(q),
                  to_rows(out),
@@ -101,7 +118,9 @@ specv_status spec_chunk_attention(const specv_cache* cache, const specv_rows* q,
                  box_rows,
                  scale * 1.4426950408889634f,
                  cap * 1.4426950408889634f,
-                 static_cast<float>(turn)};
+                 static_cast<float>(turn),
+                 small,
+                 {poly[0], poly[1], poly[2], poly[3], poly[4]}};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->dtype == SPECV_BF16 ? run<Bf16>(P, k_map, v_map, st)
                                                    : run<F16>(P, k_map, v_map, st);

@@ -36,25 +36,27 @@ using namespace specv_cache_ops;
 using namespace specv_tensor;
 
 constexpr int kKeys = 128;     // keys of a tile
+constexpr int kHalf = 64;      // and of its halves, whose scores are taken one at a time
 constexpr int kRows = 128;     // query rows of a stream
 constexpr int kRowTile = 256;  // and of an item
 static_assert(kKeys == kRows, "tiles of queries, keys and values are laid out alike");
 constexpr int kMaxCtas = kSms;
 constexpr int kMaxRequests = SPECV_MAX_CHUNK_REQUESTS;
 constexpr int kLoadWarps = 4;
-constexpr int kLoadWarp = 8;  // the first of them; the last makes the tensor copies
-constexpr int kCheckWarp = 12;
-constexpr int kScoreWarp = 13;  // issues S = Q K^T
-constexpr int kSumWarp = 14;    // issues O += P V
-constexpr int kListWarp = 15;
-constexpr int kThreads = 512;
+constexpr int kLoadWarp = 8;    // the first of them; the last makes the tensor copies
+constexpr int kScoreWarp = 12;  // two, a stream each: issue S = Q K^T
+constexpr int kSumWarp = 14;    // two: issue O += P V
+constexpr int kListWarp = 16;
+constexpr int kCheckWarp = 17;
+constexpr int kCleanWarp = 18;  // two: look at values that not every row sees
+constexpr int kThreads = 640;
 constexpr int kItems = 4;  // items listed ahead
 // What an item takes besides its key tiles, in their time: its end, and the next
 // one's first scores.
 constexpr int kItemCost = 3;
-// Registers a thread of each warpgroup: 2 * 192 + 72 + 56 = 512 = 4 * 128, what
-// the block is launched with.  The softmax keeps a row of scores in them.
-#define SPECV_CHUNK_REGS_SOFTMAX "192"
+// Registers a thread of each warpgroup: 2 * 144 + 72 + 2 * 56 <= 480 = 5 * 96, what
+// the block is launched with.  The softmax keeps half a tile's scores of a row in them.
+#define SPECV_CHUNK_REGS_SOFTMAX "144"
 #define SPECV_CHUNK_REGS_LOAD "72"
 #define SPECV_CHUNK_REGS_OTHER "56"
 constexpr float kRise = 8.0f;  // log2 of how far a maximum may rise before O is rescaled
@@ -91,6 +93,8 @@ struct Params {
   int box_rows;                       // rows that one tensor copy brings; 0: copies of 16 bytes
   float scale_log2;                   // scale log2 e
   float cap_log2, cap_turn;           // cap log2 e and 2 scale log2 e / cap; 0: no cap
+  float cap_small;                    // scores up to here take the polynomial, ...
+  float cap_poly[5];                  // in the score's square, times the score
 };
 
 // One request's place: its packed rows, its slots, the prefix that all its tokens see.
@@ -182,6 +186,20 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one)::"memory");
+  return one;
+}
+
 __device__ __forceinline__ float rcp_of(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -198,39 +216,89 @@ template <int DP> struct Shape {
   static constexpr int kTailAt = kStageAt + kStages * kTileBytes;
   static_assert(kStages * kTileBytes >= kMaxRequests * 8, "requests' units lie there at first");
 
-  // The order of an item's tiles in the ring, that of the MMAs that read them.
-  // In turn: keys a tile ahead of values, K0 K1 V0 K2 V1 .. Kn Vn-1 Vn, so that
-  // values do not wait in the ring through their tile's softmax.  A pair:
-  // K0 V0 K1 V1 ..
-  static __device__ __forceinline__ uint32_t key_job(bool pair, int i) {
-    return pair ? 2 * i : i ? 2 * i - 1 : 0;
+  // The order of an item's tiles in the ring: keys a tile ahead of values, K0 K1 V0 K2 V1 ..
+  // Kn Vn-1 Vn, as scores are taken half a tile or more ahead of the sums.
+  static __device__ __forceinline__ uint32_t key_job(int i) { return i ? 2 * i - 1 : 0; }
+  static __device__ __forceinline__ uint32_t value_job(int i, int tiles) {
+    return i == tiles - 1 ? 2 * i + 1 : 2 * i + 2;
   }
-  static __device__ __forceinline__ uint32_t value_job(bool pair, int i, int tiles) {
-    return pair || i == tiles - 1 ? 2 * i + 1 : 2 * i + 2;
-  }
-};
-
-// Tiles number t0 .. t1-1 of an item that one run has.
-struct Item {
-  int32_t b, h, row_tile, t0, t1, gap, skip, rows;  // t0 < 0: no more items
-  int32_t first, n, len, prefix;
-  int32_t pieces;  // runs that have tiles of it
-  int32_t begins;  // this is its first piece
-  int32_t bad;     // written by the checking warp
-
-  __device__ __forceinline__ int tile(int t) const { return t < gap ? t : t + skip; }
 };
 
 // Keys that some rows of an item see and others do not: behind the first row's
 // own (up to 255), and below the last row's window (as many).  A bit each.
 constexpr int kEdge = 8;
 
+// Tiles number t0 .. t1-1 of an item that one run has.  They are taken from the last
+// to the first, each from its upper half: a bias by distance is least there, so
+// maxima are found early.
+struct Item {
+  int32_t b, h, row_tile, t0, t1, gap, skip, rows;  // t0 < 0: no more items
+  int32_t first, n, len, prefix;
+  int32_t pos0, pos1, low0, low1;  // positions and lowest slots of its first and last row
+  int32_t pieces;  // runs that have tiles of it
+  int32_t begins;  // this is its first piece
+  int32_t bad;     // written by the checking warp
+  int32_t any_odd;          // some edge keys' values were not finite:
+  uint32_t odd[2 * kEdge];  // which
+};
+
+// An item's keys as a thread has them in registers.
+struct Keys {
+  int tiles, last, gap, skip, prefix, pos0, pos1, low0, low1;
+
+  __device__ __forceinline__ explicit Keys(const Item& w)
+      : tiles(w.t1 - w.t0), last(w.t1 - 1), gap(w.gap), skip(w.skip), prefix(w.prefix), pos0(w.pos0),
+        pos1(w.pos1), low0(w.low0), low1(w.low1) {}
+  // Makes them known to be the same in every lane.
+  __device__ __forceinline__ void same() {
+    for (int* x : {&tiles, &last, &gap, &skip, &prefix, &pos0, &pos1, &low0, &low1})
+      *x = __shfl_sync(kFullMask, *x, 0);
+  }
+  // The first key of the i-th tile taken.
+  __device__ __forceinline__ int first(int i) const {
+    const int t = last - i;
+    return (t < gap ? t : t + skip) * kKeys;
+  }
+  // Whether not every row sees all of these keys.
+  __device__ __forceinline__ bool mixed(int key0, int n) const {
+    return !((key0 + n <= prefix) | ((key0 >= low1) & (key0 + n - 1 <= pos0)));
+  }
+};
+
+// The halves of its tiles in which some row sees a key, in the order in which they are taken:
+// `total` of them, the first `turn` down from key `top`, the others, a prefix's, from `top2`.
+struct Halves {
+  int total, turn, top, top2;
+
+  __device__ __forceinline__ Halves(const Keys& k, int t0) {
+    const int t1 = t0 + k.tiles;
+    const int own = (k.prefix + kHalf - 1) / kHalf;  // of the prefix
+    int low = k.low0 / kHalf, high = k.pos1 / kHalf;
+    const bool joined = own > 0 && own >= low;  // the window's follow on the prefix's
+    if (joined) {
+      low = 0;
+      high = max(high, own - 1);
+    }
+    high = min(high, 2 * (t1 + k.skip) - 1);
+    turn = max(0, high - max(low, 2 * (t0 + k.skip)) + 1);
+    top = high * kHalf;
+    const int last = min(own, 2 * t1) - 1;
+    total = turn + (joined ? 0 : max(0, last - 2 * t0 + 1));
+    top2 = last * kHalf;
+  }
+  __device__ __forceinline__ int key(int i) const {
+    return i < turn ? top - i * kHalf : top2 - (i - turn) * kHalf;
+  }
+};
+
+// A stream's scores lie in two halves of its part of TMEM in turn, so that the next ones
+// are there when the softmax has done with one.
 template <int kStages> struct Tail {
-  uint64_t kv_full[kStages], kv_empty[kStages], q_full[2], q_empty[2], s_full[2], o_full[2];
-  uint64_t p_full[2][2];  // by stream and half of the keys
+  uint64_t kv_full[kStages], kv_clean[kStages], kv_empty[kStages], q_full[2], q_empty[2];
+  uint64_t s_full[2][2], p_full[2][2], o_full[2][2];  // by stream and half
   uint64_t item_full[kItems], item_checked[kItems], item_empty[kItems];
+  uint64_t joined, parted;  // both streams at the end of an item that they share
   uint64_t drained;
-  uint32_t odd[2][2 * kEdge];  // edge keys whose values were not finite, by parity of the item
   unsigned long long total;
   int gave_up;
   uint32_t tmem;
@@ -238,7 +306,47 @@ template <int kStages> struct Tail {
   float2 stats[2][kRows];
 };
 
-template <class E, int DP, bool kMod>
+// Products and sums of two in one instruction.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t twice(float x) { return pair_of(__float_as_uint(x), __float_as_uint(x)); }
+
+// Half a tile's products become capped scores in units of log 2:
+// cap tanh z, z = scale x / cap: for |z| <= 0.6 in all of the warp's rows, which scores rarely
+// leave, by z times a polynomial in z^2 (fitted to tanh(z) / z by least squares, reweighted
+// until its largest error, 2^-23.7 of the value, is about even), six instructions for two; else as
+// cap (1 - 2 / (1 + e^2z)), 2^-22 of the cap off, two of the slow functions for one.
+__device__ __forceinline__ void cap_scores(const Params& P, uint32_t (&x)[kHalf]) {
+  float most[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int e = 0; e < kHalf; e += 2)
+    most[e / 2 % 4] = fmaxf(fmaxf(most[e / 2 % 4], fabsf(__uint_as_float(x[e]))), fabsf(__uint_as_float(x[e + 1])));
+  const float all = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+  if (__all_sync(kFullMask, all <= P.cap_small)) {
+    const uint64_t k[5] = {twice(P.cap_poly[0]), twice(P.cap_poly[1]), twice(P.cap_poly[2]),
+                           twice(P.cap_poly[3]), twice(P.cap_poly[4])};
+#pragma unroll
+    for (int e = 0; e < kHalf; e += 2) {
+      const uint64_t v = pair_of(x[e], x[e + 1]), u = mul2(v, v);
+      const float2 y = halves_of(mul2(v, fma2(u, fma2(u, fma2(u, fma2(u, k[4], k[3]), k[2]), k[1]), k[0])));
+      x[e] = __float_as_uint(y.x);
+      x[e + 1] = __float_as_uint(y.y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kHalf; e++)
+      x[e] = __float_as_uint(fmaf(rcp_of(exp2_of(__uint_as_float(x[e]) * P.cap_turn) + 1.0f),
+                                  -2.0f * P.cap_log2, P.cap_log2));
+  }
+}
+
+// What is done to scores besides their scale: nothing, a cap, a bias (with or without a cap).
+enum { kPlain, kCapped, kBiased };
+
+template <class E, int DP, int kMod>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const Params P, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
@@ -259,23 +367,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kStages; i++) {
       barrier_init(smem_of(&s.kv_full[i]), P.box_rows ? 1 : 32 * kLoadWarps);
-      barrier_init(smem_of(&s.kv_empty[i]), 1);
+      barrier_init(smem_of(&s.kv_clean[i]), 2);
+      barrier_init(smem_of(&s.kv_empty[i]), 4);  // both streams' MMAs, both warps that look at it
     }
     for (int i = 0; i < 2; i++) {
       barrier_init(smem_of(&s.q_full[i]), 32 * kLoadWarps);
-      barrier_init(smem_of(&s.q_empty[i]), 1);
-      barrier_init(smem_of(&s.s_full[i]), 1);
-      barrier_init(smem_of(&s.p_full[i][0]), 4);
-      barrier_init(smem_of(&s.p_full[i][1]), 4);
-      barrier_init(smem_of(&s.o_full[i]), 1);
-      for (int k = 0; k < 2 * kEdge; k++) s.odd[i][k] = 0;
+      barrier_init(smem_of(&s.q_empty[i]), 2);
+      for (int k = 0; k < 2; k++) {
+        barrier_init(smem_of(&s.s_full[i][k]), 1);
+        barrier_init(smem_of(&s.p_full[i][k]), 4);
+        barrier_init(smem_of(&s.o_full[i][k]), 1);
+      }
     }
+    barrier_init(smem_of(&s.joined), 8);
+    barrier_init(smem_of(&s.parted), 8);
     for (int i = 0; i < kItems; i++) {
       barrier_init(smem_of(&s.item_full[i]), 1);
       barrier_init(smem_of(&s.item_checked[i]), 1);
-      barrier_init(smem_of(&s.item_empty[i]), kLoadWarps + 3 + 8);
+      barrier_init(smem_of(&s.item_empty[i]), kLoadWarps + 4 + 1 + 2 + 8);
     }
-    barrier_init(smem_of(&s.drained), 2);
+    barrier_init(smem_of(&s.drained), 4);
     s.gave_up = 0;
     s.total = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -356,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto over = [&](const Item& w) { return w.t0 < 0 || *gave_up; };
 
-  if (warp >= kLoadWarp && warp < kCheckWarp) {
+  if (warp >= kLoadWarp && warp < kLoadWarp + kLoadWarps) {
     // ------------------------------------------------------------- copies
     asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_CHUNK_REGS_LOAD ";");
     // Copies of 16 bytes, so that pages of any size and strides of any kind will
@@ -401,16 +512,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!going) break;
       // Slots that some row of the item sees; the pages of others are not followed.
-      const int at = w.row_tile * kRowTile;
-      const int low = lowest(P, w.len + at / P.group);
-      const int high = max(w.len + (at + w.rows - 1) / P.group + 1, w.prefix);
-      const int t0 = w.t0, t1 = w.t1, tiles = t1 - t0;
+      const Keys keys(w);
+      const int low = keys.low0, high = max(keys.pos1 + 1, keys.prefix), tiles = keys.tiles;
       const int32_t* table = C.page_table + static_cast<int64_t>(w.b) * C.table_stride;
       // Page numbers are read a tile ahead of their use; one out of range (its
       // request is flagged elsewhere) is no page.  Of keys key .. key+count-1, of one page:
       auto page_at = [&](int key, int count) {
         int page = -1;
-        if (key < high && (key < w.prefix || key + count > low)) page = table[key / C.page_size];
+        if (key < high && (key < keys.prefix || key + count > low)) page = table[key / C.page_size];
         return page < C.pages ? page : -1;
       };
       if (P.box_rows) {
@@ -421,11 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int per_half = kKeys / P.box_rows, boxes = per_half * (DP / 64);
           const int box = lane % per_half, half = lane / per_half;
           const int at = box * P.box_rows;
-          auto page_of = [&](int t) {
-            return t < t1 && lane < boxes ? page_at(w.tile(t) * kKeys + at, P.box_rows) : -1;
+          auto page_of = [&](int i) {
+            return i < tiles && lane < boxes ? page_at(keys.first(i) + at, P.box_rows) : -1;
           };
-          int page = page_of(t0), page_next = page_of(t0 + 1);
-          auto copy = [&](uint32_t job, const CUtensorMap* map, int page, int t) {
+          int page = page_of(0), page_next = page_of(1);
+          auto copy = [&](uint32_t job, const CUtensorMap* map, int page, int i) {
             const uint32_t stage = (jobs + job) % kStages, use = (jobs + job) / kStages;
             const uint32_t bar = smem_of(&s.kv_full[stage]);
             const int count = __popc(__ballot_sync(kFullMask, page >= 0));
@@ -436,26 +545,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (page >= 0)
               tensor_copy(base + S::kStageAt + stage * S::kTileBytes + half * (kKeys * 128) + at * 128,
-                          map, half * 64, (w.tile(t) * kKeys + at) % C.page_size, w.h, page, bar);
+                          map, half * 64, (keys.first(i) + at) % C.page_size, w.h, page, bar);
             return true;
           };
           int page_before = -1;
-          for (int t = t0; t < t1 && going; t++) {
-            const int i = t - t0;
-            going = copy(S::key_job(pair, i), &k_map, page, t);
-            if (going && pair) going = copy(S::value_job(pair, i, tiles), &v_map, page, t);
-            else if (going && i > 0) going = copy(S::value_job(pair, i - 1, tiles), &v_map, page_before, t - 1);
+          for (int i = 0; i < tiles && going; i++) {
+            going = copy(S::key_job(i), &k_map, page, i);
+            if (going && i > 0) going = copy(S::value_job(i - 1, tiles), &v_map, page_before, i - 1);
             page_before = page;
             page = page_next;
-            page_next = page_of(t + 2);
+            page_next = page_of(i + 2);
           }
-          if (going && !pair)
-            going = copy(S::value_job(pair, tiles - 1, tiles), &v_map, page_before, t1 - 1);
+          if (going) going = copy(S::value_job(tiles - 1, tiles), &v_map, page_before, tiles - 1);
         }
       } else {
-        auto key_of = [&](int t) { return w.tile(t) * kKeys + 32 * lw + lane; };
-        auto page_of = [&](int t) { return t < t1 ? page_at(key_of(t), 1) : -1; };
-        int page = page_of(t0), page_next = page_of(t0 + 1);
+        auto key_of = [&](int i) { return keys.first(i) + 32 * lw + lane; };
+        auto page_of = [&](int i) { return i < tiles ? page_at(key_of(i), 1) : -1; };
+        int page = page_of(0), page_next = page_of(1);
         auto copy = [&](uint32_t job, const uint16_t* from, int64_t off) {
           const uint32_t stage = (jobs + job) % kStages, use = (jobs + job) / kStages;
           if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.kv_empty[stage]), (use & 1) ^ 1, gave_up)))
@@ -465,20 +571,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         int64_t before = -1;
-        for (int t = t0; t < t1 && going; t++) {
-          const int i = t - t0;
+        for (int i = 0; i < tiles && going; i++) {
           const int64_t off = page < 0 ? static_cast<int64_t>(-1)
                                        : page * C.page_stride +
-                                             key_of(t) % C.page_size * C.row_stride +
+                                             key_of(i) % C.page_size * C.row_stride +
                                              w.h * C.head_stride;
           page = page_next;
-          page_next = page_of(t + 2);
-          going = copy(S::key_job(pair, i), C.k, off);
-          if (going && pair) going = copy(S::value_job(pair, i, tiles), C.v, off);
-          else if (going && i > 0) going = copy(S::value_job(pair, i - 1, tiles), C.v, before);
+          page_next = page_of(i + 2);
+          going = copy(S::key_job(i), C.k, off);
+          if (going && i > 0) going = copy(S::value_job(i - 1, tiles), C.v, before);
           before = off;
         }
-        if (going && !pair) going = copy(S::value_job(pair, tiles - 1, tiles), C.v, before);
+        if (going) going = copy(S::value_job(tiles - 1, tiles), C.v, before);
       }
       if (!going) break;
       jobs += 2 * tiles;
@@ -495,115 +599,110 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (now_ns() - start < 100000) {
       }
     }
-  } else if (warp >= kCheckWarp) {
+  } else if (warp >= kScoreWarp && warp < kScoreWarp + 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_CHUNK_REGS_OTHER ";");
     // --------------------------------------------------------------- MMAs
     constexpr uint32_t kType = std::is_same<E, Bf16>::value ? 1 : 0;
     constexpr uint32_t kIdesc = 1u << 4 | kType << 7 | kType << 10 | (kRows >> 4) << 24;
-    constexpr uint32_t kIdescS = kIdesc | (kKeys >> 3) << 17;
-    // Two threads, that neither waits for what the other issues: scores of a tile
-    // when its stream's last sum has left S, sums when the weights are there.
-    auto stage_at = [&](uint32_t job) { return base + S::kStageAt + job % kStages * S::kTileBytes; };
-    auto kv_wait = [&](uint32_t job) {
-      const bool there = barrier_wait(smem_of(&s.kv_full[job % kStages]), job / kStages & 1, gave_up);
-      // copies of 16 bytes wrote through the generic proxy, the MMA reads through the other
-      if (!P.box_rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      return there;
-    };
-    uint32_t jobs = 0;            // copies before this item
-    uint32_t issued[2] = {0, 0};  // scores or sums of each stream so far
+    constexpr uint32_t kIdescS = kIdesc | (kHalf >> 3) << 17;
+    // Two threads a stream, that neither waits for what the other issues: scores of half a
+    // tile when the sum over its stream's last but one has left its place, sums when the
+    // weights are there.
+    // (A whole warp goes through the loops, on values that the compiler knows to be the same in
+    // every lane, and one lane issues: so descriptors are in uniform registers, where a lane
+    // by itself would move each there, 100 cycles an MMA.)
+    const bool scores = __shfl_sync(kFullMask, warp, 0) < kSumWarp;
+    const int st = __shfl_sync(kFullMask, warp, 0) & 1;
     const int steps = (C.head_dim + 15) / 16;
-    if (warp == kScoreWarp && lane == 0) {
-      uint32_t queries = 0;
-      auto scores = [&](int st, uint32_t q_at, uint32_t k_at) {
-        if (issued[st] && !barrier_wait(smem_of(&s.o_full[st]), (issued[st] - 1) & 1, gave_up)) return false;
-        tmem_fence_after();
-        const uint32_t a = operand_low(q_at, 16), b = operand_low(k_at, 16);
-        mma_ss<false>(tS[st], a, b, kIdescS);
-#pragma unroll
-        for (int k = 1; k < DP / 16; k++) {
-          const uint32_t step = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;  // of both
-          if (k < steps) mma_ss<true>(tS[st], a + step, b + step, kIdescS);
-        }
-        mma_commit(smem_of(&s.s_full[st]));
-        issued[st]++;
-        return true;
-      };
-      while (true) {
-        const Item& w = next_item();
-        if (over(w)) break;
-        const bool pair = w.rows > kRows;
-        const int tiles = w.t1 - w.t0;
-        done_item();
-        bool going = true;
-        uint32_t q_at[2];
-        for (int half = 0; half < (pair ? 2 : 1) && going; half++) {
-          const uint32_t buffer = (queries + half) & 1;
-          going = barrier_wait(smem_of(&s.q_full[buffer]), (queries + half) / 2 & 1, gave_up);
-          q_at[half] = base + buffer * S::kQueryBytes;
-        }
+    const uint32_t idesc_sum = kIdesc | 1u << 16 | static_cast<uint32_t>(2 * steps) << 17;
+    const uint32_t tm = __shfl_sync(kFullMask, tmem, 0);
+    const uint32_t out = tm + 256 + st * DP, place0 = tm + st * 128;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(kFullMask, barrier_wait(smem_of(bar), parity, gave_up)) != 0;
+    };
+    uint32_t jobs = 0;     // copies before this item
+    uint32_t issued = 0;   // halves so far
+    uint32_t queries = 0;  // tiles of queries before this item
+    while (true) {
+      const Item& w = next_item();
+      if (__any_sync(kFullMask, over(w))) break;
+      Keys keys(w);
+      keys.same();
+      const Halves halves(keys, __shfl_sync(kFullMask, w.t0, 0));
+      const bool pair = __shfl_sync(kFullMask, w.rows, 0) > kRows;
+      __syncwarp();
+      done_item();
+      bool going = true, first = true;
+      uint32_t q_at = base;
+      if (scores) {
+          const uint32_t tile = queries + (pair ? st : 0);
+          going = wait(&s.q_full[tile & 1], tile / 2 & 1);
+          q_at += (tile & 1) * S::kQueryBytes;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        for (int i = 0; i < tiles && going; i++) {
-          const uint32_t job = jobs + S::key_job(pair, i);
-          going = kv_wait(job);
-          if (pair) {
-            going = going && scores(0, q_at[0], stage_at(job));
-            going = going && scores(1, q_at[1], stage_at(job));
-          } else {
-            going = going && scores(i & 1, q_at[0], stage_at(job));
-          }
-          if (going) mma_commit(smem_of(&s.kv_empty[job % kStages]));
-        }
-        if (!going) break;
-        jobs += 2 * tiles;
-        for (int half = 0; half < (pair ? 2 : 1); half++, queries++)
-          mma_commit(smem_of(&s.q_empty[queries & 1]));
       }
-      // every MMA and every arrival that waits for one must find this CTA's memory
-      mma_commit(smem_of(&s.drained));
-      barrier_wait_own(smem_of(&s.drained), 0);
+      uint32_t stage = 0, stage_at = 0;
+      int tile = -1, tiles = 0;
+      for (int i = 0; i < halves.total; i++) {
+        const int key0 = halves.key(i);
+        if (key0 / kKeys != tile) {  // the next tile
+          if (tiles && elect_one()) mma_commit(smem_of(&s.kv_empty[stage]));
+          __syncwarp();
+          tile = key0 / kKeys;
+          const uint32_t job = jobs + (scores ? S::key_job(tiles) : S::value_job(tiles, keys.tiles));
+          tiles++;
+          stage = job % kStages;
+          stage_at = base + S::kStageAt + stage * S::kTileBytes;
+          going = wait(scores ? &s.kv_full[stage] : &s.kv_clean[stage], job / kStages & 1);
+          if (!going) break;
+          // copies of 16 bytes wrote through the generic proxy, the MMA reads through the other
+          if (!P.box_rows) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (!pair && (i & 1) != st) continue;  // (of one row tile the streams take halves in turn)
+        const uint32_t place = issued & 1, use = issued / 2;
+        const uint32_t at = place0 + place * kHalf, from = stage_at + (key0 & kHalf) * 128;
+        going = scores ? wait(&s.o_full[st][place], (use & 1) ^ 1) : wait(&s.p_full[st][place], use & 1);
+        if (!going) break;
+        tmem_fence_after();
+        if (scores) {
+          const uint32_t a = operand_low(q_at, 16), b = operand_low(from, 16);
+          if (elect_one()) {
+            mma_ss<false>(at, a, b, kIdescS);
+#pragma unroll
+            for (int k = 1; k < DP / 16; k++) {
+              const uint32_t step = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;  // of both
+              if (k < steps) mma_ss<true>(at, a + step, b + step, kIdescS);
+            }
+            mma_commit(smem_of(&s.s_full[st][place]));
+          }
+        } else {
+          const uint32_t b = operand_low(from, kKeys * 128);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kHalf / 16; k++)
+              mma_ts(out, at + 8 * k, b + (k * 2048 >> 4), idesc_sum, k > 0 || !first);
+            mma_commit(smem_of(&s.o_full[st][place]));
+          }
+          first = false;
+        }
+        __syncwarp();
+        issued++;
+      }
+      if (!going) break;
+      if (elect_one()) mma_commit(smem_of(&s.kv_empty[stage]));
+      __syncwarp();
+      jobs += 2 * keys.tiles;
+      for (int half = 0; half < (pair ? 2 : 1); half++, queries++)
+        if (scores && elect_one()) mma_commit(smem_of(&s.q_empty[queries & 1]));
+      __syncwarp();
     }
-    if (warp == kSumWarp && lane == 0) {
-      const uint32_t idesc = kIdesc | 1u << 16 | static_cast<uint32_t>(2 * steps) << 17;
-      auto sums = [&](int st, uint32_t v_at, bool first) {
-        const uint32_t b = operand_low(v_at, kKeys * 128);
-#pragma unroll
-        for (int half = 0; half < 2; half++) {
-          if (!barrier_wait(smem_of(&s.p_full[st][half]), issued[st] & 1, gave_up)) return false;
-          tmem_fence_after();
-#pragma unroll
-          for (int k = half * kKeys / 32; k < (half + 1) * kKeys / 32; k++)
-            mma_ts(tO[st], tS[st] + 8 * k, b + (k * 2048 >> 4), idesc, k > 0 || !first);
-        }
-        mma_commit(smem_of(&s.o_full[st]));
-        issued[st]++;
-        return true;
-      };
-      while (true) {
-        const Item& w = next_item();
-        if (over(w)) break;
-        const bool pair = w.rows > kRows;
-        const int tiles = w.t1 - w.t0;
-        done_item();
-        bool going = true;
-        for (int i = 0; i < tiles && going; i++) {
-          const uint32_t job = jobs + S::value_job(pair, i, tiles);
-          going = kv_wait(job);
-          if (pair) {
-            going = going && sums(0, stage_at(job), i == 0);
-            going = going && sums(1, stage_at(job), i == 0);
-          } else {
-            going = going && sums(i & 1, stage_at(job), i < 2);
-          }
-          if (going) mma_commit(smem_of(&s.kv_empty[job % kStages]));
-        }
-        if (!going) break;
-        jobs += 2 * tiles;
-      }
+    // every MMA and every arrival that waits for one must find this CTA's memory
+    if (elect_one()) {
       mma_commit(smem_of(&s.drained));
       barrier_wait_own(smem_of(&s.drained), 0);
     }
     __syncwarp();
+  } else if (warp >= kListWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 " SPECV_CHUNK_REGS_OTHER ";");
     // ------------------------------------------------------------ listing
     if (warp == kListWarp) {
       int b = list_b;
@@ -674,7 +773,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             const int pieces = last_run - first_run + 1;
             s.items[slot] = Item{b, h, row_tile, t0, t1, span.gap, span.skip, span.rows, r.first, r.n,
-                                 r.len, r.prefix, pieces, t0 == 0, 0};
+                                 r.len, r.prefix, span.pos0, span.pos1, lowest(P, span.pos0),
+                                 lowest(P, span.pos1), pieces, t0 == 0, 0, 0, {}};
             if (begins && t0 > 0 && first_run == run - 1)
               P.ws.cuts[run] = Cut{b, h, row_tile, span.rows, r.first, pieces, 0, 0};
           }
@@ -745,218 +845,246 @@ __global__ void __launch_bounds__(kThreads, 1)
         done_item();
       }
     }
+    // ------------------------------------------------- values not all rows see
+    // A value that is not finite would pass through a weight of 0 into rows that do
+    // not see its key: it becomes 0 here and comes back, at the end, for those that do.
+    // (And what lies where nobody sees a key is whatever was there.)
+    if (warp >= kCleanWarp) {
+      uint32_t jobs = 0;
+      auto pass = [&](uint32_t job, auto clean) {
+        const uint32_t stage = job % kStages;
+        if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.kv_full[stage]), job / kStages & 1, gave_up)))
+          return false;
+        clean(smem + S::kStageAt + stage * S::kTileBytes);
+        __syncwarp();
+        if (lane == 0) {
+          barrier_arrive(smem_of(&s.kv_clean[stage]));
+          barrier_arrive(smem_of(&s.kv_empty[stage]));
+        }
+        return true;
+      };
+      auto look = [](char*) {};
+      while (true) {
+        Item& w = const_cast<Item&>(next_item());
+        if (__any_sync(kFullMask, over(w))) break;
+        const Keys keys(w);
+        bool going = true;
+        auto values = [&](int i) {
+          const int tile_key = keys.first(i);
+          return pass(jobs + S::value_job(i, keys.tiles), [&](char* v) {
+            if (!keys.mixed(tile_key, kKeys)) return;
+            constexpr int kPieces = DP / 8;  // of a row
+            const int me = (warp - kCleanWarp) * 32 + lane, piece = me % kPieces;
+            char* const column = v + (piece / 8) * (kKeys * 128) + (piece % 8) * 16;
+            // rows [from, to) of the tile, as keys; those below the prefix are seen by all
+            auto rows = [&](int from, int to, auto each) {
+              const int last = min(to - tile_key, kKeys);
+              for (int r = max(max(from, keys.prefix) - tile_key, 0) + me / kPieces; r < last; r += 64 / kPieces)
+                each(r, reinterpret_cast<uint4*>(column + r * 128));
+            };
+            auto clear = [](int, uint4* place) { *place = make_uint4(0, 0, 0, 0); };
+            auto check = [&](int r, uint4* place) {
+              // the exponent's bits, and one of its lowest more: the top bit where all are set
+              constexpr uint32_t kBits = kExp * 0x10001u, kLowest = (kExp & (0u - kExp)) * 0x10001u;
+              uint4 x = *place;
+              uint32_t* words = &x.x;
+              uint32_t odd[4];
+#pragma unroll
+              for (int i = 0; i < 4; i++) odd[i] = ((words[i] & kBits) + kLowest) & 0x80008000u;
+              if (!(odd[0] | odd[1] | odd[2] | odd[3])) return;
+#pragma unroll
+              for (int i = 0; i < 4; i++) words[i] &= ~((odd[i] >> 15) * 0xffffu);
+              *place = x;
+              const int key = tile_key + r;
+              const int bit = key > keys.pos0 ? key - keys.pos0 - 1 : 32 * kEdge + key - keys.low0;
+              atomicOr(w.odd + bit / 32, 1u << bit % 32);
+              w.any_odd = 1;
+            };
+            rows(tile_key, keys.low0, clear);  // nobody sees them
+            rows(keys.low0, min(keys.low1, keys.pos0 + 1), check);
+            rows(max(keys.low0, keys.pos0 + 1), keys.pos1 + 1, check);
+            rows(keys.pos1 + 1, tile_key + kKeys, clear);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          });
+        };
+        for (int i = 0; i < keys.tiles && going; i++) {
+          going = pass(jobs + S::key_job(i), look);
+          if (going && i > 0) going = values(i - 1);
+        }
+        if (going) going = values(keys.tiles - 1);
+        if (!going) break;
+        jobs += 2 * keys.tiles;
+        __syncwarp();
+        done_item();
+      }
+    }
   } else {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 " SPECV_CHUNK_REGS_SOFTMAX ";");
     const int st = warp / 4, quarter = warp % 4;
     const int row = quarter * 32 + lane;  // of the stream's tile
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const float c = P.scale_log2;
-    uint32_t jobs = 0, scored = 0;  // scored: tiles of this stream so far
+    uint32_t scored = 0;  // halves of tiles of this stream so far
+    uint32_t shared = 0;            // items that both streams had parts of
     while (true) {
-      const uint32_t item = items;
-      const Item& given = next_item();
-      if (any_of_softmax(over(given))) break;  // all leave together
-      const Item w = given;
+      Item& w = const_cast<Item&>(next_item());
+      if (__any_sync(kFullMask, over(w))) break;
       const bool pair = w.rows > kRows;
-      const int first_row = pair ? st * kRows : 0;
-      const bool working = first_row + quarter * 32 < w.rows;  // this warp has rows
-      const int item_row = w.row_tile * kRowTile;
-      const int at = item_row + min(first_row + row, w.rows - 1);
+      const int first_row = pair ? st * kRows : 0, rows = w.rows;
+      const bool working = first_row + quarter * 32 < rows;  // this warp has rows
+      const int at = w.row_tile * kRowTile + min(first_row + row, rows - 1);
       const int token = at / P.group, g = at - token * P.group;
       // slots that this row sees: below the prefix, and low .. pos
-      const int pos = w.len + token, low = lowest(P, pos);
-      // and of the item's first and last row
-      const int pos0 = w.len + item_row / P.group;
-      const int pos1 = w.len + (item_row + w.rows - 1) / P.group;
-      const int low0 = lowest(P, pos0), low1 = lowest(P, pos1);
+      const Keys keys(w);
+      const int pos = w.len + token, low = lowest(P, pos), prefix = keys.prefix;
       const float slope = kMod && P.slopes ? P.slopes[w.h * P.group + g] * 1.4426950408889634f : 0.0f;
-      uint32_t* odd = s.odd[item & 1];
-      int taken[2] = {0, 0};  // tiles of this item that each stream took
+      int taken = 0;  // halves of this item that this stream took
       float m = -INFINITY, l = 0.0f;  // m: the maximum that O and l were taken with
 
-      for (int t = w.t0; t < w.t1; t++) {
-        if (pair) {
-          taken[0]++;
-          taken[1]++;
-        } else {
-          // by the item's own count, so that a row's sums do not depend on what ran before
-          taken[(t - w.t0) & 1]++;
-          if (((t - w.t0) & 1) != st) continue;
-        }
-        if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.s_full[st]), scored & 1, gave_up))) break;
-        const int key0 = w.tile(t) * kKeys;
-        // holds keys that not every row sees
-        const bool mixed = !(key0 + kKeys <= w.prefix || (key0 >= low1 && key0 + kKeys - 1 <= pos0));
-        if (mixed && (!pair || st == 0)) {
-          // (Only now that the scores are there: a wait tells phases apart by their parity,
-          // so the copy before this one in the same stage must be known to have landed.)
-          // A value that is not finite would pass through a weight of 0 into rows that do
-          // not see its key: it becomes 0 here and comes back, at the end, for those that do.
-          // (And what lies where nobody sees a key is whatever was there.)
-          const uint32_t job = jobs + S::value_job(pair, t - w.t0, w.t1 - w.t0), stage = job % kStages;
-          if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.kv_full[stage]), job / kStages & 1, gave_up)))
-            break;
-          char* v = smem + S::kStageAt + stage * S::kTileBytes;
-          bool changed = false;
-          for (int e = quarter * 32 + lane; e < kKeys * (DP / 8); e += 128) {
-            const int r = e / (DP / 8), p = e % (DP / 8), key = key0 + r;
-            if (key < w.prefix || (key >= low1 && key <= pos0)) continue;  // all rows see it
-            uint4* place = reinterpret_cast<uint4*>(v + (p / 8) * (kKeys * 128) + r * 128 + (p % 8) * 16);
-            if (key > pos1 || key < low0) {  // nobody does
-              *place = make_uint4(0, 0, 0, 0);
-              changed = true;
-              continue;
-            }
-            uint4 x = *place;
-            uint32_t* words = &x.x;
-            bool found = false;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-              if ((words[i] & kExp) == kExp) words[i] &= 0xffff0000u, found = true;
-              if ((words[i] >> 16 & kExp) == kExp) words[i] &= 0xffffu, found = true;
-            }
-            if (found) {
-              *place = x;
-              const int bit = key > pos0 ? key - pos0 - 1 : 32 * kEdge + key - low0;
-              atomicOr(odd + bit / 32, 1u << bit % 32);
-              changed = true;
-            }
-          }
-          if (changed) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        __syncwarp();
+      const Halves halves(keys, w.t0);
+#pragma unroll 1
+      for (int i = pair ? 0 : st; i < halves.total; i += pair ? 1 : 2) {
+        // (of an item of one row tile the streams take halves in turn)
+        const int key0 = halves.key(i);
+        const uint32_t place = scored & 1, use = scored / 2;
+        if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.s_full[st][place]), use & 1, gave_up))) break;
         tmem_fence_after();
-        const bool first = taken[st] == 1;
+        const bool first = taken++ == 0;
         if (working) {
-          uint32_t x[kKeys];
-          tmem_load128(tS[st] + lanes, x);
-          if (kMod) {
-            if (P.cap_log2 > 0.0f) {
-              // cap tanh z = cap (1 - 2 / (1 + e^2z)): 2^-22 of the cap off, whatever z is
-#pragma unroll
-              for (int e = 0; e < kKeys; e++)
-                x[e] = __float_as_uint(fmaf(
-                    rcp_of(exp2_of(__uint_as_float(x[e]) * P.cap_turn) + 1.0f), -2.0f * P.cap_log2, P.cap_log2));
+          const uint32_t at_s = tS[st] + lanes + place * kHalf;
+          uint32_t x[kHalf];
+          tmem_load64(at_s, x);
+          // A score is mult x + base + step e in units of log 2, for the half's e-th key.
+          float mult = P.scale_log2, base = 0.0f, step = 0.0f;
+          if (kMod && P.cap_log2 > 0.0f) {
+            cap_scores(P, x);
+            mult = 1.0f;
+          }
+          if (kMod == kBiased) {
+            if (key0 + kHalf - 1 <= keys.pos0) {  // no key is in front of a row
+              base = slope * static_cast<float>(key0 - pos);
+              step = slope;
             } else {
 #pragma unroll
-              for (int e = 0; e < kKeys; e++) x[e] = __float_as_uint(__uint_as_float(x[e]) * c);
-            }
-            if (P.slopes) {
-              const float from = static_cast<float>(key0 - pos);
-#pragma unroll
-              for (int e = 0; e < kKeys; e++)
-                x[e] = __float_as_uint(fmaf(-slope, fabsf(from + e), __uint_as_float(x[e])));
+              for (int e = 0; e < kHalf; e++)
+                x[e] = __float_as_uint(fmaf(-slope, fabsf(static_cast<float>(key0 - pos + e)),
+                                            __uint_as_float(x[e]) * mult));
+              mult = 1.0f;
             }
           }
-          if (mixed) {
+          if (keys.mixed(key0, kHalf)) {
 #pragma unroll
-            for (int k = 0; k < kKeys; k += 32) {
+            for (int k = 0; k < kHalf; k += 32) {
               const int from = key0 + k;
               const uint32_t seen =
-                  bits_below(w.prefix - from) | (bits_below(pos + 1 - from) & ~bits_below(low - from));
+                  bits_below(prefix - from) | (bits_below(pos + 1 - from) & ~bits_below(low - from));
 #pragma unroll
               for (int e = 0; e < 32; e++)
                 if (!(seen >> e & 1)) x[k + e] = 0xff800000u;  // -inf
             }
           }
-          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < kKeys; e += 8)
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-              tops[k] = fmaxf(fmaxf(tops[k], __uint_as_float(x[e + 2 * k])),
-                              __uint_as_float(x[e + 2 * k + 1]));
-          float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-          if (!kMod) top *= c;
-          const bool rise = first || top > m + kRise;
-          float by = 1.0f;
-          if (rise) {
-            const float higher = fmaxf(m, top);
-            by = higher == -INFINITY ? 1.0f : exp2_of(m - higher);
-            m = higher;
-          }
-          if (!first && __any_sync(kFullMask, rise)) {
-            // the last update of O must be done
-            if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.o_full[st]), (scored - 1) & 1, gave_up)))
-              break;
-            tmem_fence_after();
-            l *= by;
+          // The weights with the maximum so far, beside the half's own: where that is too much
+          // above it, once more.
+          const uint64_t mult2 = twice(mult);
+          uint32_t p[kHalf / 2];
+          float sum;
+          bool again = false;
 #pragma unroll 1
-            for (int k = 0; k < DP; k += 16) {
-              uint32_t o[16];
-              tmem_load16(tO[st] + lanes + k, o);
+          while (true) {
+            const float shift = kLift - (m == -INFINITY ? 0.0f : m);
+            const float from = base + shift;
+            const uint64_t shift2 = twice(shift);
+            uint64_t sums[2] = {0, 0};
+            float tops[4];
 #pragma unroll
-              for (int e = 0; e < 16; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
-              tmem_store16(tO[st] + lanes + k, o);
-            }
-          }
-          const float shift = kLift - (m == -INFINITY ? 0.0f : m);
-          const uint64_t c2 = pair_of(__float_as_uint(c), __float_as_uint(c));
-          const uint64_t shift2 = pair_of(__float_as_uint(shift), __float_as_uint(shift));
-          uint64_t sums[2] = {0, 0};
-#pragma unroll
-          for (int k = 0; k < kKeys; k += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const uint64_t xs = pair_of(x[k + e], x[k + e + 1]);
-              const float2 y = halves_of(kMod ? add2(xs, shift2) : fma2(xs, c2, shift2));
+            for (int e = 0; e < kHalf; e += 2) {
+              const uint64_t xs = pair_of(x[e], x[e + 1]);
+              uint64_t y2;
+              if (kMod == kPlain) {
+                y2 = fma2(xs, mult2, shift2);
+              } else if (kMod == kCapped) {
+                y2 = add2(xs, shift2);
+              } else {
+                const float lo = fmaf(step, static_cast<float>(e), from), hi = fmaf(step, static_cast<float>(e + 1), from);
+                y2 = fma2(xs, mult2, pair_of(__float_as_uint(lo), __float_as_uint(hi)));
+              }
+              const float2 y = halves_of(y2);
               const float a = exp2_of(y.x), b = exp2_of(y.y);
-              sums[e / 2 % 2] =
-                  add2(sums[e / 2 % 2], pair_of(__float_as_uint(a), __float_as_uint(b)));
+              // (the largest of what costs least to have: products, or scores less the shift)
+              const float u = kMod == kBiased ? y.x : __uint_as_float(x[e]);
+              const float v = kMod == kBiased ? y.y : __uint_as_float(x[e + 1]);
+              tops[e / 2 % 4] = e < 8 ? fmaxf(u, v) : max3(tops[e / 2 % 4], u, v);
+              sums[e / 2 % 2] = add2(sums[e / 2 % 2], pair_of(__float_as_uint(a), __float_as_uint(b)));
               // the weights' one rounding, to the type of the values they meet: the MMA takes
               // both operands in one 16-bit type.  (The sum has them as they are.)
               p[e / 2] = E::pack(a, b);
             }
-            tmem_store16(tS[st] + lanes + k / 2, p);  // over scores of this row, all read
-            if (k == kKeys / 2 - 32) {  // half of the keys can be summed up
-              tmem_store_wait();
-              tmem_fence_before();
-              __syncwarp();
-              if (lane == 0) barrier_arrive(smem_of(&s.p_full[st][0]));
+            const float2 both = halves_of(add2(sums[0], sums[1]));
+            sum = both.x + both.y;
+            float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+            if (kMod == kPlain) top *= mult;
+            if (kMod == kBiased) top -= shift;
+            const bool rise = first || top > m + kRise;
+            if (again || !__any_sync(kFullMask, rise)) break;
+            again = true;
+            float by = 1.0f;
+            if (rise) {
+              const float higher = fmaxf(m, top);
+              by = higher == -INFINITY ? 1.0f : exp2_of(m - higher);
+              m = higher;
+            }
+            if (!first) {
+              // the last update of O must be done
+              const uint32_t last = scored - 1;
+              if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.o_full[st][last & 1]), last / 2 & 1, gave_up)))
+                break;
+              tmem_fence_after();
+              l *= by;
+#pragma unroll 1
+              for (int k = 0; k < DP; k += 16) {
+                uint32_t o[16];
+                tmem_load16(tO[st] + lanes + k, o);
+#pragma unroll
+                for (int e = 0; e < 16; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                tmem_store16(tO[st] + lanes + k, o);
+              }
             }
           }
-          const float2 sum = halves_of(add2(sums[0], sums[1]));
-          l += sum.x + sum.y;
+          l += sum;
+          tmem_store32(at_s, p);  // over scores of this row, all read
           tmem_store_wait();
-        } else if (lane == 0) {
-          barrier_arrive(smem_of(&s.p_full[st][0]));
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) barrier_arrive(smem_of(&s.p_full[st][1]));
+        if (lane == 0) barrier_arrive(smem_of(&s.p_full[st][place]));
         scored++;
       }
 
-      jobs += 2 * (w.t1 - w.t0);
-
-      // The item's end: this stream's last sum, and by the barrier the other's too.
-      if (taken[st]) barrier_wait(smem_of(&s.o_full[st]), (scored - 1) & 1, gave_up);
-      s.stats[st][row] = make_float2(m, l);
-      tmem_fence_before();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      tmem_fence_after();
-      uint32_t odd_rows[2 * kEdge];
-      bool fix = false;
-#pragma unroll
-      for (int k = 0; k < 2 * kEdge; k++) {
-        odd_rows[k] = odd[k];
-        fix |= odd_rows[k] != 0;
+      // The item's end: this stream's last sum, and where both have parts of the rows the
+      // other's too.
+      if (taken) {
+        const uint32_t last = scored - 1;
+        barrier_wait(smem_of(&s.o_full[st][last & 1]), last / 2 & 1, gave_up);
       }
-      const float2 other = s.stats[st ^ 1][row];
-      if (tid < 2 * kEdge) s.odd[(item & 1) ^ 1][tid] = 0;
+      int other_taken = 0;
+      float2 other = make_float2(-INFINITY, 0.0f);
+      if (!pair) {
+        s.stats[st][row] = make_float2(m, taken ? l : -1.0f);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) barrier_arrive(smem_of(&s.joined));
+        barrier_wait(smem_of(&s.joined), shared & 1, gave_up);
+        other = s.stats[st ^ 1][row];
+        other_taken = other.y >= 0.0f || other.y != other.y;
+      }
+      tmem_fence_after();
       barrier_wait(smem_of(&s.item_checked[items % kItems]), items / kItems & 1, gave_up);
-      const bool bad = __any_sync(kFullMask, given.bad != 0 || *gave_up);  // unchecked is bad
-      // Only a checked request's pages are followed.  (Of a flagged one a box may not have
-      // been copied, and what its place in the ring held before may look like such values.)
-      fix = fix && !bad;
-      __syncwarp();
-      done_item();
+      const bool bad = __any_sync(kFullMask, w.bad != 0 || *gave_up);  // unchecked is bad
       // A pair: this stream's rows, all columns; else half of the columns of both streams' sum
-      const int my_rows = w.rows - first_row;
+      const int my_rows = rows - first_row;
       if (quarter * 32 < my_rows && !(bad && !w.begins)) {
         float weight[2] = {1.0f, 1.0f};
+        const bool took[2] = {st && !pair ? other_taken != 0 : taken != 0, st || pair ? taken != 0 : other_taken != 0};
         if (!pair) {
           const float m_of[2] = {st ? other.x : m, st ? m : other.x};
           const float l_of[2] = {st ? other.y : l, st ? l : other.y};
@@ -964,87 +1092,101 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = 0.0f;
 #pragma unroll
           for (int k = 0; k < 2; k++) {
-            weight[k] = !taken[k] ? 0.0f : m_of[k] == m ? 1.0f : exp2_of(m_of[k] - m);
-            l += weight[k] * l_of[k];
+            weight[k] = !took[k] ? 0.0f : m_of[k] == m ? 1.0f : exp2_of(m_of[k] - m);
+            if (took[k]) l += weight[k] * l_of[k];
           }
         }
+        // (The code of an item's end is short on purpose: it is fetched anew for each.)
         const bool whole = w.pieces == 1 || bad;  // of a flagged request the first piece clears the rows
-        const float inv = 1.0f / l;
         const bool mine = row < my_rows;
-        uint16_t* out = P.out.data + (w.first + static_cast<int64_t>(token)) * P.out.node_stride +
-                        (w.h * P.group + g) * P.out.head_stride;
+        uint16_t* const out = P.out.data + (w.first + static_cast<int64_t>(token)) * P.out.node_stride +
+                              (w.h * P.group + g) * P.out.head_stride;
         const int64_t slot = 2 * static_cast<int>(blockIdx.x) + w.begins;
-        float4* part = P.ws.parts + slot * (DP / 4) * P.part_rows + first_row + row;
+        float4* const part = P.ws.parts + slot * (DP / 4) * P.part_rows + first_row + row;
         const int cols = pair ? DP : DP / 2, col0 = pair ? 0 : st * cols;
+        const float inv = whole ? 1.0f / l : 1.0f;
+        const int own = lane & 3;
+        uint16_t* to[4];  // rows of lanes ^ 0 .. 3
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+          to[r] = reinterpret_cast<uint16_t*>(
+              __shfl_xor_sync(kFullMask, reinterpret_cast<uint64_t>(mine ? out : nullptr), r));
 #pragma unroll 1
-        for (int k = 0; k < cols; k += 32) {
+        for (int k = col0; k < col0 + cols; k += 32) {
           float o[32];
-          uint32_t x[32];
-          if (pair) {
-            tmem_load32(tO[st] + lanes + k, x);
 #pragma unroll
-            for (int e = 0; e < 32; e++) o[e] = __uint_as_float(x[e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; e++) o[e] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-              if (taken[i]) {
-                tmem_load32(tO[i] + lanes + col0 + k, x);
-#pragma unroll
-                for (int e = 0; e < 32; e++) o[e] = fmaf(__uint_as_float(x[e]), weight[i], o[e]);
-              }
-          }
-          if (mine && fix) {
+          for (int e = 0; e < 32; e++) o[e] = 0.0f;
 #pragma unroll 1
-            for (int word = 0; word < 2 * kEdge; word++) {
-              uint32_t left = 0;
+          for (int i = pair ? st : 0; i <= (pair ? st : 1); i++) {
+            uint32_t x[32];
+            if (!(i ? took[1] : took[0])) continue;
+            const float by = (i ? weight[1] : weight[0]) * inv;
+            tmem_load32(tmem + 256 + i * DP + lanes + k, x);
 #pragma unroll
-              for (int i = 0; i < 2 * kEdge; i++)
-                if (i == word) left = odd_rows[i];
-              for (; left; left &= left - 1) {
-                const int bit = 32 * word + __ffs(left) - 1;
-                const int key = bit < 32 * kEdge ? pos0 + 1 + bit : low0 + bit - 32 * kEdge;
-                if (key > pos || key < low) continue;
-                const uint16_t* v = C.v + C.slot(w.b, key) + w.h * C.head_stride;
-#pragma unroll
-                for (int e = 0; e < 32; e++) {
-                  const int d = col0 + k + e;
-                  if (d >= C.head_dim) continue;
-                  const uint32_t bits = v[d];
-                  if ((bits & kExp) == kExp) o[e] += E::unpack(bits).x;
-                }
-              }
-            }
+            for (int e = 0; e < 32; e++) o[e] = fmaf(__uint_as_float(x[e]), by, o[e]);
           }
-          if (mine && whole) {
-            if (bad)
-#pragma unroll
-              for (int e = 0; e < 32; e++) o[e] = 0.0f;
-            const float by = bad ? 0.0f : inv;
+          if (whole) {
+            uint4 v[4];
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
-              const int d = col0 + k + e;
-              if (d < C.head_dim)
-                *reinterpret_cast<uint4*>(out + d) =
-                    make_uint4(E::pack(o[e] * by, o[e + 1] * by),
-                               E::pack(o[e + 2] * by, o[e + 3] * by),
-                               E::pack(o[e + 4] * by, o[e + 5] * by),
-                               E::pack(o[e + 6] * by, o[e + 7] * by));
+              v[e / 8] = make_uint4(E::pack(o[e], o[e + 1]), E::pack(o[e + 2], o[e + 3]),
+                                    E::pack(o[e + 4], o[e + 5]), E::pack(o[e + 6], o[e + 7]));
+              if (bad) v[e / 8] = make_uint4(0, 0, 0, 0);
+            }
+            // Four lanes have four pieces of 16 bytes of four rows: each takes one piece of every
+            // row, so that a store has 64 bytes of a row together.
+            const int d = k + 8 * own;
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+              const uint4 lo = (own ^ r) & 1 ? v[1] : v[0], hi = (own ^ r) & 1 ? v[3] : v[2];
+              uint4 x = (own ^ r) & 2 ? hi : lo;  // piece own ^ r of this lane's row
+              if (r) {
+                x.x = __shfl_xor_sync(kFullMask, x.x, r);
+                x.y = __shfl_xor_sync(kFullMask, x.y, r);
+                x.z = __shfl_xor_sync(kFullMask, x.z, r);
+                x.w = __shfl_xor_sync(kFullMask, x.w, r);
+              }
+              if (to[r] && d < C.head_dim) *reinterpret_cast<uint4*>(to[r] + d) = x;
             }
           } else if (mine) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              part[(col0 + k + e) / 4 * P.part_rows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              part[(k + e) / 4 * P.part_rows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
           __syncwarp();
         }
+        // Values that are not finite come back where they are seen.  Only a checked request's
+        // pages are followed.  (Of a flagged one a box may not have been copied, and what its
+        // place in the ring held before may look like such values.)
+        if (w.any_odd && !bad && mine) {
+#pragma unroll 1
+          for (int bit = 0; bit < 64 * kEdge; bit++) {
+            if (!(w.odd[bit / 32] >> bit % 32 & 1)) continue;
+            const int key = bit < 32 * kEdge ? keys.pos0 + 1 + bit : keys.low0 + bit - 32 * kEdge;
+            if (key > pos || key < low) continue;
+            const uint16_t* v = C.v + C.slot(w.b, key) + w.h * C.head_stride;
+#pragma unroll 1
+            for (int d = col0; d < min(col0 + cols, C.head_dim); d++) {
+              const uint32_t bits = v[d];
+              if ((bits & kExp) != kExp) continue;
+              const float odd = E::unpack(bits).x;
+              if (whole) out[d] = static_cast<uint16_t>(E::pack(E::unpack(out[d]).x + odd, 0.0f));
+              else reinterpret_cast<float*>(part + d / 4 * P.part_rows)[d % 4] += odd;
+            }
+          }
+        }
+        __syncwarp();
         if (!whole && mine && (pair || st == 0))
           P.ws.stats[slot * P.part_rows + first_row + row] = make_float2(m, l);
       }
       tmem_fence_before();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      tmem_fence_after();
+      __syncwarp();
+      done_item();
+      if (!pair) {  // the other's sums may be written over when both have read them
+        if (lane == 0) barrier_arrive(smem_of(&s.parted));
+        barrier_wait(smem_of(&s.parted), shared++ & 1, gave_up);
+        tmem_fence_after();
+      }
     }
   }
 
@@ -1168,7 +1310,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Params P) {
   }
 }
 
-template <class E, int DP, bool kMod>
+template <class E, int DP, int kMod>
 cudaError_t launch(const Params& P, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
   using S = Shape<DP>;
   constexpr int kSmem = S::kTailAt + static_cast<int>(sizeof(Tail<S::kStages>));
@@ -1197,10 +1339,11 @@ cudaError_t run(const Params& P, const CUtensorMap& k_map, const CUtensorMap& v_
 
 template <class E>
 cudaError_t run_any(const Params& P, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
-  const bool mod = P.cap_log2 > 0.0f || P.slopes;
-  if (P.cache.head_dim <= 64)
-    return mod ? launch<E, 64, true>(P, k, v, stream) : launch<E, 64, false>(P, k, v, stream);
-  return mod ? launch<E, 128, true>(P, k, v, stream) : launch<E, 128, false>(P, k, v, stream);
+  const bool narrow = P.cache.head_dim <= 64;
+  if (P.slopes) return narrow ? launch<E, 64, kBiased>(P, k, v, stream) : launch<E, 128, kBiased>(P, k, v, stream);
+  if (P.cap_log2 > 0.0f)
+    return narrow ? launch<E, 64, kCapped>(P, k, v, stream) : launch<E, 128, kCapped>(P, k, v, stream);
+  return narrow ? launch<E, 64, kPlain>(P, k, v, stream) : launch<E, 128, kPlain>(P, k, v, stream);
 }
 
 }  // namespace specv_chunk

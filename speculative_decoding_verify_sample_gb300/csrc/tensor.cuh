@@ -194,6 +194,21 @@ __device__ __forceinline__ void tmem_load128(uint32_t at, uint32_t (&x)[128]) {
       : "memory");
 }
 
+// 64 columns, waited for.
+__device__ __forceinline__ void tmem_load64(uint32_t at, uint32_t (&x)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SPECV_R32(x, 0), SPECV_R32(x, 32)
+      : "r"(at), "r"(at + 32)
+      : "memory");
+}
+
 // 16 columns, waited for.
 __device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&x)[16]) {
   asm volatile(
@@ -210,6 +225,15 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&x)[16
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::SPECV_I8(x, 0),
       SPECV_I8(x, 8), "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&x)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SPECV_I8(x, 0),
+      SPECV_I8(x, 8), SPECV_I8(x, 16), SPECV_I8(x, 24), "r"(at)
       : "memory");
 }
 
