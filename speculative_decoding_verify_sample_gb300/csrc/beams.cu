@@ -4,10 +4,10 @@
 //   score(w, v) = scores[w] + z[w,v] - log sum_u exp z[w,u],
 //
 // the K best of W V.  Within a row the order is that of z, so a block that has a part of a
-// row keeps that part's K best entries and its max and sum of exponentials; a request's
-// block then has the rows' sums, turns the W parts' entries into scores and takes the K
-// best of them.  Each logit is read once, and only the few that may be among the best
-// leave the registers.
+// row keeps that part's K best entries and its sum of exponentials; a request's block then
+// has the rows' sums, turns the parts' entries into scores and takes the K best of them.
+// Each logit is read once, and only the few that may be among the best leave the
+// registers.
 
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -21,16 +21,24 @@ using namespace specv_cache_ops;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMine = 32;                  // entries of a tile that a thread has
-constexpr int kTile = kThreads * kMine;    // entries of a row that a block looks at together
+constexpr int kWarps = kThreads / 32;
+constexpr int kVecs = 4;  // vectors of 16 bytes that a lane has of a row at a time
 constexpr int kMaxBeams = SPECV_MAX_BEAMS;
-constexpr int kFound = 1024;  // entries that may be among the best, of a tile or of a request
+constexpr int kBuffer = 128;  // entries of a warp that may be among the best, until they are sorted in
+constexpr int kFound = 1024;  // and of a request
+constexpr int kKept = 2048;   // candidates that a request's block keeps in shared memory
 constexpr int kVocabBits = 20;  // of a vocabulary entry's number
+constexpr int kMaxSplits = 32;  // parts of a row: a request's block reads what they leave
+#ifndef BLOCKS
+#define BLOCKS 6
+#endif
+constexpr int kBlocks = BLOCKS;     // of an SM, at least, where rows are long enough
 
 template <int DT> struct Elt;
 template <> struct Elt<SPECV_F32> {
   using T = float;
   static constexpr int kVec = 4;
+  static constexpr uint32_t kNone = 0xff800000u;  // -inf
   static __device__ __forceinline__ float one(float x) { return x; }
   static __device__ __forceinline__ void unpack(const uint4& v, float* z) {
     z[0] = __uint_as_float(v.x);
@@ -42,6 +50,7 @@ template <> struct Elt<SPECV_F32> {
 template <> struct Elt<SPECV_BF16> {
   using T = uint16_t;
   static constexpr int kVec = 8;
+  static constexpr uint32_t kNone = 0xff80ff80u;
   static __device__ __forceinline__ float one(uint16_t x) {
     return __uint_as_float(static_cast<uint32_t>(x) << 16);
   }
@@ -73,7 +82,7 @@ struct Params {
   int32_t* tokens;
   int32_t* beams;
   int32_t* status;
-  int W, V, K, splits, tiles, end_token;  // tiles: of a part
+  int W, V, K, splits, steps, end_token;  // parts of a row, steps of each of a part's warps
 };
 
 // An entry of a row as one number: a larger value, then a smaller place, is larger.
@@ -96,16 +105,15 @@ __device__ __forceinline__ float exp_of(float x) {
   return y;
 }
 
-// The vector of a row's entries from `at` on.  A row may begin anywhere: then two
-// aligned vectors are shifted together where both lie within the row.
+// The vector of a row's entries from `at` on, -inf behind the last.  A row may begin
+// anywhere: then two aligned vectors are shifted together where both lie within the row.
 template <int DT>
-__device__ __forceinline__ void load_vector(const typename Elt<DT>::T* row, int at, int V, int shift,
-                                            float* z) {
+__device__ __forceinline__ uint4 load_vector(const typename Elt<DT>::T* row, int at, int V, int shift) {
   using E = Elt<DT>;
   constexpr int kVec = E::kVec, kSize = 16 / kVec;
-  if (at + kVec <= V && shift == 0) {
-    E::unpack(__ldg(reinterpret_cast<const uint4*>(row + at)), z);
-  } else if (at * kSize >= shift && (at + 2 * kVec) * kSize - shift <= V * static_cast<int64_t>(kSize)) {
+  if (at + kVec <= V && shift == 0) return __ldg(reinterpret_cast<const uint4*>(row + at));
+  uint4 v = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+  if (at * kSize >= shift && (at + 2 * kVec) * static_cast<int64_t>(kSize) - shift <= V * static_cast<int64_t>(kSize)) {
     const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row + at) - shift);
     const uint4 a = __ldg(from), b = __ldg(from + 1);
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -114,27 +122,41 @@ __device__ __forceinline__ void load_vector(const typename Elt<DT>::T* row, int 
 #pragma unroll
     for (int i = 0; i < 5; i++)
       x[i] = words == 0 ? w[i] : words == 1 ? w[i + 1] : words == 2 ? w[i + 2] : w[i + 3];
-    uint4 v;
 #pragma unroll
     for (int i = 0; i < 4; i++) (&v.x)[i] = shift % 4 ? __funnelshift_r(x[i], x[i + 1], 16) : x[i];
-    E::unpack(v, z);
   } else {
 #pragma unroll
-    for (int i = 0; i < kVec; i++) z[i] = at + i < V ? E::one(row[at + i]) : -INFINITY;
+    for (int i = 0; i < kVec; i++)
+      if (at + i < V) reinterpret_cast<typename E::T*>(&v)[i] = row[at + i];
   }
+  return v;
 }
 
-// A block's part of one row.
+// The K-th largest of a warp's numbers, K <= 32 (a bitonic sort).
+__device__ __forceinline__ float kth_of_warp(float x, int K, int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+    for (int j = k / 2; j > 0; j /= 2) {
+      const float y = __shfl_xor_sync(kFullMask, x, j);
+      x = ((lane & j) == 0) == ((lane & k) == 0) ? fmaxf(x, y) : fminf(x, y);
+    }
+  return __shfl_sync(kFullMask, x, K - 1);
+}
+
+// A block's part of one row.  Its warps go through it in steps, in turn, the next step's
+// loads under way, and tell one another what no entry of the row's best can be below.
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const Params P) {
   using E = Elt<DT>;
-  constexpr int kVec = E::kVec;
-  __shared__ uint64_t s_found[kFound];
-  __shared__ uint64_t s_best[2][kMaxBeams];
-  __shared__ float s_top[kMaxBeams];
-  __shared__ float s_max[kThreads / 32];
-  __shared__ double s_sum[kThreads / 32];
-  __shared__ int s_count[3];
+  constexpr int kVec = E::kVec, kMine = kVecs * kVec, kStep = 32 * kMine;
+  __shared__ uint64_t s_best[kWarps][2][kMaxBeams];
+  __shared__ uint64_t s_found[kWarps][kBuffer];
+  __shared__ float s_max[kWarps];
+  __shared__ double s_sum[kWarps];
+  __shared__ uint64_t s_all[kWarps * kMaxBeams];
+  __shared__ uint32_t s_least;  // (as the upper half of a key)
+  __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   const int64_t row = blockIdx.x / P.splits;
   const int split = blockIdx.x - static_cast<int>(row) * P.splits, K = P.K;
@@ -144,140 +166,181 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const Params P
   const auto* from = static_cast<const typename E::T*>(P.logits) + row / P.W * P.batch_stride +
                      row % P.W * P.row_stride;
   const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15);
+  uint64_t* const found = s_found[warp];
+  if (tid == 0) {
+    s_least = 0;
+    s_count = 0;
+  }
+  __syncthreads();
 
-  float m = -INFINITY;
-  double l = 0.0;
+  float m = -INFINITY, l = 0.0f;  // of this lane's entries
   int have = 0, now = 0;  // entries of s_best[now]
-  // groups of threads, at least K of them: each has an entry of its own maximum
-  const int groups = K <= 8 ? 8 : K <= 16 ? 16 : K <= 32 ? 32 : 64, width = kThreads / groups;
-  for (int tile = 0; tile < P.tiles; tile++) {
-    const int first = (split * P.tiles + tile) * kTile;
+  int waiting = 0;        // entries of found
+  // What is below `least`, or equal and not in front of `least_at`, is not among the K best.
+  float least = -INFINITY;
+  int least_at = -1;
+  auto tell = [&]() {
+    if (lane == 0 && least > -INFINITY) atomicMax(&s_least, static_cast<uint32_t>(key_of(least, 0) >> 32));
+  };
+  // Sorts the found entries in: each goes to the place that its rank is.
+  auto merge = [&]() {
+    __syncwarp();
+    const int all = have + waiting;
+    const uint64_t* best = s_best[warp][now];
+    uint64_t* to = s_best[warp][now ^ 1];
+    for (int i = lane; i < all; i += 32) {
+      const uint64_t key = i < have ? best[i] : found[i - have];
+      int rank = 0;
+      for (int k = 0; k < have; k++) rank += best[k] > key;
+      for (int k = 0; k < waiting; k++) rank += found[k] > key;
+      if (rank < K) to[rank] = key;
+    }
+    __syncwarp();
+    have = min(K, all);
+    now ^= 1;
+    waiting = 0;
+    if (have == K) {
+      const uint64_t last = to[K - 1];
+      if (value_of(last) >= least) {
+        least = value_of(last);
+        least_at = place_of(last);
+        tell();
+      }
+    }
+  };
+
+  const int begin = split * P.steps * kWarps * kStep;
+  uint4 next[kVecs];
+  auto first_of = [&](int step) { return begin + (step * kWarps + warp) * kStep; };
+  auto fetch = [&](int step) {
+#pragma unroll
+    for (int j = 0; j < kVecs; j++) {
+      const int e = first_of(step) + (j * 32 + lane) * kVec;
+      next[j] = step < P.steps && e < P.V ? load_vector<DT>(from, e, P.V, shift)
+                                          : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+    }
+  };
+  fetch(0);
+#pragma unroll 1
+  for (int step = 0; step < P.steps; step++) {
+    const int first = first_of(step);
     if (first >= P.V) break;
-    float z[kMine];
+    float z[kMine], tops[kVecs];
 #pragma unroll
-    for (int j = 0; j < kMine / kVec; j++)
-      load_vector<DT>(from, first + (j * kThreads + tid) * kVec, P.V, shift, z + j * kVec);
-    float top = z[0];
+    for (int j = 0; j < kVecs; j++) E::unpack(next[j], z + j * kVec);
+    fetch(step + 1);
 #pragma unroll
-    for (int j = 1; j < kMine; j++) top = fmaxf(top, z[j]);
-    const float higher = fmaxf(m, top);
-    float sum = 0.0f;
-    // (a row of a NaN or +inf makes the sum a NaN, which the request's block sees)
+    for (int j = 0; j < kVecs; j++) {
+      tops[j] = z[j * kVec];
 #pragma unroll
-    for (int j = 0; j < kMine; j++) sum += exp_of(z[j] - (higher == -INFINITY ? 0.0f : higher));
-    l = l * (higher == -INFINITY ? 1.0 : static_cast<double>(exp_of(m - higher))) + sum;
+      for (int e = 1; e < kVec; e++) tops[j] = fmaxf(tops[j], z[j * kVec + e]);
+    }
+    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    // (a NaN or +inf makes the sum a NaN, which the request's block sees)
+    const float higher = fmaxf(m, top), from_max = higher == -INFINITY ? 0.0f : higher;
+    float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < kMine; j++) sums[j % 4] += exp_of(z[j] - from_max);
+    l = l * (m == higher ? 1.0f : exp_of(m - higher)) + ((sums[0] + sums[1]) + (sums[2] + sums[3]));
     m = higher;
 
-    if (tid < 3) s_count[tid] = 0;
-    float least;  // an entry below it is not among the K best
-    if (tile == 0) {
-      float all = top;
-      for (int o = width / 2; o > 0; o /= 2) all = fmaxf(all, __shfl_xor_sync(kFullMask, all, o));
-      if (tid % width == 0) s_top[tid / width] = all;
-      __syncthreads();
-      least = s_top[0];
-      for (int g = 1; g < groups; g++) least = fminf(least, s_top[g]);
-    } else {
-      __syncthreads();
-      least = have < K ? -INFINITY : value_of(s_best[now][K - 1]);
-    }
-    // (behind the first tile a value equal to the K-th comes later than it)
-    const bool equal = tile == 0 && least > -INFINITY;
-    if (equal ? top >= least : top > least) {
+    if (step == 0) {
+      // The K-th largest of the lanes' maxima (for K > 32 the least of 64, two of a lane): as many
+      // entries are not below it.
+      float kth;
+      if (K <= 32) {
+        kth = kth_of_warp(top, K, lane);
+      } else {
+        kth = fminf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
 #pragma unroll
-      for (int j = 0; j < kMine; j++)
-        if (equal ? z[j] >= least : z[j] > least) {
-          const int at = atomicAdd(&s_count[0], 1);
-          if (at < kFound)
-            s_found[at] = key_of(z[j], first + (j / kVec * kThreads + tid) * kVec + j % kVec);
-        }
-    }
-    __syncthreads();
-    int found = s_count[0];
-    if (found > kFound) {
-      // Too many: the tile's K-th best itself, bit by bit from the top of its value and place.
-      constexpr int kBits = 32 + kVocabBits;
-      auto small_key = [&](int j) {
-        const int at = first + (j / kVec * kThreads + tid) * kVec + j % kVec;
-        return z[j] > -INFINITY ? key_of(z[j], at) >> 32 << kVocabBits | ((1 << kVocabBits) - 1 - at) : 0ull;
-      };
-      uint64_t least_key = 0;
-      for (int bit = kBits - 1; bit >= 0; bit--) {
-        const uint64_t at_least = least_key | 1ull << bit;
-        int n = 0;
-#pragma unroll
-        for (int j = 0; j < kMine; j++) n += small_key(j) >= at_least;
-        n = __reduce_add_sync(kFullMask, n);
-        int* count = &s_count[1 + bit % 2];
-        if (lane == 0 && n) atomicAdd(count, n);
-        __syncthreads();
-        if (*count >= K) least_key = at_least;
-        if (tid == 0) s_count[1 + (bit + 1) % 2] = 0;
-        __syncthreads();
+        for (int o = 16; o > 0; o /= 2) kth = fminf(kth, __shfl_xor_sync(kFullMask, kth, o));
       }
-      if (tid == 0) s_count[0] = 0;
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < kMine; j++)
-        if (small_key(j) >= least_key && z[j] > -INFINITY)
-          s_found[atomicAdd(&s_count[0], 1)] =
-              key_of(z[j], first + (j / kVec * kThreads + tid) * kVec + j % kVec);
-      __syncthreads();
-      found = s_count[0];
+      least = kth;
+      least_at = kth > -INFINITY ? INT_MAX : -1;
+      tell();
     }
-    if (found) {
-      // The best of those so far and the found, each at the place that its rank is.
-      auto nth = [&](int i) { return i < have ? s_best[now][i] : s_found[i - have]; };
-      const int all = have + found;
-      for (int i = tid; i < all; i += kThreads) {
-        const uint64_t key = nth(i);
-        int rank = 0;
-        for (int k = 0; k < have; k++) rank += s_best[now][k] > key;
-        for (int k = 0; k < found; k++) rank += s_found[k] > key;
-        if (rank < K) s_best[now ^ 1][rank] = key;
+    const uint32_t told = *static_cast<volatile uint32_t*>(&s_least);
+    if (told) {
+      const float others = value_of(static_cast<uint64_t>(told) << 32);
+      if (others > least) {
+        least = others;
+        least_at = INT_MAX;
       }
-      have = min(K, all);
-      now ^= 1;
     }
-    __syncthreads();
+    if (!__any_sync(kFullMask, top >= least && top > -INFINITY)) continue;
+    // The entries not below it, each lane its own one after the other, read once more.  (Short
+    // code: a block that goes through this once or twice spends its time on fetching it.)
+    uint32_t mask = 0;
+#pragma unroll
+    for (int e = 0; e < kMine; e++) mask |= z[e] >= least ? 1u << e : 0u;
+#pragma unroll 1
+    while (__any_sync(kFullMask, mask != 0)) {
+      const int e = mask ? __ffs(mask) - 1 : 0;
+      const int place = first + (e / kVec * 32 + lane) * kVec + e % kVec;
+      const float x = mask && place < P.V ? E::one(from[place]) : -INFINITY;
+      mask &= mask - 1;
+      unsigned good = __ballot_sync(kFullMask, x > least || (x == least && place < least_at));
+      if (waiting + __popc(good) > kBuffer) {
+        merge();
+        good = __ballot_sync(kFullMask, x > least || (x == least && place < least_at));
+      }
+      if (good >> lane & 1) found[waiting + __popc(good & ((1u << lane) - 1))] = key_of(x, place);
+      waiting += __popc(good);
+    }
+    if (waiting) merge();
   }
-  // The part's maximum and sum.
+  // The part's maximum and sum, and the best of the warps' best.
   float all = m;
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) all = fmaxf(all, __shfl_xor_sync(kFullMask, all, o));
-  if (lane == 0) s_max[warp] = all;
-  __syncthreads();
+  double sum = m == all ? l : l * exp_of(m - all);
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; w++) all = fmaxf(all, s_max[w]);
-  if (all > -INFINITY) l *= static_cast<double>(exp_of(m - all));
-#pragma unroll
-  for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(kFullMask, l, o);
-  if (lane == 0) s_sum[warp] = l;
-  __syncthreads();
-  const int64_t at = row * P.splits + split;
-  if (tid == 0) {
-    double sum = 0.0;
-    for (int w = 0; w < kThreads / 32; w++) sum += s_sum[w];
-    P.parts[at] = Part{all, 0.0f, sum};
+  for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
+  int at = 0;
+  if (lane == 0) {
+    s_max[warp] = all;
+    s_sum[warp] = sum;
+    at = atomicAdd(&s_count, have);
   }
-  if (tid < K) P.keys[at * K + tid] = tid < have ? s_best[now][tid] : 0;
+  at = __shfl_sync(kFullMask, at, 0);
+  for (int k = lane; k < have; k += 32) s_all[at + k] = s_best[warp][now][k];
+  __syncthreads();
+  const int64_t part = blockIdx.x;
+  const int n = s_count;
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t key = s_all[i];
+    int rank = 0;
+    for (int k = 0; k < n; k++) rank += s_all[k] > key;
+    if (rank < K) P.keys[part * K + rank] = key;
+  }
+  for (int k = n + tid; k < K; k += kThreads) P.keys[part * K + k] = 0;
+  if (tid == 0) {
+    float most = s_max[0];
+    for (int w = 1; w < kWarps; w++) most = fmaxf(most, s_max[w]);
+    double total = 0.0;
+    for (int w = 0; w < kWarps; w++)
+      total += s_max[w] == most ? s_sum[w] : s_sum[w] * static_cast<double>(exp_of(s_max[w] - most));
+    P.parts[part] = Part{most, 0.0f, total};
+  }
 }
 
-// A candidate: its score, and beam and token as one number.
+// A candidate: its score as a whole number of the same order, and beam and token as one number.
 struct Candidate {
-  double score;
+  uint64_t score;  // kNothing: none
   uint32_t place;
 };
+constexpr uint64_t kNothing = 0x000fffffffffffffull;  // of -inf
+__device__ __forceinline__ uint64_t ordered(double x) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));  // (-0 is 0)
+  return u >> 63 ? ~u : u | 1ull << 63;
+}
+__device__ __forceinline__ double score_of(uint64_t u) {
+  return __longlong_as_double(static_cast<long long>(u >> 63 ? u & ~(1ull << 63) : ~u));
+}
 __device__ __forceinline__ bool better(const Candidate& a, const Candidate& b) {
   return a.score > b.score || (a.score == b.score && a.place < b.place);
 }
-__device__ __forceinline__ Candidate best_of_warp(Candidate c, int width) {
-  for (int o = width / 2; o > 0; o /= 2) {
-    const Candidate d{__shfl_xor_sync(kFullMask, c.score, o), __shfl_xor_sync(kFullMask, c.place, o)};
-    if (better(d, c)) c = d;
-  }
-  return c;
-}
+__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 // A request's block: the rows' sums, then the K best of the parts' entries.
 __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
@@ -285,8 +348,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   __shared__ float s_max[kMaxBeams];   // and what that sum's exponentials were taken from
   __shared__ uint8_t s_kind[kMaxBeams];  // 0: no candidate, 1: a row, 2: ended
   __shared__ Candidate s_found[kFound];
-  __shared__ double s_top[kMaxBeams];
-  __shared__ Candidate s_warp[kThreads / 32];
+  __shared__ uint64_t s_score[kKept];
+  __shared__ uint32_t s_place[kKept];
+  __shared__ uint64_t s_top[kMaxBeams];
+  __shared__ Candidate s_warp[kWarps];
   __shared__ int s_count, s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   const int64_t b = blockIdx.x;
@@ -294,7 +359,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   if (tid == 0) s_count = s_bad = 0;
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int w = warp; w < W; w += kThreads / 32) {
+  for (int w = warp; w < W; w += kWarps) {
     const int64_t row = b * W + w;
     const float score = P.scores[row];
     const bool over = P.ended && P.ended[row];
@@ -311,9 +376,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
       for (int k = lane; k < P.splits; k += 32) {
         const Part part = P.parts[row * P.splits + k];
         // (a part of -inf alone has 0, one that has a NaN a NaN)
-        sum += part.max == -INFINITY
-                   ? part.sum * 0.0
-                   : part.sum * exp(static_cast<double>(part.max) - static_cast<double>(m));
+        sum += part.max == m ? part.sum : part.sum * static_cast<double>(part.max == -INFINITY ? 0.0f : exp_of(part.max - m));
       }
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(kFullMask, sum, o);
@@ -329,44 +392,91 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
     }
   }
   __syncthreads();
-  const int per_row = P.splits * K, all = W * per_row;
-  // Entry number e; worse than any where there is none.
-  const Candidate none{-INFINITY, 0xffffffffu};
-  auto entry = [&](int e) {
-    const int w = e / per_row, k = e - w * per_row, kind = s_kind[w];
-    if (kind == 0 || (kind == 2 && k)) return none;
-    const uint32_t beam = static_cast<uint32_t>(w) << kVocabBits;
-    if (kind == 2) return Candidate{s_off[w], beam};
-    const uint64_t key = P.keys[(b * W + w) * per_row + k];
-    if (!key) return none;
-    return Candidate{s_off[w] + (static_cast<double>(value_of(key)) - static_cast<double>(s_max[w])),
-                     beam | static_cast<uint32_t>(place_of(key))};
-  };
   const bool bad = s_bad != 0;
+  const int lists = W * P.splits, all = bad ? 0 : lists * K;
+  // Entry number e; worse than any where there is none.  The lists' first entries come first, those
+  // of all rows beside one another, so that every group of threads below has good ones.
+  const Candidate none{kNothing, 0xffffffffu};
+  auto entry = [&](int e) {
+    const int k = e / lists, list = e - k * lists, split = list / W, w = list - split * W, kind = s_kind[w];
+    Candidate c = none;
+    if (kind == 1) {
+      const uint64_t key = P.keys[((b * W + w) * P.splits + split) * K + k];
+      if (key) {
+        c.score = ordered(s_off[w] + (static_cast<double>(value_of(key)) - static_cast<double>(s_max[w])));
+        c.place = static_cast<uint32_t>(w) << kVocabBits | static_cast<uint32_t>(place_of(key));
+      }
+    } else if (kind == 2 && !k && !split) {
+      c.score = ordered(s_off[w]);
+      c.place = static_cast<uint32_t>(w) << kVocabBits;
+    }
+    return c;
+  };
   // The least of K or more groups' best: nothing below it is among the K best.
-  double mine = -INFINITY;
-  if (!bad)
-    for (int e = tid; e < all; e += kThreads) mine = fmax(mine, entry(e).score);
+  uint64_t mine = kNothing;
+#pragma unroll 1
+  for (int e = tid; e < all; e += kThreads) {
+    const Candidate c = entry(e);
+    if (e < kKept) {
+      s_score[e] = c.score;
+      s_place[e] = c.place;
+    }
+    mine = larger(mine, c.score);
+  }
+  // (a thread's own, no other's)
+  auto again = [&](int e) { return e < kKept ? Candidate{s_score[e], s_place[e]} : entry(e); };
   const int groups = K <= 8 ? 8 : K <= 16 ? 16 : K <= 32 ? 32 : 64, width = kThreads / groups;
-  for (int o = width / 2; o > 0; o /= 2) mine = fmax(mine, __shfl_xor_sync(kFullMask, mine, o));
+  for (int o = width / 2; o > 0; o /= 2) mine = larger(mine, __shfl_xor_sync(kFullMask, mine, o));
   if (tid % width == 0) s_top[tid / width] = mine;
   __syncthreads();
-  double least = s_top[0];
-  for (int g = 1; g < groups; g++) least = fmin(least, s_top[g]);
-  if (!bad)
+  uint64_t least = s_top[0];
+#pragma unroll 1
+  for (int g = 1; g < groups; g++) least = s_top[g] < least ? s_top[g] : least;
+  auto collect = [&]() {
+#pragma unroll 1
     for (int e = tid; e < all; e += kThreads) {
-      const Candidate c = entry(e);
-      if (c.score > -INFINITY && c.score >= least) {
-        const int at = atomicAdd(&s_count, 1);
-        if (at < kFound) s_found[at] = c;
+      const Candidate c = again(e);
+      if (c.score <= kNothing || c.score < least) continue;
+      const int at = atomicAdd(&s_count, 1);
+      if (at < kFound) s_found[at] = c;
+    }
+  };
+  collect();
+  __syncthreads();
+  int found = s_count;
+  if (found > kFound) {
+    // Too many: halve what lies between that bound and the best until the bound leaves few enough.
+    uint64_t low = least, high = s_top[0];  // low leaves K or more, high fewer than that or too few
+    for (int g = 1; g < groups; g++) high = larger(high, s_top[g]);
+    while (found > kFound && high - low > 1) {
+      const uint64_t middle = low + (high - low) / 2;
+      int n = 0;
+#pragma unroll 1
+      for (int e = tid; e < all; e += kThreads) n += again(e).score >= middle;
+      __syncthreads();
+      if (tid == 0) s_count = 0;
+      __syncthreads();
+      n = __reduce_add_sync(kFullMask, n);
+      if (lane == 0 && n) atomicAdd(&s_count, n);
+      __syncthreads();
+      if (s_count >= K) {
+        low = middle;
+        found = s_count;
+      } else {
+        high = middle;
       }
     }
-  __syncthreads();
-  const int found = s_count;
+    least = low;
+    __syncthreads();
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    if (found <= kFound) collect();
+    __syncthreads();
+  }
   auto put = [&](int k, const Candidate& c) {
-    const bool real = c.score > -INFINITY;
+    const bool real = c.score > kNothing;
     const int w = static_cast<int>(c.place >> kVocabBits);
-    P.out_scores[b * K + k] = static_cast<float>(c.score);
+    P.out_scores[b * K + k] = real ? static_cast<float>(score_of(c.score)) : -INFINITY;
     P.beams[b * K + k] = real ? w : -1;
     P.tokens[b * K + k] = !real ? -1 : s_kind[w] == 2 ? P.end_token
                                                       : static_cast<int>(c.place & ((1u << kVocabBits) - 1));
@@ -380,19 +490,23 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
     }
     for (int k = found + tid; k < K; k += kThreads) put(k, none);
   } else {
-    // Too many (scores all alike): one after the other, each the best of those behind the last.
-    Candidate last{INFINITY, 0};
+    // Still too many (scores all alike): one after the other, each the best of those behind the last.
+    Candidate last{~0ull, 0};
     for (int k = 0; k < K; k++) {
       Candidate c = none;
       for (int e = tid; e < all; e += kThreads) {
-        const Candidate d = entry(e);
+        const Candidate d = again(e);
         if (better(last, d) && better(d, c)) c = d;
       }
-      c = best_of_warp(c, 32);
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) {
+        const Candidate d{__shfl_xor_sync(kFullMask, c.score, o), __shfl_xor_sync(kFullMask, c.place, o)};
+        if (better(d, c)) c = d;
+      }
       if (lane == 0) s_warp[warp] = c;
       __syncthreads();
       c = s_warp[0];
-      for (int i = 1; i < kThreads / 32; i++)
+      for (int i = 1; i < kWarps; i++)
         if (better(s_warp[i], c)) c = s_warp[i];
       __syncthreads();
       if (tid == 0) put(k, c);
@@ -406,19 +520,22 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // How rows are shared out over blocks, and the workspace for it.
 struct Plan {
-  int tiles, splits;  // of a part, of a row
+  int steps, splits;  // of a part's warps; parts of a row
   size_t keys, total;
 
-  Plan(int B, int W, int K, int V) {
-    const int all = (V + kTile - 1) / kTile;
-    const int64_t rows = static_cast<int64_t>(B) * W, wanted = 16 * kSms;
-    const int parts = static_cast<int>(rows >= wanted ? 1 : (wanted + rows - 1) / rows);
-    tiles = parts >= all ? 1 : (all + parts - 1) / parts;
-    splits = (all + tiles - 1) / tiles;
+  Plan(int B, int W, int K, int V, int step) {
+    const int all = (V + step * kWarps - 1) / (step * kWarps);  // steps of eight warps
+    const int64_t rows = static_cast<int64_t>(B) * W, wanted = kBlocks * kSms;
+    int64_t parts = (wanted + rows - 1) / rows;
+    if (parts > kMaxSplits) parts = kMaxSplits;
+    if (parts > all) parts = all;
+    steps = static_cast<int>((all + parts - 1) / parts);
+    splits = (all + steps - 1) / steps;
     keys = align256(rows * splits * sizeof(Part));
     total = keys + align256(rows * splits * K * sizeof(uint64_t));
   }
 };
+template <int DT> constexpr int kStepOf = 32 * kVecs * Elt<DT>::kVec;
 
 specv_status check_beams(int B, int W, int K) {
   if (B < 1 || W < 1 || K < 1) return SPECV_ERR_INVALID_ARG;
@@ -493,7 +610,9 @@ extern "C" {
 
 size_t specv_beam_workspace_bytes(int B, int W, int K, int V) {
   if (check_beams(B, W, K) != SPECV_OK || V < 1 || V > 1 << kVocabBits) return 0;
-  return Plan(B, W, K, V).total;
+  // (a 32-bit row has as many steps as a 16-bit row of twice its entries, or more)
+  const size_t half = Plan(B, W, K, V, kStepOf<SPECV_BF16>).total, full = Plan(B, W, K, V, kStepOf<SPECV_F32>).total;
+  return half > full ? half : full;
 }
 
 specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t row_stride,
@@ -512,7 +631,7 @@ specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t
       !aligned_to(beams, 4) || !aligned_to(status, 4) || !aligned_to(workspace, 256))
     return SPECV_ERR_INVALID_ARG;
   if (V > specv_max_vocab(dtype)) return SPECV_ERR_UNSUPPORTED;
-  const Plan plan(B, W, K, V);
+  const Plan plan(B, W, K, V, dtype == SPECV_F32 ? kStepOf<SPECV_F32> : kStepOf<SPECV_BF16>);
   if (workspace_bytes < plan.total) return SPECV_ERR_WORKSPACE;
   char* base = static_cast<char*>(workspace);
   const Params P{logits,
@@ -530,7 +649,7 @@ specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t
                  V,
                  K,
                  plan.splits,
-                 plan.tiles,
+                 plan.steps,
                  end_token};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const unsigned blocks = static_cast<unsigned>(B) * W * plan.splits;
