@@ -26,13 +26,10 @@ constexpr int kVecs = 4;  // vectors of 16 bytes that a lane has of a row at a t
 constexpr int kMaxBeams = SPECV_MAX_BEAMS;
 constexpr int kBuffer = 128;  // entries of a warp that may be among the best, until they are sorted in
 constexpr int kFound = 1024;  // and of a request
-constexpr int kKept = 2048;   // candidates that a request's block keeps in shared memory
+constexpr int kKept = 8192;   // candidates that a request's block keeps in shared memory, at most
 constexpr int kVocabBits = 20;  // of a vocabulary entry's number
 constexpr int kMaxSplits = 32;  // parts of a row: a request's block reads what they leave
-#ifndef BLOCKS
-#define BLOCKS 6
-#endif
-constexpr int kBlocks = BLOCKS;     // of an SM, at least, where rows are long enough
+constexpr int kBlocks = 3;     // of an SM, where rows are long enough
 
 template <int DT> struct Elt;
 template <> struct Elt<SPECV_F32> {
@@ -82,6 +79,7 @@ struct Params {
   int32_t* tokens;
   int32_t* beams;
   int32_t* status;
+  int kept;  // candidates that a request's block keeps in shared memory
   int W, V, K, splits, steps, end_token;  // parts of a row, steps of each of a part's warps
 };
 
@@ -132,7 +130,16 @@ __device__ __forceinline__ uint4 load_vector(const typename Elt<DT>::T* row, int
   return v;
 }
 
-// The K-th largest of a warp's numbers, K <= 32 (a bitonic sort).
+// Adds how many of n keys are larger, two at a time (of an odd number one more is there, 0).
+__device__ __forceinline__ void rank_among(const uint64_t* keys, int n, uint64_t key, int& rank) {
+#pragma unroll 4
+  for (int k = 0; k < n; k += 2) {
+    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(keys + k);
+    rank += (two.x > key) + (two.y > key);
+  }
+}
+
+// The K-th largest of a warp's 32 numbers (a bitonic sort).
 __device__ __forceinline__ float kth_of_warp(float x, int K, int lane) {
 #pragma unroll
   for (int k = 2; k <= 32; k *= 2)
@@ -144,18 +151,42 @@ __device__ __forceinline__ float kth_of_warp(float x, int K, int lane) {
   return __shfl_sync(kFullMask, x, K - 1);
 }
 
+// A number that K of a warp's 128, or a few more, are not below (-inf where fewer are finite).
+__device__ __forceinline__ float about_kth_of_warp(const float (&x)[4], int K) {
+  uint32_t key[4], low = 0, high = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    key[j] = x[j] > -INFINITY ? static_cast<uint32_t>(key_of(x[j], 0) >> 32) : 0;
+    high = max(high, key[j]);
+  }
+  high = __reduce_max_sync(kFullMask, high);
+  // low: K or more are not below; above high there are fewer
+#pragma unroll 1
+  while (low < high) {
+    const uint32_t middle = low + (high - low + 1) / 2;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) n += __popc(__ballot_sync(kFullMask, key[j] >= middle));
+    if (n >= K) low = middle;
+    else high = middle - 1;
+    if (n >= K && n <= K + K / 4) break;
+  }
+  return low ? value_of(static_cast<uint64_t>(low) << 32) : -INFINITY;
+}
+
 // A block's part of one row.  Its warps go through it in steps, in turn, the next step's
 // loads under way, and tell one another what no entry of the row's best can be below.
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const Params P) {
+__global__ void __launch_bounds__(kThreads, 3) select_rows_kernel(const Params P) {
   using E = Elt<DT>;
   constexpr int kVec = E::kVec, kMine = kVecs * kVec, kStep = 32 * kMine;
-  __shared__ uint64_t s_best[kWarps][2][kMaxBeams];
-  __shared__ uint64_t s_found[kWarps][kBuffer];
+  __shared__ __align__(16) uint64_t s_best[kWarps][2][kMaxBeams + 2];
+  __shared__ __align__(16) uint64_t s_found[kWarps][kBuffer + 2];
   __shared__ float s_max[kWarps];
   __shared__ double s_sum[kWarps];
-  __shared__ uint64_t s_all[kWarps * kMaxBeams];
+  __shared__ __align__(16) uint64_t s_all[kWarps * kMaxBeams + 2];
   __shared__ uint32_t s_least;  // (as the upper half of a key)
+  __shared__ float s_share[kWarps];  // a warp's best but K / kWarps
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   const int64_t row = blockIdx.x / P.splits;
@@ -171,6 +202,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const Params P
     s_least = 0;
     s_count = 0;
   }
+  if (tid < kWarps) s_share[tid] = -INFINITY;
+  const int share = (K + kWarps - 1) / kWarps;
   __syncthreads();
 
   float m = -INFINITY, l = 0.0f;  // of this lane's entries
@@ -184,6 +217,10 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const Params P
   };
   // Sorts the found entries in: each goes to the place that its rank is.
   auto merge = [&]() {
+    if (lane == 0) {  // (pairs are compared: behind the last a key that is below all)
+      found[waiting] = 0;
+      s_best[warp][now][have] = 0;
+    }
     __syncwarp();
     const int all = have + waiting;
     const uint64_t* best = s_best[warp][now];
@@ -191,14 +228,15 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const Params P
     for (int i = lane; i < all; i += 32) {
       const uint64_t key = i < have ? best[i] : found[i - have];
       int rank = 0;
-      for (int k = 0; k < have; k++) rank += best[k] > key;
-      for (int k = 0; k < waiting; k++) rank += found[k] > key;
+      rank_among(best, have, key, rank);
+      rank_among(found, waiting, key, rank);
       if (rank < K) to[rank] = key;
     }
     __syncwarp();
     have = min(K, all);
     now ^= 1;
     waiting = 0;
+    if (lane == 0 && have >= share) static_cast<volatile float*>(s_share)[warp] = value_of(to[share - 1]);
     if (have == K) {
       const uint64_t last = to[K - 1];
       if (value_of(last) >= least) {
@@ -210,25 +248,29 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const Params P
   };
 
   const int begin = split * P.steps * kWarps * kStep;
-  uint4 next[kVecs];
+  uint4 next[2][kVecs];  // of this step and the one behind it
   auto first_of = [&](int step) { return begin + (step * kWarps + warp) * kStep; };
-  auto fetch = [&](int step) {
+  auto fetch = [&](int step, uint4 (&to)[kVecs]) {
 #pragma unroll
     for (int j = 0; j < kVecs; j++) {
       const int e = first_of(step) + (j * 32 + lane) * kVec;
-      next[j] = step < P.steps && e < P.V ? load_vector<DT>(from, e, P.V, shift)
-                                          : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+      to[j] = step < P.steps && e < P.V ? load_vector<DT>(from, e, P.V, shift)
+                                        : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
     }
   };
-  fetch(0);
+  fetch(0, next[0]);
+  fetch(1, next[1]);
 #pragma unroll 1
   for (int step = 0; step < P.steps; step++) {
     const int first = first_of(step);
     if (first >= P.V) break;
     float z[kMine], tops[kVecs];
 #pragma unroll
-    for (int j = 0; j < kVecs; j++) E::unpack(next[j], z + j * kVec);
-    fetch(step + 1);
+    for (int j = 0; j < kVecs; j++) {
+      E::unpack(next[0][j], z + j * kVec);
+      next[0][j] = next[1][j];
+    }
+    fetch(step + 2, next[1]);
 #pragma unroll
     for (int j = 0; j < kVecs; j++) {
       tops[j] = z[j * kVec];
@@ -245,27 +287,22 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const Params P
     m = higher;
 
     if (step == 0) {
-      // The K-th largest of the lanes' maxima (for K > 32 the least of 64, two of a lane): as many
-      // entries are not below it.
-      float kth;
-      if (K <= 32) {
-        kth = kth_of_warp(top, K, lane);
-      } else {
-        kth = fminf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) kth = fminf(kth, __shfl_xor_sync(kFullMask, kth, o));
-      }
+      // The K-th largest of the lanes' maxima, or of all vectors': as many entries are not below it.
+      const float kth = K <= 8 ? kth_of_warp(top, K, lane) : about_kth_of_warp(tops, K);
       least = kth;
       least_at = kth > -INFINITY ? INT_MAX : -1;
       tell();
     }
+    // Nothing below another warp's K-th best is among the row's, nor below the least of what all
+    // warps have K / kWarps entries of.
     const uint32_t told = *static_cast<volatile uint32_t*>(&s_least);
-    if (told) {
-      const float others = value_of(static_cast<uint64_t>(told) << 32);
-      if (others > least) {
-        least = others;
-        least_at = INT_MAX;
-      }
+    float others = static_cast<volatile float*>(s_share)[lane % kWarps];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o /= 2) others = fminf(others, __shfl_xor_sync(kFullMask, others, o));
+    if (told) others = fmaxf(others, value_of(static_cast<uint64_t>(told) << 32));
+    if (others > least) {
+      least = others;
+      least_at = INT_MAX;
     }
     if (!__any_sync(kFullMask, top >= least && top > -INFINITY)) continue;
     // The entries not below it, each lane its own one after the other, read once more.  (Short
@@ -307,10 +344,14 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const Params P
   __syncthreads();
   const int64_t part = blockIdx.x;
   const int n = s_count;
+  if (n % 2) {
+    if (tid == 0) s_all[n] = 0;
+    __syncthreads();
+  }
   for (int i = tid; i < n; i += kThreads) {
     const uint64_t key = s_all[i];
     int rank = 0;
-    for (int k = 0; k < n; k++) rank += s_all[k] > key;
+    rank_among(s_all, n, key, rank);
     if (rank < K) P.keys[part * K + rank] = key;
   }
   for (int k = n + tid; k < K; k += kThreads) P.keys[part * K + k] = 0;
@@ -348,8 +389,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   __shared__ float s_max[kMaxBeams];   // and what that sum's exponentials were taken from
   __shared__ uint8_t s_kind[kMaxBeams];  // 0: no candidate, 1: a row, 2: ended
   __shared__ Candidate s_found[kFound];
-  __shared__ uint64_t s_score[kKept];
-  __shared__ uint32_t s_place[kKept];
+  extern __shared__ __align__(16) uint64_t s_score[];  // [kept], and behind them their places
+  uint32_t* const s_place = reinterpret_cast<uint32_t*>(s_score + P.kept);
   __shared__ uint64_t s_top[kMaxBeams];
   __shared__ Candidate s_warp[kWarps];
   __shared__ int s_count, s_bad;
@@ -417,14 +458,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
 #pragma unroll 1
   for (int e = tid; e < all; e += kThreads) {
     const Candidate c = entry(e);
-    if (e < kKept) {
+    if (e < P.kept) {
       s_score[e] = c.score;
       s_place[e] = c.place;
     }
     mine = larger(mine, c.score);
   }
   // (a thread's own, no other's)
-  auto again = [&](int e) { return e < kKept ? Candidate{s_score[e], s_place[e]} : entry(e); };
+  auto again = [&](int e) { return e < P.kept ? Candidate{s_score[e], s_place[e]} : entry(e); };
   const int groups = K <= 8 ? 8 : K <= 16 ? 16 : K <= 32 ? 32 : 64, width = kThreads / groups;
   for (int o = width / 2; o > 0; o /= 2) mine = larger(mine, __shfl_xor_sync(kFullMask, mine, o));
   if (tid % width == 0) s_top[tid / width] = mine;
@@ -444,11 +485,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   collect();
   __syncthreads();
   int found = s_count;
-  if (found > kFound) {
+  const int enough = min(kFound, 4 * K + 64);
+  if (found > enough) {
     // Too many: halve what lies between that bound and the best until the bound leaves few enough.
     uint64_t low = least, high = s_top[0];  // low leaves K or more, high fewer than that or too few
     for (int g = 1; g < groups; g++) high = larger(high, s_top[g]);
-    while (found > kFound && high - low > 1) {
+    while (found > enough && high - low > 1) {
       const uint64_t middle = low + (high - low) / 2;
       int n = 0;
 #pragma unroll 1
@@ -634,6 +676,7 @@ specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t
   const Plan plan(B, W, K, V, dtype == SPECV_F32 ? kStepOf<SPECV_F32> : kStepOf<SPECV_BF16>);
   if (workspace_bytes < plan.total) return SPECV_ERR_WORKSPACE;
   char* base = static_cast<char*>(workspace);
+  const int all = W * K * plan.splits, kept = (all < kKept ? all : kKept) + 1 & ~1;
   const Params P{logits,
                  batch_stride,
                  row_stride,
@@ -645,6 +688,7 @@ specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t
                  tokens,
                  beams,
                  status,
+                 kept,
                  W,
                  V,
                  K,
@@ -662,6 +706,13 @@ specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(B);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kept * (sizeof(uint64_t) + sizeof(uint32_t));
+  if (cfg.dynamicSmemBytes > 16384 &&
+      cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kKept * (sizeof(uint64_t) + sizeof(uint32_t)))) != cudaSuccess) {
+    cudaGetLastError();
+    return SPECV_ERR_CUDA;
+  }
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

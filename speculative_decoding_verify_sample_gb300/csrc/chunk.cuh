@@ -51,9 +51,11 @@ constexpr int kCheckWarp = 17;
 constexpr int kCleanWarp = 18;  // two: look at values that not every row sees
 constexpr int kThreads = 640;
 constexpr int kItems = 4;  // items listed ahead
-// What an item takes besides its key tiles, in their time: its end, and the next
-// one's first scores.
-constexpr int kItemCost = 3;
+// Units of work: a pair's tile is two, a single row tile's one.  What an item takes besides its
+// tiles, its end and the next one's first scores (a mixed batch with 6 and 3, 6 and 5, 6 and 8, 10
+// and 8: 213, 199, 186, 187 us; first chunks with 4, 6, 8, 10, 14 for pairs: 360, 333, 326, 328,
+// 340; a key head to each query head 154, 145, 136, 137, 136):
+constexpr int kPairCost = 8, kSingleCost = 8;
 // Registers a thread of each warpgroup: 2 * 144 + 72 + 2 * 56 <= 480 = 5 * 96, what
 // the block is launched with.  The softmax keeps half a tile's scores of a row in them.
 #define SPECV_CHUNK_REGS_SOFTMAX "144"
@@ -145,9 +147,10 @@ __device__ __forceinline__ Span span_of(const Params& P, const Request& r, int r
   return s;
 }
 
-// An item's units of work: kItemCost and its tiles, a pair's twice.
+// An item's units of work: what it takes besides its tiles, and they.
+__device__ __forceinline__ int cost_of(const Span& s) { return s.rows > kRows ? kPairCost : kSingleCost; }
 __device__ __forceinline__ int units_of(const Span& s) {
-  return (s.tiles + kItemCost) * (s.rows > kRows ? 2 : 1);
+  return cost_of(s) + s.tiles * (s.rows > kRows ? 2 : 1);
 }
 
 __device__ __forceinline__ int row_tiles_of(const Params& P, const Request& r) {
@@ -754,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           span = span_of(P, r, row_tile);
           const int weight = span.rows > kRows ? 2 : 1;
           // its first tile's first unit, and what of its tiles this run has
-          const int64_t first = before + h * head + passed + weight * kItemCost;
+          const int64_t first = before + h * head + passed + cost_of(span);
           auto tile_of = [&](int64_t unit) {
             return static_cast<int>(min(max(unit - first + weight - 1, static_cast<int64_t>(0)) / weight,
                                         static_cast<int64_t>(span.tiles)));
