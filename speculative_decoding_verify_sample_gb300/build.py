@@ -17,7 +17,7 @@ SOURCES = [os.path.join(PKG_DIR, "csrc", name)
            for name in ("specverify.cu", "cache.cu", "attention.cu", "logits.cu", "beams.cu",
                         "chunk.cu", "chunk_bf16.cu", "chunk_f16.cu")]
 HEADERS = [os.path.join(INCLUDE, "specverify.h"),
-           *(os.path.join(PKG_DIR, "csrc", name) for name in ("cache.cuh", "tensor.cuh", "chunk.cuh"))]
+           *(os.path.join(PKG_DIR, "csrc", name) for name in ("cache.cuh", "tensor.cuh", "chunk.cuh", "single.cuh"))]
 LIB_PATH = os.path.join(PKG_DIR, "libspecverify.so")
 BINDING_SOURCE = os.path.join(PKG_DIR, "csrc", "binding.cpp")
 

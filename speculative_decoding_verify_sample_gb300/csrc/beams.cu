@@ -103,14 +103,15 @@ __device__ __forceinline__ float exp_of(float x) {
   return y;
 }
 
-// The vector of a row's entries from `at` on, -inf behind the last.  A row may begin
-// anywhere: then two aligned vectors are shifted together where both lie within the row.
+// The vector of a row's entries from `at` on, -inf behind the last, where it is not one of 16
+// aligned bytes: two such are shifted together where both lie within the row.  (By itself, for
+// its code is seldom needed and long.)
 template <int DT>
-__device__ __forceinline__ uint4 load_vector(const typename Elt<DT>::T* row, int at, int V, int shift) {
+__device__ __noinline__ uint4 load_odd(const typename Elt<DT>::T* row, int at, int V, int shift) {
   using E = Elt<DT>;
   constexpr int kVec = E::kVec, kSize = 16 / kVec;
-  if (at + kVec <= V && shift == 0) return __ldg(reinterpret_cast<const uint4*>(row + at));
   uint4 v = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+  if (at >= V) return v;
   if (at * kSize >= shift && (at + 2 * kVec) * static_cast<int64_t>(kSize) - shift <= V * static_cast<int64_t>(kSize)) {
     const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row + at) - shift);
     const uint4 a = __ldg(from), b = __ldg(from + 1);
@@ -248,14 +249,16 @@ __global__ void __launch_bounds__(kThreads, 3) select_rows_kernel(const Params P
   };
 
   const int begin = split * P.steps * kWarps * kStep;
+  const int whole = shift ? 0 : P.V;  // entries in aligned vectors
   uint4 next[2][kVecs];  // of this step and the one behind it
   auto first_of = [&](int step) { return begin + (step * kWarps + warp) * kStep; };
   auto fetch = [&](int step, uint4 (&to)[kVecs]) {
 #pragma unroll
     for (int j = 0; j < kVecs; j++) {
       const int e = first_of(step) + (j * 32 + lane) * kVec;
-      to[j] = step < P.steps && e < P.V ? load_vector<DT>(from, e, P.V, shift)
-                                        : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+      if (step < P.steps && e + kVec <= whole) to[j] = __ldg(reinterpret_cast<const uint4*>(from + e));
+      else to[j] = step < P.steps && e < P.V ? load_odd<DT>(from, e, P.V, shift)
+                                             : make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
     }
   };
   fetch(0, next[0]);

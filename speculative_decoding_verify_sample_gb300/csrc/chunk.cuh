@@ -1336,6 +1336,16 @@ cudaError_t launch(const Params& P, const CUtensorMap& k_map, const CUtensorMap&
   return cudaLaunchKernelEx(&cfg, join_kernel<E, DP>, P);
 }
 
+// Whether the call is for the small kernel (single.cuh): no request has more than one token, a key
+// head no more than 16 rows, and there are few key heads' slots (their lengths are on the device:
+// what the page table or the window has room for stands for them).
+inline bool singles(const Params& P) {
+  const int64_t heads = static_cast<int64_t>(P.B) * P.cache.heads;
+  const int64_t slots = static_cast<int64_t>(P.cache.max_pages) * P.cache.page_size;
+  return P.longest == 1 && P.group <= 16 && heads <= kSms / 2 &&
+         heads * (slots < P.window ? slots : P.window) <= 65536;
+}
+
 // One translation unit for each type of the cache.
 template <class E>
 cudaError_t run(const Params& P, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);

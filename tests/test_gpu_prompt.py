@@ -102,6 +102,102 @@ def test_attention(sv, dtype, shape, mod):  # noqa: F811
         sv, longest=max(new) if mod % 2 else None)
 
 
+SINGLES = [  # new, lens, Hq, Hkv, D, page: no request with more than one token
+    ([1], [0], 1, 1, 8, 16),
+    ([1, 0, 1], [1, 70, 63], 16, 1, 128, 16),        # sixteen rows, 64 slots
+    ([1, 1], [64, 511], 17, 1, 64, 8),               # one row more than the small kernel takes
+    ([1, 1, 1], [4001, 0, 2500], 32, 8, 128, 16),
+    ([1], [4001], 32, 8, 128, 16),
+    ([1], [8191], 16, 4, 64, 32),
+    ([0, 1, 1], [5, 999, 513], 14, 2, 80, 24),
+    ([1, 1], [3000, 130], 6, 3, 96, 1),
+    ([1] * 5, [40, 700, 5, 1, 3000], 9, 3, 24, 100),
+    ([1, 1], [7000, 12], 8, 8, 112, 64),
+    ([1, 1], [777, 63], 11, 1, 40, 7),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("shape", range(len(SINGLES)))
+@pytest.mark.parametrize("mod", range(len(MODS)))
+def test_attention_single_tokens(sv, dtype, shape, mod):  # noqa: F811
+    new, lens, Hq, Hkv, D, page = SINGLES[shape]
+    kw = dict(MODS[mod])
+    if "prefix" in kw:
+        kw["prefix"] = [max(0, kw["prefix"] - b) for b in range(len(new))]
+    Attn(37 * shape + mod, new, lens, Hq, Hkv, D, page, dtype, spare=2 * (shape % 2), **kw).check(sv, longest=1)
+
+
+@pytest.mark.parametrize("layout", ["heads", "pairs"])
+def test_attention_single_tokens_of_many_requests(sv, layout):  # noqa: F811
+    """Clusters of eight CTAs, of four and of two, and more requests than the small kernel takes."""
+    rng = np.random.default_rng(4)
+    for B, most in ((8, 900), (16, 900), (38, 700), (39, 700), (700, 150)):
+        new, lens = [int(x) for x in rng.integers(0, 2, B)], [int(x) for x in rng.integers(0, most, B)]
+        Attn(B, new, lens, 8, 2, 64, 16, F16, window=200, prefix=[3] * B, layout=layout).check(sv, longest=1)
+
+
+def test_attention_single_tokens_flagged_and_repeated(sv):  # noqa: F811
+    a = Attn(79, [1, 1, 1, 1], [300, 40, 900, 12], 8, 2, 128, 16, BF16, window=500)
+    args = a.args()
+    want, status = sv.chunk_attention(*args, longest=1, **a.kw())
+    assert status.tolist() == [0] * 4
+
+    def call(lens=a.lens, cu=a.cu, table=a.table):
+        out = torch.full_like(a.q, 7.0)
+        _, status = sv.chunk_attention(a.q, a.k, a.v, table, i32(lens), i32(cu), window=500, longest=1, out=out)
+        return out, status.tolist()
+
+    for bad_page in (-1, 10 ** 6, 2 ** 31 - 1):
+        for at in (401 // 16, 900 // 16):  # the window's first page, and the last
+            table = a.table.clone()
+            table[2, at] = bad_page
+            out, status = call(table=table)
+            assert status == [0, 0, sv.DEV_BAD_CACHE, 0] and (out[2] == 0).all()
+            assert torch.equal(out[[0, 1, 3]], want[[0, 1, 3]])
+    for lens in ([300, -1, 900, 12], [300, 10 ** 6, 900, 12], [300, 2 ** 31 - 1, 900, 12]):
+        out, status = call(lens=lens)
+        assert status == [0, sv.DEV_BAD_CACHE, 0, 0] and (out[1] == 0).all()
+        assert torch.equal(out[[0, 2, 3]], want[[0, 2, 3]])
+    out, status = call(cu=[0, 1, 3, 4, 4])  # two tokens where one was said
+    assert status == [0, sv.DEV_BAD_DRAFT_LEN, 0, 0] and (out[1:3] == 0).all() and torch.equal(out[0], want[0])
+    out, status = call(cu=[0, 1, 10 ** 6, 3, 4])
+    assert status == [0, sv.DEV_BAD_DRAFT_LEN, sv.DEV_BAD_DRAFT_LEN, 0] and (out[1:3] == 7.0).all()
+    # the same on another stream, and in a graph over other lengths
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got, _ = sv.chunk_attention(*args, longest=1, stream=side, **a.kw())
+    side.synchronize()
+    assert torch.equal(got, want)
+    out, status = torch.zeros_like(a.q), i32([9] * 4)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sv.chunk_attention(*args, longest=1, out=out, status=status, window=500)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and status.tolist() == [0] * 4
+    args[4].copy_(i32([100, 20, 900, 2]))  # places that hold values, pages that exist
+    g.replay()
+    torch.cuda.synchronize()
+    fresh, status = sv.chunk_attention(*args, longest=1, window=500)
+    assert torch.equal(out, fresh) and status.tolist() == [0] * 4
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_attention_single_tokens_hidden_places_hold_anything(sv, bad):  # noqa: F811
+    a = Attn(83, [1, 1], [90, 333], 4, 2, 64, 32, BF16, window=70, prefix=[5, 40])
+    for b, slots in ((0, (6, 20, 21)), (1, (41, 200, 263))):  # behind the prefix, before the window
+        for at in slots:
+            page = a.table[b, at // 32]
+            if page >= 0:
+                a.k[page.long(), at % 32] = bad
+                a.v[page.long(), at % 32] = bad
+    a.check(sv, longest=1)
+    at = 333  # its own: seen
+    a.v[a.table[1, at // 32].long(), at % 32, 0, 3] = bad
+    a.check(sv, longest=1)
+
+
 @pytest.mark.parametrize("page", [2, 12, 40, 48, 96, 136, 384])
 @pytest.mark.parametrize("layout", ["rows", "heads", "pairs"])
 def test_attention_pages_and_layouts(sv, page, layout):  # noqa: F811
