@@ -578,7 +578,8 @@ size_t specv_chunk_workspace_bytes(int longest, int q_heads, int kv_heads, int h
  *   longest   no request has more tokens (T will do; the work is laid out
  *             for it); longest * q_heads / heads < 2^29.
  *   scale     > 0 (1/sqrt(head_dim) as a rule).
- *   cap       > 0, or 0: scores are not capped.
+ *   cap       > 0 (and 2 scale / cap between 1e-30 and 1e30), or 0: scores are
+ *             not capped.
  *   window    >= 1, or 0: no limit.
  *   prefix_lens [B] int32 >= 0 (else SPECV_DEV_BAD_CACHE), or NULL: 0.  The
  *             part of it that lens[b] and the tokens do not reach is not there.

@@ -602,7 +602,7 @@ struct Moved {
 struct MoveParams {
   const int32_t* beams;
   int32_t* status;
-  int W, K, states;
+  int B, W, K, states;
   Moved state[SPECV_MAX_STATES];
 };
 
@@ -627,6 +627,7 @@ __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(const __grid_cons
   __shared__ int s_beams[kMaxBeams];
   const int tid = threadIdx.x;
   const int64_t b = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 32768;
+  if (b >= P.B) return;
   bool bad = false;
   if (tid < P.K) {
     const int w = P.beams[b * P.K + tid];
@@ -736,6 +737,7 @@ specv_status spec_reorder_beams(const int32_t* beams, int B, int W, int K, const
   MoveParams P;
   P.beams = beams;
   P.status = status;
+  P.B = B;
   P.W = W;
   P.K = K;
   P.states = num_states;

@@ -84,20 +84,23 @@ specv_status spec_chunk_attention(const specv_cache* cache, const specv_rows* q,
   if (box_rows && (!tensor_map(&k_map, cache, cache->k, box_rows) ||
                    !tensor_map(&v_map, cache, cache->v, box_rows)))
     box_rows = 0;
-  // cap tanh(z) in units of log 2 as score * poly(score^2), for |z| <= 0.6 (chunk.cuh)
+  // cap tanh(z) in units of log 2 as score * poly(score^2), for |z| <= 0.6 (chunk.cuh).  Where a cap
+  // is so large that the last coefficients are no 32-bit numbers, they are left out, and |z| is
+  // bounded by what they are less than 2^-24 of the value for.
   static const double kTanh[5] = {0.9999999268676429, -0.33332309962801215, 0.13310173497792807,
                                   -0.05210147302447307, 0.015475417666045245};
+  static const double kBound[5] = {4e-4, 0.026, 0.1, 0.2, 0.6};
   float poly[5] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, small = -1.0f;
   if (cap > 0.0f) {
     const double z = static_cast<double>(scale) / cap;
     double power = 1.4426950408889634 * cap * z;
-    bool fits = true;
     for (int i = 0; i < 5; i++, power *= z * z) {
-      poly[i] = static_cast<float>(kTanh[i] * power);
-      fits = fits && std::fabs(poly[i]) > 1e-35 && std::fabs(poly[i]) < 1e35;
+      const double k = kTanh[i] * power, bound = kBound[i] / z;
+      // (a square of a score up to the bound is a number, too)
+      if (std::fabs(k) < 1e-35 || std::fabs(k) > 1e35 || bound > 1e18) break;
+      poly[i] = static_cast<float>(k);
+      small = static_cast<float>(bound);
     }
-    // (a square of a score up to here is a number, too)
-    if (fits && 0.6 / z < 1e18) small = static_cast<float>(0.6 / z);
   }
   const Params P{to_cache(cache),
                  to_rows(q),

@@ -317,11 +317,19 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t twice(float x) { return pair_of(__float_as_uint(x), __float_as_uint(x)); }
 
-// Half a tile's products become capped scores in units of log 2:
-// cap tanh z, z = scale x / cap: for |z| <= 0.6 in all of the warp's rows, which scores rarely
-// leave, by z times a polynomial in z^2 (fitted to tanh(z) / z by least squares, reweighted
-// until its largest error, 2^-23.7 of the value, is about even), six instructions for two; else as
-// cap (1 - 2 / (1 + e^2z)), 2^-22 of the cap off, two of the slow functions for one.
+// cap tanh z, z = scale x / cap, in units of log 2: for |z| <= 0.6 z times a polynomial in z^2
+// (fitted to tanh(z) / z by least squares, reweighted until its largest error, 2^-23.7 of the
+// value, is about even), else cap (1 - 2 / (1 + e^2z)), within 2^-20 of the value there.
+__device__ __forceinline__ float capped(const Params& P, float x) {
+  const float u = x * x;
+  const float near = x * fmaf(u, fmaf(u, fmaf(u, fmaf(u, P.cap_poly[4], P.cap_poly[3]), P.cap_poly[2]),
+                                      P.cap_poly[1]), P.cap_poly[0]);
+  const float far = fmaf(rcp_of(exp2_of(x * P.cap_turn) + 1.0f), -2.0f * P.cap_log2, P.cap_log2);
+  return fabsf(x) <= P.cap_small ? near : far;
+}
+
+// Half a tile's products become capped scores.  Those of a warp's rows rarely leave the
+// polynomial, which is six instructions for two of them; where they do, both forms are taken.
 __device__ __forceinline__ void cap_scores(const Params& P, uint32_t (&x)[kHalf]) {
   float most[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -340,9 +348,7 @@ __device__ __forceinline__ void cap_scores(const Params& P, uint32_t (&x)[kHalf]
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < kHalf; e++)
-      x[e] = __float_as_uint(fmaf(rcp_of(exp2_of(__uint_as_float(x[e]) * P.cap_turn) + 1.0f),
-                                  -2.0f * P.cap_log2, P.cap_log2));
+    for (int e = 0; e < kHalf; e++) x[e] = __float_as_uint(capped(P, __uint_as_float(x[e])));
   }
 }
 

@@ -194,11 +194,7 @@ __global__ void __launch_bounds__(kOneWarps * 32, 1) single_kernel(const Params 
 #pragma unroll
         for (int k = 0; k < 2; k++) {
           float y = x[n][2 * k + e];
-          // cap tanh z = cap (1 - 2 / (1 + e^2z)): 2^-22 of the cap off, whatever z is
-          if (P.cap_log2 > 0.0f)
-            y = fmaf(rcp_of(exp2_of(y * P.cap_turn) + 1.0f), -2.0f * P.cap_log2, P.cap_log2);
-          else
-            y *= P.scale_log2;
+          y = P.cap_log2 > 0.0f ? capped(P, y) : y * P.scale_log2;
           y = fmaf(-slope[k], away, y);
           if (i >= count) y = -INFINITY;
           x[n][2 * k + e] = y;

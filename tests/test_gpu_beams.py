@@ -240,6 +240,26 @@ def test_reorder_flags_bad_requests(sv):  # noqa: F811
     assert torch.equal(out[0], x[0, [0, 3]]) and (out[1:] == 7.0).all()
 
 
+def test_reorder_many_requests(sv):  # noqa: F811
+    """More requests than one axis of a grid has here: none behind the last is looked at."""
+    B = 32768 + 5
+    rng = np.random.default_rng(2)
+    beams = rng.integers(-1, 3, (B, 2))
+    x = normal(7, B, 3, 5)
+    out = torch.zeros(B, 2, 5, device="cuda")
+    status = torch.full((B + 64,), 9, dtype=torch.int32, device="cuda")
+    _, flags = sv.reorder_beams(i32(beams), x, out=out, status=status[:B])
+    torch.cuda.synchronize()
+    at = torch.as_tensor(beams).cuda()
+    want = torch.where(at[:, :, None] >= 0, x.gather(1, at.clamp(min=0)[:, :, None].expand(B, 2, 5)), 0.0)
+    assert torch.equal(out, want) and (flags == 0).all() and (status[B:] == 9).all()
+
+
+def test_select_many_requests(sv):  # noqa: F811
+    z, scores = normal(31, 5000, 2, 33, dtype=BF16), totals(31, 5000, 2)
+    check(sv, z, scores, 3)
+
+
 def test_reorder_strides_streams_and_graphs(sv):  # noqa: F811
     layers = normal(3, 4, 3, 5, 64, dtype=BF16)  # [layers, B, W, ...]: a state to each
     beams = i32([[1, 1, 0, 4, 2], [4, 3, 2, 1, 0], [-1, 0, 0, 0, 0]])

@@ -228,6 +228,21 @@ def test_attention_flat_and_sharp_scores(sv, sharp, cap):  # noqa: F811
     Attn(13, [200, 3], [300, 900], 8, 2, 128, 64, F16, sharp=sharp, cap=cap).check(sv)
 
 
+@pytest.mark.parametrize("longest", [1, 70])
+@pytest.mark.parametrize("cap", [0.5, 8.0, 1000.0, 1e6])
+def test_attention_caps(sv, cap, longest):  # noqa: F811
+    """Scores far below the cap, about it and far above; a large cap costs no precision."""
+    a = Attn(19, [1, 1] if longest == 1 else [70, 1], [300, 901], 4, 2, 64, 32, F16, sharp=3.0, cap=cap)
+    at = 120  # one key much larger than all others, which sees only few scores near the cap
+    a.k[a.table[0, at // 32].long(), at % 32] *= 40
+    a.check(sv, longest=longest)
+    want, _ = a.want()
+    got, _ = sv.chunk_attention(*a.args(), longest=longest, **a.kw())
+    rel = ((got.double() - want).norm() / want.norm()).item()
+    # the output's and the weights' roundings to f16, 2^-11 of a value each, with half as much again
+    assert rel < 1.5 * 2.0 ** -10, rel
+
+
 def test_attention_rising_maxima(sv):  # noqa: F811
     """Every tile has larger scores than the one before, so every one scales the sums again."""
     a = Attn(17, [150], [1000], 2, 2, 64, 32, BF16, scale=1.0)
