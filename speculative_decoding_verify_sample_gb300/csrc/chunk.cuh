@@ -644,9 +644,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool going = true, first = true;
       uint32_t q_at = base;
       if (scores) {
-          const uint32_t tile = queries + (pair ? st : 0);
+        // (Both streams' warps wait for all of an item's tiles and give all back.  One that waited for
+        // its own alone could go through a short item and give a tile back before it was even
+        // loaded, for the other's warp.)
+        for (uint32_t tile = queries; tile < queries + (pair ? 2 : 1) && going; tile++)
           going = wait(&s.q_full[tile & 1], tile / 2 & 1);
-          q_at += (tile & 1) * S::kQueryBytes;
+        if (!going) break;
+        q_at += ((queries + (pair ? st : 0)) & 1) * S::kQueryBytes;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       uint32_t stage = 0, stage_at = 0;
@@ -957,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key0 = halves.key(i);
         const uint32_t place = scored & 1, use = scored / 2;
         if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.s_full[st][place]), use & 1, gave_up))) break;
+        __syncwarp();  // (lanes may leave a wait apart, and tensor memory is read by whole warps)
         tmem_fence_after();
         const bool first = taken++ == 0;
         if (working) {
@@ -1047,6 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t last = scored - 1;
               if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.o_full[st][last & 1]), last / 2 & 1, gave_up)))
                 break;
+              __syncwarp();
               tmem_fence_after();
               l *= by;
 #pragma unroll 1
@@ -1060,6 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           l += sum;
+          __syncwarp();
           tmem_store32(at_s, p);  // over scores of this row, all read
           tmem_store_wait();
         }
@@ -1089,6 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_fence_after();
       barrier_wait(smem_of(&s.item_checked[items % kItems]), items / kItems & 1, gave_up);
       const bool bad = __any_sync(kFullMask, w.bad != 0 || *gave_up);  // unchecked is bad
+      __syncwarp();
       // A pair: this stream's rows, all columns; else half of the columns of both streams' sum
       const int my_rows = rows - first_row;
       if (quarter * 32 < my_rows && !(bad && !w.begins)) {
@@ -1130,6 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t x[32];
             if (!(i ? took[1] : took[0])) continue;
             const float by = (i ? weight[1] : weight[0]) * inv;
+            __syncwarp();
             tmem_load32(tmem + 256 + i * DP + lanes + k, x);
 #pragma unroll
             for (int e = 0; e < 32; e++) o[e] = fmaf(__uint_as_float(x[e]), by, o[e]);

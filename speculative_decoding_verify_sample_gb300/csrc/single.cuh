@@ -49,6 +49,7 @@ __device__ __forceinline__ void load_transposed(uint32_t at, uint32_t (&x)[4]) {
 }
 
 __device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // A number in the shared memory of the cluster's CTA `rank`, at this CTA's address `at`.

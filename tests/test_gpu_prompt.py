@@ -692,79 +692,3 @@ def test_a_prompt_in_chunks_then_a_drafted_chain(sv, dtype):  # noqa: F811
     close(out.flatten(0, 1), want, tol)
     chunk, _ = sv.chunk_attention(rotated.flatten(0, 1), kc, vc, table, i32(lens), i32([0, 5, 10]))
     close(chunk, want, tol)
-
-
-# ------------------------------------------------------------ waits that run out
-
-
-WAITS = (0, 2000, 6000, 12000, 25000)  # ns
-
-
-@pytest.fixture(scope="module")
-def impatient(sv, tmp_path_factory):  # noqa: F811
-    """The attention with waits so short that they run out, by their length: functions like
-    chunk_attention of a case and an output, that return the status."""
-    import ctypes
-    import importlib
-    import struct
-    import subprocess
-
-    from speculative_decoding_verify_sample_gb300 import _native
-
-    how = importlib.import_module("speculative_decoding_verify_sample_gb300.build")
-    where = tmp_path_factory.mktemp("impatient")
-    sources = [x for x in how.SOURCES if "chunk" in x]
-    builds = [subprocess.Popen([how.nvcc_path(), *how.ARCH_FLAGS, "-O3", "-std=c++17", "-I", how.INCLUDE,
-                                "-shared", "-Xcompiler", "-fPIC", "-cudart", "shared", "--threads", "3",
-                                f"-DSPECV_ATTENTION_WAIT_NS={ns}ull", "-o", str(where / f"{ns}.so"), *sources])
-              for ns in WAITS]
-    assert [b.wait() for b in builds] == [0] * len(WAITS)
-
-    def bind(ns):
-        fn = ctypes.CDLL(str(where / f"{ns}.so")).spec_chunk_attention
-        fn.restype, fn.argtypes = _native.SIGNATURES["spec_chunk_attention"]
-
-        def call(a, args, out, ws):
-            q, k, v, table, lens, cu = args
-            status = i32([-1] * a.B)  # whatever was there
-            cache = struct.pack("@4P4q8i", k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), 0,
-                                *k.stride()[:3], 1, k.shape[0], k.shape[1], table.shape[1], table.stride(0),
-                                k.shape[2], a.D, 1 if a.dtype == BF16 else 2)
-            rows = [struct.pack("@P3q", t.data_ptr(), 0, *t.stride()[:2]) for t in (q, out)]
-            assert fn(cache, rows[0], cu.data_ptr(), a.B, q.shape[0], max(a.new), a.Hq, a.D ** -0.5, 0.0,
-                      a.window or 0, None, None, rows[1], status.data_ptr(), ws.tensor.data_ptr(), ws.nbytes,
-                      torch.cuda.current_stream().cuda_stream) == 0
-            torch.cuda.synchronize()
-            return status.tolist()
-
-        return call
-
-    return {ns: bind(ns) for ns in WAITS}
-
-
-GIVE_UP = [  # new, lens, Hq, Hkv, D, page, window
-    ([5, 1, 3], [3000, 12, 700], 8, 2, 128, 64, None),         # tensor copies
-    ([5, 1, 3], [3000, 12, 700], 8, 2, 128, 8, None),          # copies of 16 bytes
-    ([300, 700], [2000, 900], 16, 2, 128, 64, None),           # pairs of row tiles
-    ([300, 1], [2000, 900], 16, 2, 64, 12, 500),
-    ([i % 5 for i in range(40)], [100 * (i % 7) for i in range(40)], 8, 2, 64, 32, None),
-]
-
-
-@pytest.mark.parametrize("new,lens,Hq,Hkv,D,page,window", GIVE_UP)
-def test_attention_gives_up_and_leaves_the_device_usable(sv, impatient, new, lens, Hq, Hkv, D, page, window):  # noqa: F811
-    """Every status is written.  If a wait ran out anywhere, all of them say so; if none did, the rows
-    are right.  Wherever its waits run out the call ends, and those behind it are right."""
-    a = Attn(71, new, lens, Hq, Hkv, D, page, BF16, window=window)
-    args, ws = a.args(), sv.ChunkWorkspace(max(new), Hq, Hkv, D, device="cuda")
-    want, _ = sv.chunk_attention(*args, window=window, longest=max(new))
-    for ns in WAITS:
-        for _ in range(3):
-            out = torch.zeros_like(a.q)
-            status = impatient[ns](a, args, out, ws)
-            if ns == 0 or any(status):
-                assert status == [sv.DEV_TIMEOUT] * a.B, ns
-            else:
-                assert torch.equal(out, want), ns
-            got, status = sv.chunk_attention(*args, workspace=ws, window=window, longest=max(new))
-            assert torch.equal(got, want) and status.tolist() == [0] * a.B
