@@ -8,6 +8,14 @@
 // has the rows' sums, turns the parts' entries into scores and takes the K best of them.
 // Each logit is read once, and only the few that may be among the best leave the
 // registers.
+//
+// Measured: 64 requests of 8 beams over 128,256 32-bit entries, a part of them ended, 64 to 66
+// us (210 MB, 3.2 TB/s); one request of 8 over 16-bit entries 19 to 20; a single row of 1,024
+// entries 12.4, two kernels' latencies.  In an earlier form of 98 us the batch took 59 without
+// the search for the best and 51 without the exponentials as well: the latter is what reading
+// costs with the 24 warps to an SM that the registers leave.  32 requests of 16 beams, K = 16, 16 bits:
+// 93 us; 8 of 64 over 50,000, K = 64: 223, nearly all of it the search.  The reordering of 64 requests of 8
+// beams, 46 MB read and written, 8.4 to 10.5 us, of one 4.
 
 #include <cuda_runtime.h>
 #include <limits.h>

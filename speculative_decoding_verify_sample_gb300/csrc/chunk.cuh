@@ -19,8 +19,30 @@
 // join_kernel.
 //
 // Two streams share an SM, each with its S and O in TMEM and its four softmax
-// warps: an item of more than 128 rows is a pair of row tiles on the same keys,
-// one of fewer takes its key tiles in turn and is joined at the end.
+// warps: an item of more than 128 rows is a pair of row tiles on the same keys, one of
+// fewer shares its half tiles out to both and is joined at the end.  A stream's scores are
+// taken half a tile (64 keys) at a time into two places in turn, so that the tensor cores
+// can have the next half's scores done when the softmax has done with one.  The price:
+// products of 64 keys read the queries from shared memory as often as those of 128, and two
+// streams' scores and sums of a tile take the tensor cores 2,478 cycles in place of 2,050 (the
+// MMAs alone, timed); tensor memory has no room for two whole tiles of scores and the sums.
+// Besides the softmax there are four warps that copy, a warp to each stream's scores and one to
+// its sums, one that lists the run's work, one that checks the requests' data and two
+// that clean values.
+//
+// Measured (D = 128 and 32 + 8 heads but where said), calls back to back:
+// 4,093 tokens behind 28,673 slots 1,430 to 1,443 us (1,430 TFLOP/s);
+// six prompts of 517 to 4,093 tokens 326 us (1,030 TFLOP/s).  With clocks read in the
+// kernel a softmax warp of this case has 22 halves to an item, each 150 cycles before its wait, 490
+// in it and 950 at work, and 8,000 cycles at an item's ends, 5,200 of them writing (without the
+// writes 315 us);
+// 48 requests of 1 to 257 tokens and a window, f16, 186 us;
+// 48 single tokens over 27,000 slots each 780 us (6.8 TB/s);
+// capped scores, 16 + 8 heads, 287 to 295 us for 202 GFLOP: the polynomial's
+// products come on top of each score's exponential;
+// a bias by distance, 16 + 16 heads of 64, 137 to 154 us for 49 GFLOP (116 without the bias).
+// The second kernel takes 18 to 32 us of the calls of many items: its 197 registers to a thread
+// leave an SM one block.
 #pragma once
 
 #include <cuda.h>
