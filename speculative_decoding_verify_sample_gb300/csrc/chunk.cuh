@@ -41,7 +41,7 @@
 // capped scores, 16 + 8 heads, 287 to 295 us for 202 GFLOP: the polynomial's
 // products come on top of each score's exponential;
 // a bias by distance, 16 + 16 heads of 64, 137 to 154 us for 49 GFLOP (116 without the bias).
-// The second kernel takes 18 to 32 us of the calls of many items: its 197 registers to a thread
+// The second kernel takes 18 to 41 us where items are many (under a profiler): its 197 registers to a thread
 // leave an SM one block.
 #pragma once
 
