@@ -147,7 +147,7 @@ __device__ __forceinline__ Request request_of(const Params& P, int b) {
 }
 
 // The first slot in the window of the token at pos.
-__device__ __forceinline__ int lowest(const Params& P, int pos) {
+__host__ __device__ __forceinline__ int lowest(const Params& P, int pos) {
   return P.window > pos ? 0 : pos - P.window + 1;
 }
 
@@ -157,7 +157,7 @@ struct Span {
   int rows, pos0, pos1, tiles, gap, skip;
 };
 
-__device__ __forceinline__ Span span_of(const Params& P, const Request& r, int row_tile) {
+__host__ __device__ __forceinline__ Span span_of(const Params& P, const Request& r, int row_tile) {
   Span s;
   const int all = r.n * P.group, at = row_tile * kRowTile;
   s.rows = min(kRowTile, all - at);
@@ -271,7 +271,7 @@ struct Item {
 struct Keys {
   int tiles, last, gap, skip, prefix, pos0, pos1, low0, low1;
 
-  __device__ __forceinline__ explicit Keys(const Item& w)
+  __host__ __device__ __forceinline__ explicit Keys(const Item& w)
       : tiles(w.t1 - w.t0), last(w.t1 - 1), gap(w.gap), skip(w.skip), prefix(w.prefix), pos0(w.pos0),
         pos1(w.pos1), low0(w.low0), low1(w.low1) {}
   // Makes them known to be the same in every lane.
@@ -280,7 +280,7 @@ struct Keys {
       *x = __shfl_sync(kFullMask, *x, 0);
   }
   // The first key of the i-th tile taken.
-  __device__ __forceinline__ int first(int i) const {
+  __host__ __device__ __forceinline__ int first(int i) const {
     const int t = last - i;
     return (t < gap ? t : t + skip) * kKeys;
   }
@@ -295,7 +295,7 @@ struct Keys {
 struct Halves {
   int total, turn, top, top2;
 
-  __device__ __forceinline__ Halves(const Keys& k, int t0) {
+  __host__ __device__ __forceinline__ Halves(const Keys& k, int t0) {
     const int t1 = t0 + k.tiles;
     const int own = (k.prefix + kHalf - 1) / kHalf;  // of the prefix
     int low = k.low0 / kHalf, high = k.pos1 / kHalf;
@@ -311,8 +311,18 @@ struct Halves {
     total = turn + (joined ? 0 : max(0, last - 2 * t0 + 1));
     top2 = last * kHalf;
   }
-  __device__ __forceinline__ int key(int i) const {
+  __host__ __device__ __forceinline__ int key(int i) const {
     return i < turn ? top - i * kHalf : top2 - (i - turn) * kHalf;
+  }
+  // How many of them stream st takes: all of a pair's, of one row tile's every other one.
+  __host__ __device__ __forceinline__ int taken(bool pair, int st) const {
+    return pair ? total : (total + 1 - st) / 2;
+  }
+  // Whether stream st's sums are in the rows that stream `of_rows` writes at the item's end.  Made of
+  // what all lanes know alike, for tensor memory is read by whole warps; and of an item that is
+  // flagged, or behind a wait that gave up, nothing is read.
+  __host__ __device__ __forceinline__ bool summed(bool pair, int of_rows, int st, bool bad) const {
+    return !bad && (!pair || of_rows == st) && taken(pair, st) > 0;
   }
 };
 
@@ -986,6 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();  // (lanes may leave a wait apart, and tensor memory is read by whole warps)
         tmem_fence_after();
         const bool first = taken++ == 0;
+        bool going = true;  // the same on every lane
         if (working) {
           const uint32_t at_s = tS[st] + lanes + place * kHalf;
           uint32_t x[kHalf];
@@ -1072,8 +1083,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!first) {
               // the last update of O must be done
               const uint32_t last = scored - 1;
-              if (!__all_sync(kFullMask, barrier_wait(smem_of(&s.o_full[st][last & 1]), last / 2 & 1, gave_up)))
-                break;
+              going = __all_sync(kFullMask, barrier_wait(smem_of(&s.o_full[st][last & 1]), last / 2 & 1, gave_up));
+              if (!going) break;
               __syncwarp();
               tmem_fence_after();
               l *= by;
@@ -1087,6 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+          if (!going) break;
           l += sum;
           __syncwarp();
           tmem_store32(at_s, p);  // over scores of this row, all read
@@ -1099,21 +1111,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // The item's end: this stream's last sum, and where both have parts of the rows the
-      // other's too.
+      // other's too.  (Whichever of these waits gave up, in whichever lane, `bad` says so in all of them:
+      // then neither the other's numbers nor tensor memory are read, for they may not be there.)
       if (taken) {
         const uint32_t last = scored - 1;
         barrier_wait(smem_of(&s.o_full[st][last & 1]), last / 2 & 1, gave_up);
       }
-      int other_taken = 0;
-      float2 other = make_float2(-INFINITY, 0.0f);
       if (!pair) {
-        s.stats[st][row] = make_float2(m, taken ? l : -1.0f);
+        s.stats[st][row] = make_float2(m, l);
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) barrier_arrive(smem_of(&s.joined));
         barrier_wait(smem_of(&s.joined), shared & 1, gave_up);
-        other = s.stats[st ^ 1][row];
-        other_taken = other.y >= 0.0f || other.y != other.y;
       }
       tmem_fence_after();
       barrier_wait(smem_of(&s.item_checked[items % kItems]), items / kItems & 1, gave_up);
@@ -1123,8 +1132,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int my_rows = rows - first_row;
       if (quarter * 32 < my_rows && !(bad && !w.begins)) {
         float weight[2] = {1.0f, 1.0f};
-        const bool took[2] = {st && !pair ? other_taken != 0 : taken != 0, st || pair ? taken != 0 : other_taken != 0};
-        if (!pair) {
+        const bool took[2] = {halves.summed(pair, st, 0, bad), halves.summed(pair, st, 1, bad)};
+        if (!pair && !bad) {
+          const float2 other = s.stats[st ^ 1][row];
           const float m_of[2] = {st ? other.x : m, st ? m : other.x};
           const float l_of[2] = {st ? other.y : l, st ? l : other.y};
           m = fmaxf(m_of[0], m_of[1]);
