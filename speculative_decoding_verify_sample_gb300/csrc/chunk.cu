@@ -1,7 +1,5 @@
 // The prompt's pass over the paged cache, host side of its attention.
 
-#include <cmath>
-
 #include "chunk.cuh"
 
 using namespace specv_chunk;
@@ -63,8 +61,8 @@ specv_status spec_chunk_attention(const specv_cache* cache, const specv_rows* q,
     return SPECV_ERR_INVALID_ARG;
   const int group = q_heads / cache->heads;
   if (q_heads > 1024 || B > kMaxRequests || too_long(longest, group)) return SPECV_ERR_UNSUPPORTED;
-  // the scores' factor and its twice in the cap's tanh, as 32-bit numbers
-  const double turn = cap > 0.0f ? 2.0 * scale / cap * 1.4426950408889634 : 0.0;
+  // the scores' factor in the cap's tanh, a 32-bit number as what follows from it is
+  const double unit = cap > 0.0f ? static_cast<double>(scale) / cap : 0.0, turn = 2.0 * unit * 1.4426950408889634;
   if (turn > 1e30 || (cap > 0.0f && turn < 1e-30)) return SPECV_ERR_INVALID_ARG;
   const Plan plan(longest, group, cache->head_dim);
   if (workspace_bytes < plan.total) return SPECV_ERR_WORKSPACE;
@@ -84,24 +82,12 @@ specv_status spec_chunk_attention(const specv_cache* cache, const specv_rows* q,
   if (box_rows && (!tensor_map(&k_map, cache, cache->k, box_rows) ||
                    !tensor_map(&v_map, cache, cache->v, box_rows)))
     box_rows = 0;
-  // cap tanh(z) in units of log 2 as score * poly(score^2), for |z| <= 0.6 (chunk.cuh).  Where a cap
-  // is so large that the last coefficients are no 32-bit numbers, they are left out, and |z| is
-  // bounded by what they are less than 2^-24 of the value for.
+  // cap tanh(z) in units of log 2 as z * poly(z^2), for |z| <= 0.6 (chunk.cuh).
   static const double kTanh[5] = {0.9999999268676429, -0.33332309962801215, 0.13310173497792807,
                                   -0.05210147302447307, 0.015475417666045245};
-  static const double kBound[5] = {4e-4, 0.026, 0.1, 0.2, 0.6};
-  float poly[5] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, small = -1.0f;
-  if (cap > 0.0f) {
-    const double z = static_cast<double>(scale) / cap;
-    double power = 1.4426950408889634 * cap * z;
-    for (int i = 0; i < 5; i++, power *= z * z) {
-      const double k = kTanh[i] * power, bound = kBound[i] / z;
-      // (a square of a score up to the bound is a number, too)
-      if (std::fabs(k) < 1e-35 || std::fabs(k) > 1e35 || bound > 1e18) break;
-      poly[i] = static_cast<float>(k);
-      small = static_cast<float>(bound);
-    }
-  }
+  float poly[5];
+  for (int i = 0; i < 5; i++) poly[i] = static_cast<float>(kTanh[i] * cap * 1.4426950408889634);
+  const float small = cap > 0.0f ? static_cast<float>(0.6 / unit) : 0.0f;
   const Params P{to_cache(cache),
                  to_rows(q),
                  to_rows(out),
@@ -121,7 +107,7 @@ specv_status spec_chunk_attention(const specv_cache* cache, const specv_rows* q,
                  box_rows,
                  scale * 1.4426950408889634f,
                  cap * 1.4426950408889634f,
-                 static_cast<float>(turn),
+                 static_cast<float>(unit),
                  small,
                  {poly[0], poly[1], poly[2], poly[3], poly[4]}};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -116,9 +116,9 @@ struct Params {
   int part_rows;                      // rows of a piece in the workspace
   int box_rows;                       // rows that one tensor copy brings; 0: copies of 16 bytes
   float scale_log2;                   // scale log2 e
-  float cap_log2, cap_turn;           // cap log2 e and 2 scale log2 e / cap; 0: no cap
-  float cap_small;                    // scores up to here take the polynomial, ...
-  float cap_poly[5];                  // in the score's square, times the score
+  float cap_log2, cap_unit;           // cap log2 e and scale / cap; 0: no cap
+  float cap_small;                    // products up to here take the polynomial, ...
+  float cap_poly[5];                  // in the square of the product over the cap, times that
 };
 
 // One request's place: its packed rows, its slots, the prefix that all its tokens see.
@@ -351,17 +351,19 @@ __device__ __forceinline__ uint64_t twice(float x) { return pair_of(__float_as_u
 
 // cap tanh z, z = scale x / cap, in units of log 2: for |z| <= 0.6 z times a polynomial in z^2
 // (fitted to tanh(z) / z by least squares, reweighted until its largest error, 2^-23.7 of the
-// value, is about even), else cap (1 - 2 / (1 + e^2z)), within 2^-20 of the value there.
+// value, is about even), else cap (1 - 2 / (1 + e^2z)), within 2^-20 of the value there.  (z itself
+// costs a product.  Coefficients for powers of x would save it, but are no 32-bit numbers for large
+// caps, and for those the other form is good for nothing: 1 - 2 / (1 + e^2z) is 0 where z is below 2^-24.)
 __device__ __forceinline__ float capped(const Params& P, float x) {
-  const float u = x * x;
-  const float near = x * fmaf(u, fmaf(u, fmaf(u, fmaf(u, P.cap_poly[4], P.cap_poly[3]), P.cap_poly[2]),
+  const float z = x * P.cap_unit, u = z * z;
+  const float near = z * fmaf(u, fmaf(u, fmaf(u, fmaf(u, P.cap_poly[4], P.cap_poly[3]), P.cap_poly[2]),
                                       P.cap_poly[1]), P.cap_poly[0]);
-  const float far = fmaf(rcp_of(exp2_of(x * P.cap_turn) + 1.0f), -2.0f * P.cap_log2, P.cap_log2);
+  const float far = fmaf(rcp_of(exp2_of(z * 2.8853900817779268f) + 1.0f), -2.0f * P.cap_log2, P.cap_log2);
   return fabsf(x) <= P.cap_small ? near : far;
 }
 
 // Half a tile's products become capped scores.  Those of a warp's rows rarely leave the
-// polynomial, which is six instructions for two of them; where they do, both forms are taken.
+// polynomial, which is seven instructions for two of them; where they do, both forms are taken.
 __device__ __forceinline__ void cap_scores(const Params& P, uint32_t (&x)[kHalf]) {
   float most[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -371,10 +373,11 @@ __device__ __forceinline__ void cap_scores(const Params& P, uint32_t (&x)[kHalf]
   if (__all_sync(kFullMask, all <= P.cap_small)) {
     const uint64_t k[5] = {twice(P.cap_poly[0]), twice(P.cap_poly[1]), twice(P.cap_poly[2]),
                            twice(P.cap_poly[3]), twice(P.cap_poly[4])};
+    const uint64_t unit = twice(P.cap_unit);
 #pragma unroll
     for (int e = 0; e < kHalf; e += 2) {
-      const uint64_t v = pair_of(x[e], x[e + 1]), u = mul2(v, v);
-      const float2 y = halves_of(mul2(v, fma2(u, fma2(u, fma2(u, fma2(u, k[4], k[3]), k[2]), k[1]), k[0])));
+      const uint64_t z = mul2(pair_of(x[e], x[e + 1]), unit), u = mul2(z, z);
+      const float2 y = halves_of(mul2(z, fma2(u, fma2(u, fma2(u, fma2(u, k[4], k[3]), k[2]), k[1]), k[0])));
       x[e] = __float_as_uint(y.x);
       x[e + 1] = __float_as_uint(y.y);
     }

@@ -243,6 +243,28 @@ def test_attention_caps(sv, cap, longest):  # noqa: F811
     assert rel < 1.5 * 2.0 ** -10, rel
 
 
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("longest", [1, 70])
+@pytest.mark.parametrize("cap", [1e-29, 1e9, 1e15, 1e21, 1e25, 1e29])
+def test_attention_caps_of_any_size(sv, cap, longest, slopes):  # noqa: F811
+    """A cap far above all scores leaves them as they are: cap tanh(y / cap) is y (1 - (y / cap)^2 / 3).  For
+    these y below 300 it is less than 2^-40 of it, and the kernels' form of it is off by the
+    polynomial's 2^-23.7 and four roundings, together below 2^-21 of y: the tolerance of an
+    attention without caps has it among the 2^-19 that it gives to a score beside its D sums.  A cap far
+    below them makes all weights alike."""
+    a = Attn(101, [1, 1] if longest == 1 else [70, 1], [300, 901], 4, 2, 64, 32, F16, sharp=3.0, slopes=slopes)
+    if cap < 1.0:
+        a.cap = cap
+    want, tol = a.want()
+    a.cap = cap
+    got, status = sv.chunk_attention(*a.args(), longest=longest, **a.kw())
+    assert status.tolist() == [0, 0]
+    close(got, want, tol)
+    rel = ((got.double() - want).norm() / want.norm()).item()
+    # the output's and the weights' roundings to f16, 2^-11 of a value each, with half as much again
+    assert rel < 1.5 * 2.0 ** -10, rel
+
+
 def test_attention_rising_maxima(sv):  # noqa: F811
     """Every tile has larger scores than the one before, so every one scales the sums again."""
     a = Attn(17, [150], [1000], 2, 2, 64, 32, BF16, scale=1.0)
