@@ -611,7 +611,7 @@ size_t specv_beam_workspace_bytes(int B, int W, int K, int V);
  *   ended     [B, W] int32 or NULL: a beam whose text has ended (not 0) is one
  *             candidate, with the score and end_token as it is; its row is not read.
  *   out_scores [B, K] float32, tokens, beams [B, K] int32: behind the last
- *             candidate above -inf: -inf, -1, -1.
+ *             candidate whose score, rounded to 32 bits, is above -inf: -inf, -1, -1.
  *   status    [B]: SPECV_DEV_BAD_ROW (a row has a NaN or +inf), or
  *             SPECV_DEV_BAD_BEAM (a score is one); such a request has no candidates.
  *             A row of -inf alone has none either, and is no error.

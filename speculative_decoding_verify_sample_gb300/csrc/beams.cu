@@ -527,9 +527,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
     __syncthreads();
   }
   auto put = [&](int k, const Candidate& c) {
-    const bool real = c.score > kNothing;
+    // (a score below the lowest 32-bit number is out of play behind this call, as one of -inf)
+    const float score = c.score > kNothing ? static_cast<float>(score_of(c.score)) : -INFINITY;
+    const bool real = score > -INFINITY;
     const int w = static_cast<int>(c.place >> kVocabBits);
-    P.out_scores[b * K + k] = real ? static_cast<float>(score_of(c.score)) : -INFINITY;
+    P.out_scores[b * K + k] = score;
     P.beams[b * K + k] = real ? w : -1;
     P.tokens[b * K + k] = !real ? -1 : s_kind[w] == 2 ? P.end_token
                                                       : static_cast<int>(c.place & ((1u << kVocabBits) - 1));

@@ -84,6 +84,21 @@ def test_select_few_allowed(sv, dtype):  # noqa: F811
     check(sv, z, [[-1.0, -2.5], [-0.5, -np.inf], [-700.0, -0.125]], 40)
 
 
+def test_select_scores_below_the_lowest(sv):  # noqa: F811
+    """A score that rounds to -inf is no candidate: no place has -inf and a token."""
+    low = torch.finfo(F32).min
+    z = torch.full((2, 2, 5), low, device="cuda")
+    z[:, :, 3] = 1.0
+    out, tokens, beams, status = sv.select_beams(z, f32([[low, -1.0], [low, low]]), 10)
+    assert status.tolist() == [0, 0]
+    # request 0: beam 1's token 3; beam 0's and beam 1's masked ones, alike in 64 bits; beam 0's masked
+    # ones are 2 low
+    assert tokens[0].tolist() == [3, 3, 0, 1, 2, 4, -1, -1, -1, -1]
+    assert beams[0].tolist() == [1, 0, 1, 1, 1, 1, -1, -1, -1, -1]
+    assert out[0].tolist() == [-1.0] + [low] * 5 + [float("-inf")] * 4
+    assert tokens[1].tolist() == [3, 3] + [-1] * 8 and beams[1].tolist() == [0, 1] + [-1] * 8
+
+
 def test_select_ties_go_to_the_lowest(sv):  # noqa: F811
     """Equal scores: the lower beam, then the lower token, however many there are."""
     for V in (50, 8192, 40003):
