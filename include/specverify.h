@@ -602,7 +602,8 @@ size_t specv_beam_workspace_bytes(int B, int W, int K, int V);
 /*
  * The best next tokens of a request's W beams: of all (w, v)
  *   score(w, v) = scores[b,w] + logits[b,w,v] - log sum_u exp logits[b,w,u]
- * the K largest, falling, ties to the lower beam and then the lower token.  The
+ * the K largest, falling, ties to the lower beam and then the lower token (within a beam
+ * logits are compared: they tie where scores do, however large scores[b,w] is).  The
  * nodes of a drafted tree's next level (the beams are the last level's, scores
  * their summed log probabilities), or a beam search's step.
  *   logits    [B, W, V] of `dtype` (SPECV_F32 or SPECV_BF16), element (b, w, v)

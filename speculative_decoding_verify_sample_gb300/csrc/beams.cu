@@ -376,11 +376,26 @@ __global__ void __launch_bounds__(kThreads, 3) select_rows_kernel(const Params P
   }
 }
 
-// A candidate: its score as a whole number of the same order, and beam and token as one number.
+// A candidate: its score as a whole number of the same order, and what decides between equal ones,
+// the larger first: the lower beam, the larger logit (of one beam's entries the score falls
+// with it, also where a sum far from 0, a score of -1e30, leaves no difference in 64 bits, and a
+// part's list is in that order), the lower token.
 struct Candidate {
   uint64_t score;  // kNothing: none
-  uint32_t place;
+  uint64_t tie;
 };
+constexpr uint32_t kLastEntry = (1u << kVocabBits) - 1;
+static_assert((kMaxBeams & (kMaxBeams - 1)) == 0 && kMaxBeams <= 1 << (32 - kVocabBits), "bits of a tie");
+__device__ __forceinline__ uint64_t tie_of(int w, uint32_t logit, int token) {
+  return static_cast<uint64_t>(kMaxBeams - 1 - w) << (32 + kVocabBits) |
+         static_cast<uint64_t>(logit) << kVocabBits | (kLastEntry - static_cast<uint32_t>(token));
+}
+__device__ __forceinline__ int beam_of(uint64_t tie) {
+  return kMaxBeams - 1 - static_cast<int>(tie >> (32 + kVocabBits));
+}
+__device__ __forceinline__ int token_of(uint64_t tie) {
+  return static_cast<int>(kLastEntry - (static_cast<uint32_t>(tie) & kLastEntry));
+}
 constexpr uint64_t kNothing = 0x000fffffffffffffull;  // of -inf
 __device__ __forceinline__ uint64_t ordered(double x) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));  // (-0 is 0)
@@ -390,7 +405,7 @@ __device__ __forceinline__ double score_of(uint64_t u) {
   return __longlong_as_double(static_cast<long long>(u >> 63 ? u & ~(1ull << 63) : ~u));
 }
 __device__ __forceinline__ bool better(const Candidate& a, const Candidate& b) {
-  return a.score > b.score || (a.score == b.score && a.place < b.place);
+  return a.score > b.score || (a.score == b.score && a.tie > b.tie);
 }
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
@@ -400,8 +415,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   __shared__ float s_max[kMaxBeams];   // and what that sum's exponentials were taken from
   __shared__ uint8_t s_kind[kMaxBeams];  // 0: no candidate, 1: a row, 2: ended
   __shared__ Candidate s_found[kFound];
-  extern __shared__ __align__(16) uint64_t s_score[];  // [kept], and behind them their places
-  uint32_t* const s_place = reinterpret_cast<uint32_t*>(s_score + P.kept);
+  extern __shared__ __align__(16) uint64_t s_score[];  // [kept], and behind them what decides ties
+  uint64_t* const s_tie = s_score + P.kept;
   __shared__ uint64_t s_top[kMaxBeams];
   __shared__ Candidate s_warp[kWarps];
   __shared__ int s_count, s_bad;
@@ -448,7 +463,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   const int lists = W * P.splits, all = bad ? 0 : lists * K;
   // Entry number e; worse than any where there is none.  The lists' first entries come first, those
   // of all rows beside one another, so that every group of threads below has good ones.
-  const Candidate none{kNothing, 0xffffffffu};
+  const Candidate none{kNothing, 0};
   auto entry = [&](int e) {
     const int k = e / lists, list = e - k * lists, split = list / W, w = list - split * W, kind = s_kind[w];
     Candidate c = none;
@@ -456,11 +471,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
       const uint64_t key = P.keys[((b * W + w) * P.splits + split) * K + k];
       if (key) {
         c.score = ordered(s_off[w] + (static_cast<double>(value_of(key)) - static_cast<double>(s_max[w])));
-        c.place = static_cast<uint32_t>(w) << kVocabBits | static_cast<uint32_t>(place_of(key));
+        c.tie = tie_of(w, static_cast<uint32_t>(key >> 32), place_of(key));
       }
     } else if (kind == 2 && !k && !split) {
       c.score = ordered(s_off[w]);
-      c.place = static_cast<uint32_t>(w) << kVocabBits;
+      c.tie = tie_of(w, 0, 0);
     }
     return c;
   };
@@ -471,12 +486,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
     const Candidate c = entry(e);
     if (e < P.kept) {
       s_score[e] = c.score;
-      s_place[e] = c.place;
+      s_tie[e] = c.tie;
     }
     mine = larger(mine, c.score);
   }
   // (a thread's own, no other's)
-  auto again = [&](int e) { return e < P.kept ? Candidate{s_score[e], s_place[e]} : entry(e); };
+  auto again = [&](int e) { return e < P.kept ? Candidate{s_score[e], s_tie[e]} : entry(e); };
   const int groups = K <= 8 ? 8 : K <= 16 ? 16 : K <= 32 ? 32 : 64, width = kThreads / groups;
   for (int o = width / 2; o > 0; o /= 2) mine = larger(mine, __shfl_xor_sync(kFullMask, mine, o));
   if (tid % width == 0) s_top[tid / width] = mine;
@@ -530,11 +545,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
     // (a score below the lowest 32-bit number is out of play behind this call, as one of -inf)
     const float score = c.score > kNothing ? static_cast<float>(score_of(c.score)) : -INFINITY;
     const bool real = score > -INFINITY;
-    const int w = static_cast<int>(c.place >> kVocabBits);
+    const int w = real ? beam_of(c.tie) : 0;
     P.out_scores[b * K + k] = score;
     P.beams[b * K + k] = real ? w : -1;
-    P.tokens[b * K + k] = !real ? -1 : s_kind[w] == 2 ? P.end_token
-                                                      : static_cast<int>(c.place & ((1u << kVocabBits) - 1));
+    P.tokens[b * K + k] = !real ? -1 : s_kind[w] == 2 ? P.end_token : token_of(c.tie);
   };
   if (found <= kFound) {
     for (int i = tid; i < found; i += kThreads) {
@@ -555,7 +569,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
       }
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) {
-        const Candidate d{__shfl_xor_sync(kFullMask, c.score, o), __shfl_xor_sync(kFullMask, c.place, o)};
+        const Candidate d{__shfl_xor_sync(kFullMask, c.score, o), __shfl_xor_sync(kFullMask, c.tie, o)};
         if (better(d, c)) c = d;
       }
       if (lane == 0) s_warp[warp] = c;
@@ -720,10 +734,10 @@ specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(B);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kept * (sizeof(uint64_t) + sizeof(uint32_t));
+  cfg.dynamicSmemBytes = kept * sizeof(Candidate);
   if (cfg.dynamicSmemBytes > 16384 &&
       cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kKept * (sizeof(uint64_t) + sizeof(uint32_t)))) != cudaSuccess) {
+                           static_cast<int>(kKept * sizeof(Candidate))) != cudaSuccess) {
     cudaGetLastError();
     return SPECV_ERR_CUDA;
   }

@@ -99,6 +99,35 @@ def test_select_scores_below_the_lowest(sv):  # noqa: F811
     assert tokens[1].tolist() == [3, 3] + [-1] * 8 and beams[1].tolist() == [0, 1] + [-1] * 8
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("far", [-1e9, -1e30, -3.4028234663852886e38, 1e30])
+def test_select_far_scores_keep_the_order_of_logits(sv, dtype, far):  # noqa: F811
+    """Beams put out of the others' way by a large score: a beam's own tokens are still in the order of
+    its logits, and its ties in that of the tokens."""
+    for V, K, B in ((40, 32, 2), (9000, 64, 300)):  # (with few candidates, and one after the other)
+        z = normal(37, B, 2, V, dtype=dtype)
+        out, tokens, beams, status = sv.select_beams(z, f32([[far, -float("inf")], [-float("inf"), far]] * (B // 2)), K)
+        assert (status == 0).all()
+        for b in (0, 1, B - 1):
+            row = z[b, b % 2].float().cpu().numpy()
+            assert tokens[b].tolist() == np.lexsort((np.arange(V), -row))[:K].tolist()
+            assert (beams[b] == b % 2).all()
+    z = torch.zeros(1, 64, 64, device="cuda", dtype=dtype)  # more alike than are sorted at once
+    z[:, :, 1::2] = torch.arange(32, device="cuda", dtype=dtype)
+    tokens, beams = sv.select_beams(z, f32([[far] * 64]), 64)[1:3]
+    want = list(range(63, 0, -2)) + list(range(0, 64, 2))
+    if far != -1e9:  # (there the sums of 64 rows tell the logits apart)
+        assert beams[0].tolist() == [0] * 64 and sorted(tokens[0].tolist()) == list(range(64))
+        order = tokens[0].tolist()
+        assert order == [t for t in want if t != 1 and t % 2] + sorted(t for t in want if t == 1 or t % 2 == 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_select_more_candidates_than_are_kept(sv, dtype):  # noqa: F811
+    """64 beams' lists of 64 in three parts or more: what a block's shared memory does not hold is read again."""
+    check(sv, normal(41, 1, 64, 20000, dtype=dtype), totals(41, 1, 64), 64)
+
+
 def test_select_ties_go_to_the_lowest(sv):  # noqa: F811
     """Equal scores: the lower beam, then the lower token, however many there are."""
     for V in (50, 8192, 40003):
