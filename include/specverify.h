@@ -647,7 +647,8 @@ typedef struct specv_state {
  *             states stay as they were).
  *   states    1..SPECV_MAX_STATES of them, on the host.  out may be in itself, with
  *             its strides (then every old state is read before it is overwritten);
- *             otherwise no out may overlap an in or another out.
+ *             otherwise no out may overlap an in or another out (refused where both have
+ *             the same strides or begin together).
  * One kernel; no workspace.
  */
 specv_status spec_reorder_beams(const int32_t* beams, int B, int W, int K, const specv_state* states,

@@ -52,7 +52,8 @@ def reorder_beams(beams, states, *, out=None, status=None, stream=None):
     rows of a page table), each beam's part contiguous: all in one call.
     ``out``: as many tensors [B, K, ...]; None: the states themselves, with K =
     W.  Returns (out, status [B] int32: 0 or DEV_* bits), out a tensor or a tuple
-    as the states are; a flagged request's states stay as they were.
+    as the states are; a flagged request's states stay as they were.  No state may be
+    given twice, nor lie on memory that another is moved to.
     Asynchronous."""
     one = hasattr(states, "is_cuda")
     given = (states,) if one else tuple(states)

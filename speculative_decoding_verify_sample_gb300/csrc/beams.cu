@@ -674,6 +674,40 @@ __global__ void __launch_bounds__(kMoveThreads) reorder_kernel(const __grid_cons
   else move_column<uint8_t, kMost>(s, b, at, s_beams, P.K);
 }
 
+// Where a state's beams lie: `bytes` bytes at + b batch + w beam, for b < B and w < beams.
+struct Places {
+  __int128 at, end, batch, beam, bytes;
+  int B, beams;
+
+  Places(const void* p, int64_t batch_stride, int64_t beam_stride, int64_t bytes, int B, int beams)
+      : at(reinterpret_cast<uintptr_t>(p)), batch(B > 1 ? batch_stride : 0), beam(beam_stride), bytes(bytes), B(B),
+        beams(beams) {
+    end = at + (B - 1) * batch + (beams - 1) * beam + bytes;
+  }
+};
+
+// Whether two states' places have a byte in common.  Exact for strides that are alike, as those of views
+// of one tensor are; others are only known to if they begin together.
+bool overlap(const Places& x, const Places& y) {
+  if (x.at == y.at) return true;
+  if (x.end <= y.at || y.end <= x.at) return false;
+  const __int128 beam = x.beams > 1 ? x.beam : y.beam, most = x.B - 1;
+  if ((y.beams > 1 && y.beam != beam) || x.batch != y.batch) return false;
+  for (int w = 1 - x.beams; w < y.beams; w++) {  // y's beam less x's
+    // y's place less x's is `off` and b batches more: the first that is not wholly below
+    const __int128 off = y.at - x.at + w * beam;
+    __int128 b = -most;
+    if (x.batch > 0) {
+      const __int128 past = -y.bytes - off;  // b batch is above it
+      const __int128 first = past / x.batch - (past % x.batch < 0) + 1;
+      if (b < first) b = first;
+    }
+    const __int128 from = off + b * x.batch;
+    if (b <= most && from > -y.bytes && from < x.bytes) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -783,6 +817,18 @@ specv_status spec_reorder_beams(const int32_t* beams, int B, int W, int K, const
                        unit, static_cast<int>(tiles)};
     tiles += (x.bytes / unit + kMoveThreads - 1) / kMoveThreads;
     if (tiles > INT_MAX) return SPECV_ERR_UNSUPPORTED;
+  }
+  // What one state's blocks write must not be what another's, or they themselves, still have to read.
+  for (int i = 0; i < num_states; i++) {
+    const specv_state& x = states[i];
+    const Places to(x.out, x.out_batch_stride, x.out_beam_stride, x.bytes, B, K);
+    for (int j = 0; j < num_states; j++) {
+      const specv_state& y = states[j];
+      if ((j < i && overlap(to, Places(y.out, y.out_batch_stride, y.out_beam_stride, y.bytes, B, K))) ||
+          ((j != i || x.in != x.out) &&
+           overlap(to, Places(y.in, y.in_batch_stride, y.in_beam_stride, y.bytes, B, W))))
+        return SPECV_ERR_INVALID_ARG;
+    }
   }
   // requests along two axes of the grid, of at most 65,535 blocks each
   const dim3 grid(static_cast<unsigned>(tiles), B < 32768 ? B : 32768, (B + 32767) / 32768);

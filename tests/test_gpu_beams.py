@@ -336,6 +336,35 @@ def test_reorder_refusals(sv):  # noqa: F811
         sv.reorder_beams(beams, [x] * 33, out=[torch.zeros_like(x) for _ in range(33)])
 
 
+def test_reorder_states_of_one_tensor(sv):  # noqa: F811
+    """Views that lie between one another's beams are moved beside one another; places that two would write, or one
+    write and the other read, are refused, as blocks of a call run in any order."""
+    beams = i32([[2, 0, 1], [1, 1, 2]])
+    whole = normal(7, 2, 3, 4, 16)
+    want = moved(beams, whole, whole)
+    views = [whole[:, :, i] for i in range(4)]
+    sv.reorder_beams(beams, views)
+    assert torch.equal(whole, want)
+    wide = normal(8, 2, 6, 16)
+    want = moved(beams, wide[:, :3], wide[:, 3:])
+    sv.reorder_beams(beams, wide[:, :3], out=wide[:, 3:])
+    assert torch.equal(wide[:, 3:], want)
+    turned = normal(9, 3, 2, 16).transpose(0, 1)  # a beam's requests beside one another
+    want = moved(beams, turned, turned)
+    sv.reorder_beams(beams, turned)
+    assert torch.equal(turned, want)
+    x, y = normal(10, 2, 3, 16), normal(11, 2, 3, 16)
+    was = x.clone(), y.clone(), wide.clone(), whole.clone()
+    for states, out in [((x, x), None), ((x, x[:, :, :8]), None), ((x, y), (y, x)), ((x, y), (torch.zeros_like(x), x)),
+                        ((x, y), (y, torch.zeros_like(x))), ((whole[:, :, 0:2], whole[:, :, 1:3]), None),
+                        ((wide[:, :3],), (wide[:, 2:5],)), ((wide[:, :3],), (wide[:, 1:4],)),
+                        ((wide[:, 3:],), (wide[:, 1:4],)), ((x[:, :, 4:8], x[:, :, 7:11]), None)]:
+        with pytest.raises(sv.SpecVerifyError):
+            sv.reorder_beams(beams, states, out=out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(was, (x, y, wide, whole)))
+
+
 # --------------------------------------------------------- a tree, level by level
 
 

@@ -10,6 +10,7 @@ torch = pytest.importorskip("torch")
 
 import prompt_reference as ref  # noqa: E402
 import speculative_decoding_verify_sample_gb300 as sv  # noqa: E402
+from test_chunk_items_cpu import run as run_on_host  # noqa: E402
 from test_tree_cpu import BAD_CACHES, FAKE, INVALID, UNSUPPORTED, cache  # noqa: E402
 
 
@@ -113,6 +114,61 @@ def test_select_refusals(L, over, status):
 ])
 def test_reorder_refusals(L, over, status):
     assert reorder(L, **over) == status
+
+
+def test_reorder_refuses_states_on_one_another(L):
+    """Written twice, or read and written by different states, or moved onto part of itself."""
+    a = dict(ib=48, iw=10, ob=48, ow=10, n=8)
+    for off in (-8, 0, 4, 8, 14, 54, 60):  # (the beams' gaps have 2 bytes)
+        for two in (state(o=8 * FAKE, **a) + state(2 * FAKE, 8 * FAKE + off, **a),
+                    state(o=8 * FAKE, **a) + state(2 * FAKE, FAKE + off, **a)):
+            assert reorder(L, states=two, num=2) == INVALID, off
+        if off:
+            assert reorder(L, states=state(o=FAKE + off, **a)) == INVALID, off
+    for other in (dict(a, ow=20), dict(a, ob=96)):  # other strides: where both begin together
+        assert reorder(L, states=state(o=8 * FAKE, **a) + state(2 * FAKE, 8 * FAKE, **other), num=2) == INVALID
+
+
+PLACES = r"""
+#include <cstdio>
+#include <set>
+#include "beams.cu"
+
+int specv_max_vocab(specv_dtype) { return 0; }  // (of another file; not called)
+
+int main() {
+  int met = 0, apart = 0;
+  for (int B : {1, 2, 3})
+    for (int W : {1, 3})
+      for (int K : {1, 2, 3})
+        for (int batch : {0, 7, 16, 40})
+          for (int beam : {0, 3, 7, 40})
+            for (int n : {1, 3, 5})
+              for (int off = -130; off <= 130; off++) {
+                const auto place = [](int at) { return reinterpret_cast<const void*>(static_cast<uintptr_t>(at)); };
+                const Places x(place(1000), batch, beam, n, B, W), y(place(1000 + off), batch, beam, n + 1, B, K);
+                std::set<int> bytes;
+                bool want = false;
+                for (int b = 0; b < B; b++)
+                  for (int w = 0; w < W; w++)
+                    for (int e = 0; e < n; e++) bytes.insert(1000 + b * batch + w * beam + e);
+                for (int b = 0; b < B; b++)
+                  for (int k = 0; k < K; k++)
+                    for (int e = 0; e <= n; e++) want |= bytes.count(1000 + off + b * batch + k * beam + e) > 0;
+                if (overlap(x, y) != want || overlap(y, x) != want) {
+                  std::printf("B %d W %d K %d batch %d beam %d n %d off %d: not %d\n", B, W, K, batch, beam, n, off, want);
+                  return 1;
+                }
+                (want ? met : apart)++;
+              }
+  std::printf("%d\n", met < apart ? met : apart);
+}
+"""
+
+
+def test_reorder_knows_which_places_meet(tmp_path):
+    """Against all bytes of both, for strides that are alike."""
+    assert int(run_on_host(PLACES, tmp_path)) > 10000
 
 
 def test_workspace_sizes(L):
