@@ -596,7 +596,8 @@ specv_status spec_chunk_attention(const specv_cache* cache, const specv_rows* q,
                                   const float* slopes, const specv_rows* out, int32_t* status,
                                   void* workspace, size_t workspace_bytes, specv_stream_t stream);
 
-/* Bytes of workspace spec_select_beams needs (0 for sizes out of range). */
+/* Bytes of workspace spec_select_beams needs for sizes up to these, of both dtypes
+ * (0 for sizes out of range). */
 size_t specv_beam_workspace_bytes(int B, int W, int K, int V);
 
 /*
@@ -617,8 +618,8 @@ size_t specv_beam_workspace_bytes(int B, int W, int K, int V);
  *             SPECV_DEV_BAD_BEAM (a score is one); such a request has no candidates.
  *             A row of -inf alone has none either, and is no error.
  *   W, K      1..SPECV_MAX_BEAMS.
- *   workspace specv_beam_workspace_bytes bytes, 256-byte aligned, whatever it
- *             holds.  Calls that may run at the same time need one each.
+ *   workspace specv_beam_workspace_bytes bytes for these sizes or larger ones,
+ *             256-byte aligned, whatever it holds.  Calls that may run at the same time need one each.
  * The rows' sums are held in 64 bits (of exponentials in 32), scores are compared
  * in 64 bits and rounded once.  Two kernels, the second as a programmatic dependent
  * launch.

@@ -14,8 +14,8 @@ from ._native import lib
 
 
 class BeamWorkspace:
-    """Device workspace for select_beams of K among W beams of a V-entry
-    vocabulary, for B requests.  Calls that may run at the same time need one each."""
+    """Device workspace for select_beams of up to K among up to W beams of vocabularies of
+    up to V entries, for up to B requests.  Calls that may run at the same time need one each."""
 
     def __init__(self, B: int, W: int, K: int, V: int, device=None):
         import torch

@@ -603,6 +603,15 @@ struct Plan {
     keys = align256(rows * splits * sizeof(Part));
     total = keys + align256(rows * splits * K * sizeof(uint64_t));
   }
+
+  // Enough for every call of up to B, W, K and V: fewer rows have more parts each, at most kMaxSplits
+  // and at most this many in all, for parts < wanted / rows + 1.
+  static size_t most(int B, int W, int K, int V, int step) {
+    const int64_t rows = static_cast<int64_t>(B) * W, all = (V + step * kWarps - 1) / (step * kWarps);
+    const int64_t each = rows * (all < kMaxSplits ? all : kMaxSplits), dealt = rows + kBlocks * kSms - 1;
+    const int64_t parts = each < dealt ? each : dealt;
+    return align256(parts * sizeof(Part)) + align256(parts * K * sizeof(uint64_t));
+  }
 };
 template <int DT> constexpr int kStepOf = 32 * kVecs * Elt<DT>::kVec;
 
@@ -714,9 +723,7 @@ extern "C" {
 
 size_t specv_beam_workspace_bytes(int B, int W, int K, int V) {
   if (check_beams(B, W, K) != SPECV_OK || V < 1 || V > 1 << kVocabBits) return 0;
-  // (a 32-bit row has as many steps as a 16-bit row of twice its entries, or more)
-  const size_t half = Plan(B, W, K, V, kStepOf<SPECV_BF16>).total, full = Plan(B, W, K, V, kStepOf<SPECV_F32>).total;
-  return half > full ? half : full;
+  return Plan::most(B, W, K, V, kStepOf<SPECV_F32>);  // (a 16-bit row has no more steps)
 }
 
 specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t row_stride,

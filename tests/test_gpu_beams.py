@@ -209,6 +209,14 @@ def test_select_the_same_every_time_and_in_graphs(sv):  # noqa: F811
         assert all(torch.equal(a, b) for a, b in zip(want, outs))
 
 
+def test_select_a_workspace_for_the_largest_batch(sv):  # noqa: F811
+    ws = sv.BeamWorkspace(64, 8, 8, 32003, device="cuda")
+    for B, W, K, V in ((64, 8, 8, 32003), (56, 8, 8, 32003), (40, 8, 8, 30000), (13, 8, 8, 32003), (1, 8, 8, 32003),
+                       (11, 3, 8, 20000), (33, 8, 1, 16385)):
+        for dtype in (BF16, F32):
+            check(sv, normal(B, B, W, V, dtype=dtype), totals(B, B, W), K, workspace=ws)
+
+
 def test_select_offsets_past_32_bits(sv):  # noqa: F811
     z = normal(23, 3, 2, 1000, dtype=BF16)
     far = torch.empty(2 ** 32 + 2000, dtype=BF16, device="cuda").as_strided((3, 2, 1000), (2 ** 31, 1000, 1))

@@ -190,6 +190,51 @@ def test_workspace_sizes(L):
         sv.BeamWorkspace(1, 65, 1, 10)
 
 
+def test_a_beam_workspace_serves_smaller_calls(L):
+    """What is enough for a call is enough for one of fewer requests, beams, places or entries."""
+    need = L.specv_beam_workspace_bytes
+    for W, K, V in ((8, 8, 128256), (1, 1, 9), (5, 3, 32003), (64, 64, 50000), (2, 17, 1 << 20)):
+        sizes = [need(B, W, K, V) for B in (*range(1, 600), 4000, 65535)]
+        assert sizes[0] > 0 and sizes == sorted(sizes), (W, K, V)
+    for B in (1, 3, 40, 64, 700):
+        sizes = [need(B, W, 8, 128256) for W in range(1, 65)]
+        assert sizes == sorted(sizes), B
+        sizes = [need(B, 8, K, 128256) for K in range(1, 65)]
+        assert sizes == sorted(sizes), B
+        sizes = [need(B, 8, 8, V) for V in (*range(1, 140000, 511), 131072, 131073, 1 << 20)]
+        assert sizes[:-3] == sorted(sizes[:-3]) and sizes[-3] <= sizes[-2] <= sizes[-1], B
+
+
+PLANS = r"""
+#include <cstdio>
+#include "beams.cu"
+
+int specv_max_vocab(specv_dtype) { return 0; }  // (of another file; not called)
+
+int main() {
+  int calls = 0;
+  for (int B = 1; B <= 600; B += B < 100 ? 1 : 7)
+    for (int W : {1, 2, 5, 8, 31, 64})
+      for (int K : {1, 8, 64})
+        for (int V : {1, 4095, 4096, 4097, 8193, 32003, 50000, 128256, 131072, 131073, 524288, 1 << 20}) {
+          const size_t most = specv_beam_workspace_bytes(B, W, K, V);
+          const size_t half = Plan(B, W, K, V, kStepOf<SPECV_BF16>).total;
+          const size_t full = Plan(B, W, K, V, kStepOf<SPECV_F32>).total;
+          if (half > most || full > most) {
+            std::printf("B %d W %d K %d V %d: %zu, needed %zu and %zu\n", B, W, K, V, most, half, full);
+            return 1;
+          }
+          calls++;
+        }
+  std::printf("%d\n", calls);
+}
+"""
+
+
+def test_a_beam_workspace_is_large_enough(tmp_path):
+    assert int(run_on_host(PLANS, tmp_path)) > 10000
+
+
 def i32(*shape):
     return torch.zeros(*shape, dtype=torch.int32)
 
