@@ -620,8 +620,9 @@ size_t specv_beam_workspace_bytes(int B, int W, int K, int V);
  *   W, K      1..SPECV_MAX_BEAMS.
  *   workspace specv_beam_workspace_bytes bytes for these sizes or larger ones,
  *             256-byte aligned, whatever it holds.  Calls that may run at the same time need one each.
- * The rows' sums are held in 64 bits (of exponentials in 32), scores are compared
- * in 64 bits and rounded once.  Two kernels, the second as a programmatic dependent
+ * A row's sum of exponentials (each within 2^-22, those of 16 entries of float32 or 32 of
+ * bf16 added in 32 bits) is held in 64 bits or a pair of 32, scores are compared in 64 bits
+ * and rounded once.  Two kernels, the second as a programmatic dependent
  * launch.
  */
 specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t row_stride,

@@ -217,6 +217,21 @@ def test_select_a_workspace_for_the_largest_batch(sv):  # noqa: F811
             check(sv, normal(B, B, W, V, dtype=dtype), totals(B, B, W), K, workspace=ws)
 
 
+@pytest.mark.parametrize("dtype,V,low,every", [(F32, 1 << 19, -1.1171624660491943, 4), (BF16, 1 << 20, -0.83984375, 8)])
+def test_select_long_rows_sums(sv, dtype, V, low, every):  # noqa: F811
+    """Rows of so many requests that a block has a whole one: a lane adds the same sum 128 times, of a size that
+    one 32-bit number would round the same way each time, 1.9e-6 of the sum in the end.  Of the
+    sum the exponentials are off by 2^-22 and the argument's rounding, 2^-24 of at most 1.7, and those of a
+    step by 10 roundings: 2^-20 of it, and as much of its logarithm."""
+    row = torch.full((V,), low, dtype=dtype, device="cuda")
+    row[::every] = 0.0
+    z = row.expand(8, 64, V)
+    out, tokens, beams, status = sv.select_beams(z, f32([[12.5] * 64] * 8), 1)
+    assert (status == 0).all() and (tokens == 0).all() and (beams == 0).all()
+    want = 12.5 - np.log(V // every * (1.0 + (every - 1) * np.exp(np.float64(low))))
+    assert abs(want) < 1.0 and np.abs(out.cpu().double().numpy() - want).max() <= 2.0 ** -20
+
+
 def test_select_offsets_past_32_bits(sv):  # noqa: F811
     z = normal(23, 3, 2, 1000, dtype=BF16)
     far = torch.empty(2 ** 32 + 2000, dtype=BF16, device="cuda").as_strided((3, 2, 1000), (2 ** 31, 1000, 1))
