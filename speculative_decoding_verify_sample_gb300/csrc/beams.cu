@@ -35,6 +35,12 @@ constexpr int kMaxBeams = SPECV_MAX_BEAMS;
 constexpr int kBuffer = 128;  // entries of a warp that may be among the best, until they are sorted in
 constexpr int kFound = 1024;  // and of a request
 constexpr int kKept = 8192;   // candidates that a request's block keeps in shared memory, at most
+// Shared memory of a request's block where there are no more of them than SMs: an SM has one.  With only what
+// it needs, how many an SM gets (and shares its 64-bit units, which are few) hangs on a few
+// hundred bytes: 32 requests of 16 beams, K = 16, 16 bits took 93 or 116 us for 3 or 4 KB more, and 89 so; 64 of 8,
+// 32 bits, a fifth of them ended, 66 and 59; 16 of 16, K = 32, 98 and 63.  More requests than SMs:
+// 200 of 2 beams 31 and 35, 1,000 of 4 151 and 176.
+constexpr int kAlone = 100 * 1024;
 constexpr int kVocabBits = 20;  // of a vocabulary entry's number
 constexpr int kMaxSplits = 32;  // parts of a row: a request's block reads what they leave
 constexpr int kBlocks = 3;     // of an SM, where rows are long enough
@@ -784,6 +790,7 @@ specv_status spec_select_beams(const void* logits, int64_t batch_stride, int64_t
   cfg.gridDim = dim3(B);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kept * sizeof(Candidate);
+  if (B <= kSms && cfg.dynamicSmemBytes < kAlone) cfg.dynamicSmemBytes = kAlone;
   if (cfg.dynamicSmemBytes > 16384 &&
       cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kKept * sizeof(Candidate))) != cudaSuccess) {
