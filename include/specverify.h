@@ -588,7 +588,8 @@ size_t specv_chunk_workspace_bytes(int longest, int q_heads, int kv_heads, int h
  *             it holds.  Calls that may run at the same time need one each.
  * A wait inside the kernel that lasts two seconds gives up: then every request
  * of the call has SPECV_DEV_TIMEOUT in its status, and the rows hold anything.
- * Two kernels, the second as a programmatic dependent launch.
+ * Two kernels, the second as a programmatic dependent launch; one where longest is 1
+ * and there is room for few slots.
  */
 specv_status spec_chunk_attention(const specv_cache* cache, const specv_rows* q,
                                   const int32_t* cu_tokens, int B, int T, int longest, int q_heads,

@@ -9,13 +9,14 @@
 // Each logit is read once, and only the few that may be among the best leave the
 // registers.
 //
-// Measured: 64 requests of 8 beams over 128,256 32-bit entries, a part of them ended, 64 to 66
-// us (210 MB, 3.2 TB/s); one request of 8 over 16-bit entries 19 to 20; a single row of 1,024
-// entries 12.4, two kernels' latencies.  In an earlier form of 98 us the batch took 59 without
-// the search for the best and 51 without the exponentials as well: the latter is what reading
-// costs with the 24 warps to an SM that the registers leave.  32 requests of 16 beams, K = 16, 16 bits:
-// 93 us; 8 of 64 over 50,000, K = 64: 223, nearly all of it the search.  The reordering of 64 requests of 8
-// beams, 46 MB read and written, 8.4 to 10.5 us, of one 4.
+// Measured: 64 requests of 8 beams over 128,256 32-bit entries, a fifth of them ended, 59 to 60
+// us (210 MB, 3.5 TB/s), none ended 85 (263 MB): more rows than blocks fit at a time, 456, so the
+// last 56 run by themselves (57 requests, 456 rows: 60).  Rows that do not begin at 16 bytes, as those of 128,257
+// entries, 142 and 170.  One request of 8 over 16-bit entries 19 to 20; a single row of 1,024
+// entries 12.4, two kernels' latencies.  32 requests of 16 beams, K = 16, 16 bits: 89;
+// 8 of 64 over 50,000, K = 64: 177, nearly all of it the search.  What bounds the rows is not separated: in
+// an earlier form of 98 us the batch took 59 without the search for the best and 51 without the
+// exponentials as well.  The reordering of 64 requests of 8 beams, 46 MB read and written, 10.5 us, of one 4.
 
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -36,8 +37,8 @@ constexpr int kBuffer = 128;  // entries of a warp that may be among the best, u
 constexpr int kFound = 1024;  // and of a request
 constexpr int kKept = 8192;   // candidates that a request's block keeps in shared memory, at most
 // Shared memory of a request's block where there are no more of them than SMs: an SM has one.  With only what
-// it needs, how many an SM gets (and shares its 64-bit units, which are few) hangs on a few
-// hundred bytes: 32 requests of 16 beams, K = 16, 16 bits took 93 or 116 us for 3 or 4 KB more, and 89 so; 64 of 8,
+// it needs, how many an SM gets hangs on a few hundred bytes (why more are slower was not looked
+// into): 32 requests of 16 beams, K = 16, 16 bits took 93 or 116 us for 3 or 4 KB more, and 89 so; 64 of 8,
 // 32 bits, a fifth of them ended, 66 and 59; 16 of 16, K = 32, 98 and 63.  More requests than SMs:
 // 200 of 2 beams 31 and 35, 1,000 of 4 151 and 176.
 constexpr int kAlone = 100 * 1024;

@@ -350,7 +350,8 @@ __device__ __forceinline__ int request_of(const ChunkParams& P, int t, int lane)
 //
 // Each row is read and written once: 16 requests of 513 to 4,093 tokens, three axes, 168 us
 // (906 MB, 5.4 TB/s, 0.80 of a plain copy); one of 517 tokens 10.3 us, launch and the chain to a
-// token's slot and angles.  With 24, 48, 72 and 144 warps to an SM in the grid the first took
+// token's slot and angles; a single token of each of 64, 256 and 1,024 requests 8.3, 10.4, 14.4.
+// With 24, 48, 72 and 144 warps to an SM in the grid the first took
 // 168, 181, 166 and 168.
 //
 // A warp has `each` tokens in a row (or every slices-th pass of them), and its copies

@@ -31,16 +31,17 @@
 // that clean values.
 //
 // Measured (D = 128 and 32 + 8 heads but where said), calls back to back:
-// 4,093 tokens behind 28,673 slots 1,430 to 1,443 us (1,430 TFLOP/s);
-// six prompts of 517 to 4,093 tokens 326 us (1,030 TFLOP/s).  With clocks read in the
+// 4,093 tokens behind 28,673 slots 1,423 to 1,452 us (1,430 TFLOP/s);
+// six prompts of 517 to 4,093 tokens 327 us (1,020 TFLOP/s).  With clocks read in the
 // kernel a softmax warp of this case has 22 halves to an item, each 150 cycles before its wait, 490
 // in it and 950 at work, and 8,000 cycles at an item's ends, 5,200 of them writing (without the
 // writes 315 us);
-// 48 requests of 1 to 257 tokens and a window, f16, 186 us;
-// 48 single tokens over 27,000 slots each 780 us (6.8 TB/s);
-// capped scores, 16 + 8 heads, 287 to 295 us for 202 GFLOP: the polynomial's
+// 48 requests of 1 to 257 tokens and a window, f16, 185 us;
+// single tokens: 48 over 27,000 slots each 780 us (6.8 TB/s), 64 over 4,001 174, 16 over 2,000 to 5,750 62, one
+// over 32,001 42, over 4,001 in a table of 16,384 20 (in one of 4,032 it is the small kernel's, 12.4);
+// capped scores, 16 + 8 heads, 297 us for 202 GFLOP: the polynomial's
 // products come on top of each score's exponential;
-// a bias by distance, 16 + 16 heads of 64, 137 to 154 us for 49 GFLOP (116 without the bias).
+// a bias by distance, 16 + 16 heads of 64, 138 to 140 us for 49 GFLOP (116 without the bias).
 // The second kernel takes 18 to 41 us where items are many (under a profiler): its 197 registers to a thread
 // leave an SM one block.
 #pragma once

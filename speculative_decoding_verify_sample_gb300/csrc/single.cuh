@@ -9,9 +9,9 @@
 // The warps' (m, l, O) are joined in their CTA, the CTAs' through the cluster's
 // shared memory: one kernel.
 //
-// For few bytes, where a call is latencies and the fetching of code: one request of 8 + 8 heads
+// For few bytes, where a call is latencies and the fetching of code: one request of 32 + 8 heads
 // of 128, a slot 10.4 us (tiles of 128 rows and a second kernel for the join: 14.7), 4,002 slots
-// 12.5 (20.9), 32,001 slots 67 (46); 16 requests of 2,000 to 6,000 slots 88 to 99 (67).
+// 12.4 (20), 32,002 slots 67 (42); 16 requests of 2,000 to 6,000 slots 88 to 99 (62).
 #pragma once
 
 #include "chunk.cuh"
